@@ -501,3 +501,8 @@ def tier_verify_step(tiers: Sequence[TieredLayer], x: torch.Tensor, out: torch.T
                                           _ptr(ws), ws.numel(), _ptr(union_mask), _ptr(stats), _stream()),
            "colibri_tier_verify_step")
     return out
+
+
+# The operators around the layer (block.py).
+from .block import (KVCache, NormResult, add_rms_norm, kv_append, kv_attention, kv_attention_workspace,  # noqa: E402
+                    kv_page_shape, kv_read, linear_q, linear_workspace)

@@ -21,7 +21,8 @@ PROBES_LIB = os.path.join(PKG, "libcolibri_probes.so")
 PROBES_SRC = "probes.hip"
 
 SOURCES = ["ffn_gemv.hip", "ffn_mfma.hip", "api.hip", "q8_router.hip", "dispatch.hip", "tier.hip",
-           "tier_kernels.hip", "expert_cache.cpp"]
+           "tier_kernels.hip", "expert_cache.cpp", "linear.hip", "kv_attention.hip", "norm.hip", "kv_cache.hip",
+           "block_api.hip"]
 
 ARCH = "gfx950"
 # -ffp-contract=off: every fused multiply-add in the kernels is an explicit

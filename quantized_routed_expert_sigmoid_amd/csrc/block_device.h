@@ -1,0 +1,111 @@
+/*
+ * block_device.h -- device helpers shared by the operators around the layer:
+ * typed loads and stores of activations, the cache's page layout, and the
+ * bounds of one sequence of a batch.
+ */
+#ifndef COLI_BLOCK_DEVICE_H
+#define COLI_BLOCK_DEVICE_H
+
+#include "block.h"
+#include "device_common.h"
+
+namespace coli {
+
+/* bf16 as its bits: the upper half of an fp32. */
+struct bf16 {
+    uint16_t u;
+};
+
+__device__ __forceinline__ float to_f32(float v)
+{
+    return v;
+}
+
+__device__ __forceinline__ float to_f32(bf16 v)
+{
+    return __uint_as_float((uint32_t)v.u << 16);
+}
+
+/* Two fp32 as bf16, each rounded to nearest even, in one word (lo in its
+ * lower half). */
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi)
+{
+    typedef __bf16 b2 __attribute__((ext_vector_type(2)));
+    b2 p = {(__bf16)lo, (__bf16)hi};
+    uint32_t u;
+    __builtin_memcpy(&u, &p, 4);
+    return u;
+}
+
+__device__ __forceinline__ void store1(float* p, float v)
+{
+    *p = v;
+}
+
+__device__ __forceinline__ void store1(bf16* p, float v)
+{
+    p->u = (uint16_t)pack_bf16(v, 0.0f);
+}
+
+__device__ __forceinline__ float4 load4(const float* p)
+{
+    return *reinterpret_cast<const float4*>(p);
+}
+
+__device__ __forceinline__ float4 load4(const bf16* p)
+{
+    const uint2 u = *reinterpret_cast<const uint2*>(p);
+    return make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xFFFF0000u), __uint_as_float(u.y << 16),
+                       __uint_as_float(u.y & 0xFFFF0000u));
+}
+
+__device__ __forceinline__ void store4(float* p, float4 v)
+{
+    *reinterpret_cast<float4*>(p) = v;
+}
+
+__device__ __forceinline__ void store4(bf16* p, float4 v)
+{
+    *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16(v.x, v.y), pack_bf16(v.z, v.w));
+}
+
+/* Byte of (token t, dim c) inside a page's keys and values of one head. */
+__device__ __forceinline__ int key_byte(int t, int c, int D)
+{
+    return (t >> 5) * (32 * D) + (c >> 4) * 512 + (t & 31) * 16 + (c & 15);
+}
+
+__device__ __forceinline__ int value_byte(int t, int c, int D)
+{
+    return (t >> 5) * (32 * D) + c * 32 + ((t >> 2) & 1) * 16 + ((t & 31) >> 3) * 4 + (t & 3);
+}
+
+/* One sequence of a batch: its packed rows [row0, row0 + q_len), its cached
+ * tokens [0, kv_len), the token number of row0 (negative if the rows outnumber
+ * the tokens).  Every bound that addresses memory is clamped. */
+struct SeqBounds {
+    int row0, q_len, kv_len, first;
+};
+
+__device__ __forceinline__ SeqBounds seq_bounds(const coli_kv_batch& b, int s)
+{
+    SeqBounds r;
+    const int lo = min(max(b.cu_q[s], 0), b.n_tokens), hi = min(max(b.cu_q[s + 1], 0), b.n_tokens);
+    const int64_t cap = (int64_t)b.max_pages * COLI_KV_BLOCK;
+    r.row0 = lo;
+    r.q_len = max(hi - lo, 0);
+    r.kv_len = (int)min((int64_t)max(b.kv_len[s], 0), cap);
+    r.first = r.kv_len - r.q_len;
+    return r;
+}
+
+/* The page of block `blk` of sequence s, or -1 for a missing one. */
+__device__ __forceinline__ int page_of(const coli_kv_batch& b, int n_pages, int s, int blk)
+{
+    const int p = b.page_table[(int64_t)s * b.max_pages + blk];
+    return (uint32_t)p < (uint32_t)n_pages ? p : -1;
+}
+
+} // namespace coli
+
+#endif
