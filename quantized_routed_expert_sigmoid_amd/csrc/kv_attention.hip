@@ -535,40 +535,63 @@ __global__ __launch_bounds__(256, 2) void kv_attention_split(AttnArgs g)
     }
 }
 
-/* Joins the ranges' partial sums, in their order: a wave per (token, head). */
-template <typename T, int D>
+/* Joins the ranges' partial sums, W waves per (token, head): wave w takes the
+ * ranges w, w + W, ... in order, four rows of partial sums in flight, and the
+ * waves' sums are added in wave order. */
+template <typename T, int D, int W>
 __global__ __launch_bounds__(256) void kv_attention_join(AttnArgs g)
 {
-    const int lane = threadIdx.x & 63;
+    constexpr int E = D / 64;
+    __shared__ float so[4][D], sl[4];
+    const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6, part = wv % W;
     const int64_t n = (int64_t)g.b.n_tokens * g.a.n_heads;
-    const int64_t at = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-    if (at >= n)
-        return;
+    const int64_t want = (int64_t)blockIdx.x * (4 / W) + wv / W;
+    const int64_t at = min(want, n - 1);
     const int64_t tok = at / g.a.n_heads;
     const int head = (int)(at % g.a.n_heads);
-    if (tok < g.b.cu_q[0] || tok >= g.b.cu_q[g.b.n_seq])
-        return; /* a row of no sequence */
+    /* not a row of no sequence */
+    const bool live = want < n && tok >= g.b.cu_q[0] && tok < g.b.cu_q[g.b.n_seq];
     const float2* ml = (const float2*)g.part_ml + at;
-    float m = -__builtin_inff();
-    for (int i = lane; i < g.nsplit; i += 64)
-        m = fmaxf(m, ml[i * n].x);
-    for (int w = 32; w >= 1; w >>= 1)
-        m = fmaxf(m, shfl_xor(m, w));
-    const float base = m == -__builtin_inff() ? 0.0f : m;
-    constexpr int E = D / 64;
-    float l = 0.0f, o[E];
+    float m = -__builtin_inff(), l = 0.0f, o[E];
 #pragma unroll
     for (int e = 0; e < E; ++e)
         o[e] = 0.0f;
-    for (int i = 0; i < g.nsplit; ++i) {
-        const float2 v = ml[i * n];
-        const float f = __builtin_amdgcn_exp2f(v.x - base);
-        l = __builtin_fmaf(v.y, f, l);
-        const float* p = g.part_o + (i * n + at) * D;
+    if (live) {
+        for (int i = lane; i < g.nsplit; i += 64)
+            m = fmaxf(m, ml[i * n].x);
+        for (int w = 32; w >= 1; w >>= 1)
+            m = fmaxf(m, shfl_xor(m, w));
+        const float base = m == -__builtin_inff() ? 0.0f : m;
+#pragma unroll 4
+        for (int i = part; i < g.nsplit; i += W) {
+            const float2 v = ml[i * n];
+            const float f = __builtin_amdgcn_exp2f(v.x - base);
+            l = __builtin_fmaf(v.y, f, l);
+            const float* p = g.part_o + (i * n + at) * D;
+#pragma unroll
+            for (int e = 0; e < E; ++e)
+                o[e] = __builtin_fmaf(p[lane + 64 * e], f, o[e]);
+        }
+    }
+    if constexpr (W > 1) {
 #pragma unroll
         for (int e = 0; e < E; ++e)
-            o[e] = __builtin_fmaf(p[lane + 64 * e], f, o[e]);
+            so[wv][lane + 64 * e] = o[e];
+        if (lane == 0)
+            sl[wv] = l;
+        __syncthreads();
+        if (part)
+            return;
+#pragma unroll
+        for (int w = 1; w < W; ++w) {
+            l += sl[wv + w];
+#pragma unroll
+            for (int e = 0; e < E; ++e)
+                o[e] += so[wv + w][lane + 64 * e];
+        }
     }
+    if (!live)
+        return;
     const float inv = l == 0.0f ? 0.0f : 1.0f / l;
 #pragma unroll
     for (int e = 0; e < E; ++e)
@@ -590,6 +613,7 @@ struct Plan {
 
 constexpr int64_t kTargetUnits = 1024;
 constexpr int kMaxSplit = 256;
+constexpr int64_t kMaxSplitRows = 1 << 22; /* bounds the workspace and the join's grid */
 
 Plan plan_attention(const coli_kv_cache& c, const coli_kv_batch& b, const coli_kv_attn& a)
 {
@@ -602,6 +626,8 @@ Plan plan_attention(const coli_kv_cache& c, const coli_kv_batch& b, const coli_k
     const int64_t seen = a.window > 0 ? min((int64_t)a.max_kv, (int64_t)a.window + b.max_q) : a.max_kv;
     const int64_t blocks = (seen + kBlk - 1) / kBlk;
     p.nsplit = (int)max((int64_t)1, min(min((kTargetUnits + units - 1) / units, (blocks + 3) / 4), (int64_t)kMaxSplit));
+    if ((int64_t)b.n_tokens * a.n_heads > kMaxSplitRows)
+        p.nsplit = 1;
     p.units = units * p.nsplit;
     const size_t n = (size_t)p.nsplit * b.n_tokens * a.n_heads;
     p.o_bytes = p.nsplit == 1 ? 0 : (n * c.head_dim * 4 + kPartAlign - 1) / kPartAlign * kPartAlign;
@@ -619,7 +645,10 @@ hipError_t launch(const AttnArgs& g, int rows, hipStream_t s)
         hipLaunchKernelGGL((kv_attention_split<bf16, 32, D>), dim3(grid), dim3(256), 0, s, g);
     if (g.nsplit > 1) {
         const int64_t n = (int64_t)g.b.n_tokens * g.a.n_heads;
-        hipLaunchKernelGGL((kv_attention_join<T, D>), dim3((uint32_t)((n + 3) / 4)), dim3(256), 0, s, g);
+        if (g.nsplit <= 8)
+            hipLaunchKernelGGL((kv_attention_join<T, D, 1>), dim3((uint32_t)((n + 3) / 4)), dim3(256), 0, s, g);
+        else
+            hipLaunchKernelGGL((kv_attention_join<T, D, 4>), dim3((uint32_t)n), dim3(256), 0, s, g);
     }
     return hipGetLastError();
 }
