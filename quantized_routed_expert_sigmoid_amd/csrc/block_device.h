@@ -69,6 +69,34 @@ __device__ __forceinline__ void store4(bf16* p, float4 v)
     *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16(v.x, v.y), pack_bf16(v.z, v.w));
 }
 
+/* The same where only the element's own alignment is known (the memory takes
+ * vectors at any address). */
+__device__ __forceinline__ float4 load4_any(const float* p)
+{
+    float4 v;
+    __builtin_memcpy(&v, p, 16);
+    return v;
+}
+
+__device__ __forceinline__ float4 load4_any(const bf16* p)
+{
+    uint2 u;
+    __builtin_memcpy(&u, p, 8);
+    return make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xFFFF0000u), __uint_as_float(u.y << 16),
+                       __uint_as_float(u.y & 0xFFFF0000u));
+}
+
+__device__ __forceinline__ void store4_any(float* p, float4 v)
+{
+    __builtin_memcpy(p, &v, 16);
+}
+
+__device__ __forceinline__ void store4_any(bf16* p, float4 v)
+{
+    const uint2 u = make_uint2(pack_bf16(v.x, v.y), pack_bf16(v.z, v.w));
+    __builtin_memcpy(p, &u, 8);
+}
+
 /* Byte of (token t, dim c) inside a page's keys and values of one head. */
 __device__ __forceinline__ int key_byte(int t, int c, int D)
 {

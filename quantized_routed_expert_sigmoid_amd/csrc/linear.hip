@@ -32,8 +32,8 @@ __device__ __forceinline__ float activate(float v, int act)
 {
     if (act == COLI_ACT_RELU)
         return fmaxf(v, 0.0f);
-    if (act == COLI_ACT_SILU)
-        return canon_silu(v);
+    if (act == COLI_ACT_SILU) /* 2^-21: one rounding each of the product, the power and the reciprocal */
+        return v * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(v * -1.44269504088896340736f));
     if (act == COLI_ACT_GELU)
         return 0.5f * v * (1.0f + erff(v * 0.70710678118654752f));
     return v;
@@ -100,53 +100,59 @@ __device__ __forceinline__ int k_order(int i)
 
 /*
  * Activations as fp16 operands: [step][tile of 32 tokens][term][chunk of 8 k][token] of 16 bytes, so that
- * a wave's operand load is one run of 1 KB.  The last step covers k = K - 64 .. K - 1; what an earlier step
- * has covered already is zero in it, as are tokens from S on.  A workgroup takes one token: its largest
- * value first, then its chunks.
+ * a wave's operand load is one run of 1 KB.  Steps past the row's end cover k = K - 64 .. K - 1; what an
+ * earlier step has covered already is zero in them, as are tokens from S on.  A workgroup takes a tile of 32 tokens and
+ * per steps: eight threads find a token's largest scale, then 32 threads write the tokens of one
+ * chunk as a run of 512 bytes.
  */
 template <int BITS, int NT>
-__global__ __launch_bounds__(256) void linear_expand(LinearArgs a, uint8_t* xh, float* xs, int tiles)
+__global__ __launch_bounds__(256) void linear_expand(LinearArgs a, uint8_t* xh, float* xs, int tiles, int steps, int per)
 {
-    __shared__ float part[4];
-    const int t = blockIdx.x, nb = a.K / 32, steps = (a.K + kKB - 1) / kKB;
+    __shared__ float up_of[kTileTok];
+    const int tile = blockIdx.x, step0 = blockIdx.y * per, nb = a.K / 32;
+    {
+        const int t = tile * kTileTok + (threadIdx.x >> 3);
+        const float* d = a.xd + (int64_t)min(t, a.S - 1) * nb;
+        float top = 0.0f;
+        for (int b = threadIdx.x & 7; b < nb; b += 8)
+            top = fmaxf(top, fabsf(d[b]));
+        top = fmaxf(top, shfl_xor(top, 1));
+        top = fmaxf(top, shfl_xor(top, 2));
+        top = fmaxf(top, shfl_xor(top, 4));
+        /* 2^e > 127 top, so |x| 2^(15 - e) < 2^15 */
+        int e = 0;
+        if (top > 0.0f)
+            (void)frexpf(top, &e);
+        e = max(e + 7, -111); /* 2^(15 - e) stays finite */
+        if ((threadIdx.x & 7) == 0) {
+            up_of[threadIdx.x >> 3] = top > 0.0f ? ldexpf(1.0f, 15 - e) : 0.0f;
+            if (step0 == 0 && t < a.S)
+                xs[t] = ldexpf(1.0f, e - 15);
+        }
+    }
+    __syncthreads();
+    const int t = tile * kTileTok + (threadIdx.x & 31);
     const bool live = t < a.S;
     const float* d = a.xd + (int64_t)min(t, a.S - 1) * nb;
     const int8_t* q = a.xq + (int64_t)min(t, a.S - 1) * a.K;
-    float top = 0.0f;
-    for (int b = threadIdx.x; b < nb; b += 256)
-        top = fmaxf(top, fabsf(d[b]));
-    for (int m = 32; m >= 1; m >>= 1)
-        top = fmaxf(top, shfl_xor(top, m));
-    if ((threadIdx.x & 63) == 0)
-        part[threadIdx.x >> 6] = top;
-    __syncthreads();
-    top = fmaxf(fmaxf(part[0], part[1]), fmaxf(part[2], part[3]));
-    /* 2^e > 127 top, so |x| 2^(15 - e) < 2^15 */
-    int e = 0;
-    if (top > 0.0f)
-        (void)frexpf(top, &e);
-    e = max(e + 7, -111); /* 2^(15 - e) stays finite */
-    const float up = top > 0.0f ? ldexpf(1.0f, 15 - e) : 0.0f;
-    if (threadIdx.x == 0 && live)
-        xs[t] = ldexpf(1.0f, e - 15);
-    for (int c = threadIdx.x; c < steps * 8; c += 256) {
-        const int step = c >> 3, k0 = step * kKB, at = min(k0, a.K - kKB) + (c & 7) * 8;
-        v8h hi = {0, 0, 0, 0, 0, 0, 0, 0}, lo = hi;
-        if (live && at >= k0) {
-            const uint2 w = *(const uint2*)(q + at);
-            const float s = d[at >> 5] * up;
+    const float up = live ? up_of[threadIdx.x & 31] : 0.0f;
+    const int c = threadIdx.x >> 5;
+    for (int step = step0; step < min(step0 + per, steps); ++step) {
+        const int at = min(step * kKB, a.K - kKB) + c * 8;
+        const uint2 w = *(const uint2*)(q + at);
+        const float s = at >= step * kKB ? d[at >> 5] * up : 0.0f;
+        v8h hi, lo;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const int k = k_order<BITS>(i);
-                float x = (float)(int8_t)((k < 4 ? w.x : w.y) >> (8 * (k & 3))) * s;
-                /* pinned: the compiler may otherwise take hi from the unrounded
-                 * product in one of its two uses, and a tie both ways */
-                asm("" : "+v"(x));
-                hi[i] = (_Float16)x;
-                lo[i] = (_Float16)(x - (float)hi[i]);
-            }
+        for (int i = 0; i < 8; ++i) {
+            const int k = k_order<BITS>(i);
+            float x = (float)(int8_t)((k < 4 ? w.x : w.y) >> (8 * (k & 3))) * s;
+            /* pinned: the compiler may otherwise take hi from the unrounded
+             * product in one of its two uses, and a tie both ways */
+            asm("" : "+v"(x));
+            hi[i] = (_Float16)x;
+            lo[i] = (_Float16)(x - (float)hi[i]);
         }
-        uint8_t* o = xh + ((((int64_t)step * tiles + t / kTileTok) * NT * 8 + (c & 7)) * kTileTok + t % kTileTok) * kChunk;
+        uint8_t* o = xh + ((((int64_t)step * tiles + tile) * NT * 8 + c) * kTileTok + (threadIdx.x & 31)) * kChunk;
         *(v8h*)o = hi;
         if constexpr (NT == 2)
             *(v8h*)(o + 8 * kTileTok * kChunk) = lo;
@@ -203,58 +209,135 @@ __device__ __forceinline__ v8h codes_f16(uint32_t w0, uint32_t w1)
     return v;
 }
 
+/* Where a workgroup's tile lies, and a wave's part of it: rows n0 + 32 r,
+ * r < 2, tokens tok0 + 32 t, t < TT; lane (col, h) of a tile holds the token
+ * col and the rows 8 (i / 4) + 4 h + i % 4 of accumulator register i. */
+struct TileAt {
+    int n0, tok0, tile0; /* tile0: the workgroup's first tile of 32 tokens */
+};
+
+template <int TT>
+__device__ __forceinline__ TileAt tile_at(int id, int n_tiles, int t_tiles, int wv)
+{
+    /* bands of eight token tiles, column by column of weight tiles */
+    constexpr int GT = 8;
+    const int band = id / (GT * n_tiles), in = id % (GT * n_tiles), wide = min(GT, t_tiles - band * GT);
+    TileAt t;
+    t.n0 = in / wide * kTileN + (wv & 1) * 64;
+    t.tile0 = (band * GT + in % wide) * 2 * TT;
+    t.tok0 = (t.tile0 + (wv >> 1) * TT) * kTileTok;
+    return t;
+}
+
+/* One uniform branch on the activation for N values. */
+template <int N>
+__device__ __forceinline__ void activate_all(float* v, int act)
+{
+    if (act == COLI_ACT_RELU) {
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            v[i] = activate(v[i], COLI_ACT_RELU);
+    } else if (act == COLI_ACT_SILU) {
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            v[i] = activate(v[i], COLI_ACT_SILU);
+    } else if (act == COLI_ACT_GELU) {
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            v[i] = activate(v[i], COLI_ACT_GELU);
+    }
+}
+
+/* Residual and store of four consecutive rows n .. n + 3 of a token. */
+template <typename TO>
+__device__ __forceinline__ void store_rows(const LinearArgs& a, int tok, int n, const float* v)
+{
+    if (tok >= a.S || n >= a.N)
+        return;
+    TO* out = (TO*)a.out + (int64_t)tok * a.N + n;
+    const TO* res = a.residual ? (const TO*)a.residual + (int64_t)tok * a.N + n : nullptr;
+    if (n + 4 <= a.N) {
+        float4 r = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (res)
+            r = load4_any(res);
+        store4_any(out, make_float4(v[0] + r.x, v[1] + r.y, v[2] + r.z, v[3] + r.w));
+    } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (n + j < a.N)
+                store1(out + j, v[j] + (res ? to_f32(res[j]) : 0.0f));
+    }
+}
+
+/* What the tile kernels share of a launch. */
+struct TileArgs {
+    const uint8_t* xh;
+    const float* xs;
+    float* part; /* [split][tile][wave][r][t][i / 4][lane] of four sums, or null */
+    int tiles, n_tiles, t_tiles, stages, splits;
+};
+
 /*
  * A workgroup of 2 x 2 waves takes 128 weight rows x 64 TT tokens, a wave 64
- * rows x 32 TT tokens of them (2 x TT tiles of v_mfma_f32_32x32x16_f16), with
- * steps of 64 k: the next step's operands travel from memory to LDS under this
- * step's products.  Weights stay packed in LDS and are unpacked by the waves
- * that multiply them.  Lane (l % 32, h = l / 32) of instruction i of a step
- * takes k = 16 i + 8 h .. + 7 of a step, so that one instruction stays inside
- * one scale group.
+ * rows x 32 TT tokens of them (2 x TT tiles of v_mfma_f32_32x32x16_f16), in
+ * stages of SPB steps of 64 k: the next stage's operands travel from memory to
+ * LDS under this stage's products.  Weights stay packed in LDS and are
+ * unpacked by the waves that multiply them.  Lane (l % 32, h = l / 32) of
+ * instruction i of a step takes k = 16 i + 8 h .. + 7 of the step, so that one
+ * instruction stays inside one scale group.  With splits > 1 the stages are
+ * shared out and linear_join adds the parts.
  */
-template <int BITS, int NT, int TT, bool GROUPED, typename TO>
-__global__ __launch_bounds__(256, 2) void linear_tiles(LinearArgs a, const uint8_t* xh, const float* xs, int tiles,
-                                                       int n_tiles, int t_tiles, int vec)
+template <int BITS, int NT, int TT, int SPB, bool GROUPED, typename TO>
+__global__ __launch_bounds__(256, 2) void linear_tiles(LinearArgs a, TileArgs ta)
 {
-    constexpr int XB = 2 * TT * NT * 8 * kTileTok * kChunk; /* bytes of a step's activations */
-    constexpr int WC = BITS / 2;                            /* 16-byte chunks of a row's step (int2: 1) */
-    constexpr int WB = kTileN * WC * kChunk;
+    constexpr int XS = 2 * TT * NT * 8 * kTileTok * kChunk; /* bytes of a step's activations */
+    constexpr int XB = XS * SPB;
+    constexpr int CPS = BITS / 2;   /* 16-byte chunks of a row's step */
+    constexpr int LPR = CPS * SPB;  /* and of its stage */
+    constexpr int WB = kTileN * LPR * kChunk;
+    constexpr int kWRuns = WB / 1024;
     extern __shared__ __align__(1024) uint8_t lds[];
     const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6, h = lane >> 5, col = lane & 31;
     const int wn = wv & 1, wt = wv >> 1;
 
     /* Workgroups go to the eight XCDs in turn; each XCD takes a contiguous run
-     * of tiles, eight token tiles to a column of weight tiles, so that the
-     * tiles it works on at a time share operands in its L2. */
-    const int total = n_tiles * t_tiles, per = (total + 7) / 8;
-    const int id = (int)(blockIdx.x & 7) * per + (int)(blockIdx.x >> 3);
-    if (id >= total || (int)(blockIdx.x >> 3) >= per)
+     * of tiles, so that the tiles it works on at a time share operands in its
+     * L2. */
+    const int per = (int)gridDim.x >> 3, total = ta.n_tiles * ta.t_tiles;
+    const int unit = (int)(blockIdx.x & 7) * per + (int)(blockIdx.x >> 3);
+    if (unit >= total * ta.splits)
         return;
-    constexpr int GT = 8;
-    const int band = id / (GT * n_tiles), in = id % (GT * n_tiles), wide = min(GT, t_tiles - band * GT);
-    const int tn = in / wide, tt0 = band * GT + in % wide;
+    const int id = unit / ta.splits, split = unit % ta.splits;
+    const TileAt at = tile_at<TT>(id, ta.n_tiles, ta.t_tiles, wv);
+    const int nw0 = at.n0 - wn * 64; /* the workgroup's first row */
+    const int each = (ta.stages + ta.splits - 1) / ta.splits;
+    const int s0 = split * each, s1 = min(s0 + each, ta.stages);
 
-    const int steps = (a.K + kKB - 1) / kKB, n0 = tn * kTileN;
     const int64_t row_bytes = (int64_t)a.K * BITS / 8;
     const uint8_t* w = (const uint8_t*)a.w;
+    /* Chunk c of row n of a stage lies in LDS slot c ^ f(n) of the row's LPR, so
+     * that 16 rows' reads of one chunk fall into different banks. */
+    constexpr int RPB = LPR >= 16 ? 1 : 16 / LPR;
+    auto swz = [](int n) { return n / RPB % LPR; };
 
-    /* this wave's share of a step's loads: runs of 64 chunks */
-    auto fetch = [&](int step, uint8_t* buf) {
-        const uint8_t* x = xh + ((int64_t)step * tiles + tt0 * 2 * TT) * (NT * 8 * kTileTok * kChunk);
+    auto fetch = [&](int stage, uint8_t* buf) {
+        const uint8_t* x = ta.xh + ((int64_t)stage * SPB * ta.tiles + at.tile0) * (NT * 8 * kTileTok * kChunk);
+        const int64_t x_step = (int64_t)ta.tiles * (NT * 8 * kTileTok * kChunk);
 #pragma unroll
-        for (int i = 0; i < XB / 4096; ++i) {
-            const int o = (i * 4 + wv) * 1024;
-            to_lds(x + o + lane * 16, buf + o);
-        }
-        const int64_t kb = (int64_t)min(step * kKB, a.K - kKB) * BITS / 8;
-        /* chunk c of row n at (c * 128 + n) * 16 */
+        for (int j = 0; j < SPB; ++j)
 #pragma unroll
-        for (int i = 0; i < (WB / 1024 + 3) / 4; ++i) {
+            for (int i = 0; i < XS / 4096; ++i) {
+                const int o = (i * 4 + wv) * 1024;
+                to_lds(x + j * x_step + o + lane * 16, buf + j * XS + o);
+            }
+#pragma unroll
+        for (int i = 0; i < (kWRuns + 3) / 4; ++i) {
             const int run = i * 4 + wv;
-            if (WB / 1024 % 4 && run >= WB / 1024)
+            if (kWRuns % 4 && run >= kWRuns)
                 break;
-            const int c = run * 64 / kTileN, n = min(n0 + run * 64 % kTileN + lane, a.N - 1);
-            to_lds(w + n * row_bytes + kb + c * 16, buf + XB + run * 1024);
+            const int slot = run * 64 + lane, n = slot / LPR, c = slot % LPR ^ swz(n);
+            const int64_t kb = (int64_t)min((stage * SPB + c / CPS) * kKB, a.K - kKB) * BITS / 8;
+            to_lds(w + min(nw0 + n, a.N - 1) * row_bytes + kb + c % CPS * kChunk, buf + XB + run * 1024);
         }
     };
 
@@ -279,7 +362,7 @@ __global__ __launch_bounds__(256, 2) void linear_tiles(LinearArgs a, const uint8
             for (int r = 0; r < 2; ++r)
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
-                    const int n = min(n0 + wn * 64 + r * 32 + 8 * (i / 4) + 4 * h + i % 4, a.N - 1);
+                    const int n = min(at.n0 + r * 32 + 8 * (i / 4) + 4 * h + i % 4, a.N - 1);
                     const float s = a.w_scale[(int64_t)n * gpr + g];
 #pragma unroll
                     for (int t = 0; t < TT; ++t) {
@@ -289,128 +372,175 @@ __global__ __launch_bounds__(256, 2) void linear_tiles(LinearArgs a, const uint8
                 }
         }
     };
+    auto group_of = [&](int step, int i) { return (min(step * kKB, a.K - kKB) + 16 * i) / a.group; };
 
-    fetch(0, lds);
-    __syncthreads();
-    int g = 0;
-    for (int step = 0; step < steps; ++step) {
-        uint8_t* buf = lds + (step & 1) * (XB + WB);
-        if (step + 1 < steps)
-            fetch(step + 1, lds + (~step & 1) * (XB + WB));
-        const int kb = min(step * kKB, a.K - kKB);
+    int g = GROUPED ? group_of(s0 * SPB, 0) : 0;
+    if (s0 < s1)
+        fetch(s0, lds);
+    for (int stage = s0; stage < s1; ++stage) {
+        /* past the barrier this stage's loads have arrived in every wave, and every
+         * wave has left the buffer that is loaded next */
+        __syncthreads();
+        if (stage + 1 < s1)
+            fetch(stage + 1, lds + ((stage - s0 + 1) & 1) * (XB + WB));
+        const uint8_t* buf = lds + ((stage - s0) & 1) * (XB + WB);
+        /* Instruction i multiplies what was read two and unpacked one
+         * instruction ago, so that reads and unpacking run in the shadow of the
+         * matrix cores. */
+        constexpr int I = 4 * SPB;
+        uint2 wraw[2][2];
+        v8h xf[2][TT * NT], wf[2][2];
+        auto read_w = [&](int i) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+            for (int r = 0; r < 2; ++r) {
+                const int n = wn * 64 + r * 32 + col;
+                const uint8_t* p = buf + XB + n * (LPR * kChunk);
+                const int k = i & 3;
+                auto slot = [&](int c) { return ((i >> 2) * CPS + c ^ swz(n)) * kChunk; };
+                if constexpr (BITS == 8)
+                    wraw[i & 1][r] = *(const uint2*)(p + slot(k) + h * 8);
+                else if constexpr (BITS == 4)
+                    wraw[i & 1][r].x = *(const uint32_t*)(p + slot(k >> 1) + (k & 1) * 8 + h * 4);
+                else
+                    wraw[i & 1][r].x = *(const uint32_t*)(p + slot(0) + k * 4);
+            }
+        };
+        auto read_x = [&](int i) {
+#pragma unroll
+            for (int t = 0; t < TT * NT; ++t)
+                xf[i & 1][t] = *(const v8h*)(buf + (i >> 2) * XS +
+                                             ((wt * TT * NT + t) * 8 + 2 * (i & 3)) * (kTileTok * kChunk) + lane * 16);
+        };
+        auto unpack = [&](int i) {
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                const uint2 v = wraw[i & 1][r];
+                if constexpr (BITS == 2)
+                    wf[i & 1][r] = codes_f16<2>(__builtin_amdgcn_perm(0, v.x, h ? 0x0C030C02u : 0x0C010C00u), 0);
+                else
+                    wf[i & 1][r] = codes_f16<BITS>(v.x, v.y);
+            }
+        };
+        read_w(0);
+        read_x(0);
+        read_w(1);
+        unpack(0);
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int i = 0; i < I; ++i) {
             if constexpr (GROUPED) {
-                /* a step may start in an earlier group than the last one ended in:
-                 * its activations there are zero */
+                /* the last step may start in an earlier group than the one before
+                 * ended in: its activations there are zero */
                 if (!(i & 1)) {
-                    const int now = (kb + 16 * i) / a.group;
+                    const int now = group_of(stage * SPB + (i >> 2), i & 3);
                     if (now > g) {
                         fold(g);
                         g = now;
                     }
                 }
             }
-            v8h wf[2];
-#pragma unroll
-            for (int r = 0; r < 2; ++r) {
-                const int n = wn * 64 + r * 32 + col;
-                const uint8_t* p = buf + XB;
-                if constexpr (BITS == 8) {
-                    const uint2 v = *(const uint2*)(p + (i * kTileN + n) * 16 + h * 8);
-                    wf[r] = codes_f16<8>(v.x, v.y);
-                } else if constexpr (BITS == 4) {
-                    wf[r] = codes_f16<4>(*(const uint32_t*)(p + ((i >> 1) * kTileN + n) * 16 + (i & 1) * 8 + h * 4), 0);
-                } else {
-                    const uint32_t v = *(const uint32_t*)(p + n * 16 + i * 4);
-                    wf[r] = codes_f16<2>(__builtin_amdgcn_perm(0, v, h ? 0x0C030C02u : 0x0C010C00u), 0);
-                }
+            if (i + 1 < I) {
+                read_x(i + 1);
+                unpack(i + 1);
             }
+            if (i + 2 < I)
+                read_w(i + 2);
 #pragma unroll
             for (int t = 0; t < TT; ++t)
 #pragma unroll
-                for (int e = 0; e < NT; ++e) {
-                    const v8h x = *(const v8h*)(buf + (((wt * TT + t) * NT + e) * 8 + 2 * i) * (kTileTok * kChunk) +
-                                                lane * 16);
+                for (int e = 0; e < NT; ++e)
 #pragma unroll
                     for (int r = 0; r < 2; ++r) {
                         v16f& o = GROUPED ? part[GROUPED ? r : 0][GROUPED ? t : 0] : acc[r][t];
-                        o = __builtin_amdgcn_mfma_f32_32x32x16_f16(wf[r], x, o, 0, 0, 0);
+                        o = __builtin_amdgcn_mfma_f32_32x32x16_f16(wf[i & 1][r], xf[i & 1][t * NT + e], o, 0, 0, 0);
                     }
-                }
+#pragma unroll
+            for (int k = 0; k < 2 * TT * NT; ++k) {
+                __builtin_amdgcn_sched_group_barrier(0x008, 1, 0); /* a matrix instruction, */
+                __builtin_amdgcn_sched_group_barrier(0x100, 1, 0); /* an LDS read and */
+                __builtin_amdgcn_sched_group_barrier(0x002, 4, 0); /* four VALU under it */
+            }
+            __builtin_amdgcn_sched_barrier(0);
         }
-        __syncthreads();
     }
     fold(g);
 
-    /* epilogue: lane (token col, rows 8 (i / 4) + 4 h + i % 4), one uniform
-     * branch on the activation for all of them */
-    const int tok0 = (tt0 * 2 * TT + wt * TT) * kTileTok + col;
-    float scale[TT];
+    if (ta.splits == 1) {
+        float v[2][TT][16], xscale[TT];
 #pragma unroll
-    for (int t = 0; t < TT; ++t)
-        scale[t] = xs[min(tok0 + t * kTileTok, a.S - 1)];
+        for (int t = 0; t < TT; ++t)
+            xscale[t] = ta.xs[min(at.tok0 + t * kTileTok + col, a.S - 1)];
+#pragma unroll
+        for (int r = 0; r < 2; ++r)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                const int n = min(at.n0 + r * 32 + 8 * (i / 4) + 4 * h + i % 4, a.N - 1);
+                const float ws = GROUPED ? 1.0f : a.w_scale[n], bias = a.bias ? a.bias[n] : 0.0f;
+#pragma unroll
+                for (int t = 0; t < TT; ++t)
+                    v[r][t][i] = __builtin_fmaf(acc[r][t][i], xscale[t] * ws, bias);
+            }
+        activate_all<2 * TT * 16>(&v[0][0][0], a.act);
+#pragma unroll
+        for (int t = 0; t < TT; ++t)
+#pragma unroll
+            for (int r = 0; r < 2; ++r)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    store_rows<TO>(a, at.tok0 + t * kTileTok + col, at.n0 + r * 32 + 8 * i + 4 * h, &v[r][t][4 * i]);
+        return;
+    }
+    float4* o = (float4*)ta.part + (((int64_t)split * total + id) * 4 + wv) * (2 * TT * 4 * 64) + lane;
 #pragma unroll
     for (int r = 0; r < 2; ++r)
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            const int n = min(n0 + wn * 64 + r * 32 + 8 * (i / 4) + 4 * h + i % 4, a.N - 1);
-            const float ws = GROUPED ? 1.0f : a.w_scale[n], bias = a.bias ? a.bias[n] : 0.0f;
+        for (int t = 0; t < TT; ++t)
 #pragma unroll
-            for (int t = 0; t < TT; ++t)
-                acc[r][t][i] = __builtin_fmaf(acc[r][t][i], scale[t] * ws, bias);
-        }
-    auto each = [&](auto f) {
-#pragma unroll
-        for (int r = 0; r < 2; ++r)
-#pragma unroll
-            for (int t = 0; t < TT; ++t)
-#pragma unroll
-                for (int i = 0; i < 16; ++i)
-                    acc[r][t][i] = f(acc[r][t][i]);
-    };
-    if (a.act == COLI_ACT_RELU)
-        each([](float v) { return activate(v, COLI_ACT_RELU); });
-    else if (a.act == COLI_ACT_SILU)
-        each([](float v) { return activate(v, COLI_ACT_SILU); });
-    else if (a.act == COLI_ACT_GELU)
-        each([](float v) { return activate(v, COLI_ACT_GELU); });
-#pragma unroll
-    for (int t = 0; t < TT; ++t) {
-        const int tok = tok0 + t * kTileTok;
-        if (tok >= a.S)
-            continue;
-        TO* out = (TO*)a.out + (int64_t)tok * a.N;
-        const TO* res = a.residual ? (const TO*)a.residual + (int64_t)tok * a.N : nullptr;
-#pragma unroll
-        for (int r = 0; r < 2; ++r)
-#pragma unroll
-            for (int i = 0; i < 16; i += 4) {
-                const int n = n0 + wn * 64 + r * 32 + 2 * i + 4 * h;
-                float4 y = make_float4(acc[r][t][i], acc[r][t][i + 1], acc[r][t][i + 2], acc[r][t][i + 3]);
-                if (vec) {
-                    if (n >= a.N)
-                        continue;
-                    if (res) {
-                        const float4 v = load4(res + n);
-                        y = make_float4(y.x + v.x, y.y + v.y, y.z + v.z, y.w + v.w);
-                    }
-                    store4(out + n, y);
-                } else {
-                    const float e[4] = {y.x, y.y, y.z, y.w};
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        if (n + j < a.N)
-                            store1(out + n + j, e[j] + (res ? to_f32(res[n + j]) : 0.0f));
-                }
-            }
+            for (int i = 0; i < 4; ++i)
+                o[((r * TT + t) * 4 + i) * 64] =
+                    make_float4(acc[r][t][4 * i], acc[r][t][4 * i + 1], acc[r][t][4 * i + 2], acc[r][t][4 * i + 3]);
+}
+
+/* Adds the splits' sums in their order and finishes them: a workgroup takes
+ * one of a tile's 2 TT * 4 groups of four rows, in the tile kernel's layout. */
+template <int TT, bool GROUPED, typename TO>
+__global__ __launch_bounds__(256) void linear_join(LinearArgs a, TileArgs ta)
+{
+    const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6, total = ta.n_tiles * ta.t_tiles;
+    const int id = blockIdx.x, q = blockIdx.y, i = q & 3, t = (q >> 2) % TT, r = (q >> 2) / TT;
+    const float4* o = (const float4*)ta.part + (((int64_t)id * 4 + wv) * (2 * TT * 4) + q) * 64 + lane;
+    const int64_t step = (int64_t)total * 4 * (2 * TT * 4) * 64;
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int s = 0; s < ta.splits; ++s) {
+        const float4 x = o[s * step];
+        v = make_float4(v.x + x.x, v.y + x.y, v.z + x.z, v.w + x.w);
     }
+    const TileAt at = tile_at<TT>(id, ta.n_tiles, ta.t_tiles, wv);
+    const int tok = at.tok0 + t * kTileTok + (lane & 31), n = at.n0 + r * 32 + 8 * i + 4 * (lane >> 5);
+    const float xscale = ta.xs[min(tok, a.S - 1)];
+    float e[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const int m = min(n + j, a.N - 1);
+        e[j] = __builtin_fmaf(e[j], GROUPED ? xscale : xscale * a.w_scale[m], a.bias ? a.bias[m] : 0.0f);
+    }
+    activate_all<4>(e, a.act);
+    store_rows<TO>(a, tok, n, e);
 }
 
 struct TilePlan {
-    int tt, tiles, n_tiles, t_tiles, steps, terms;
-    size_t x_bytes, total;
+    int tt, spb, tiles, n_tiles, t_tiles, stages, splits, terms;
+    size_t x_bytes, part_at, total;
 };
+
+constexpr int kWantTiles = 256; /* workgroups that a launch should have: one per CU */
+
+/* steps per stage of a tile width */
+constexpr int stage_steps(int tt, int terms)
+{
+    return tt == 4 ? 1 : tt == 2 ? (terms == 1 ? 2 : 1) : (terms == 1 ? 4 : 2);
+}
 
 TilePlan tile_plan(int32_t S, int32_t N, int32_t K, int32_t group, int32_t out_type)
 {
@@ -422,11 +552,16 @@ TilePlan tile_plan(int32_t S, int32_t N, int32_t K, int32_t group, int32_t out_t
     p.tt = most;
     while (p.tt > 1 && (int64_t)p.n_tiles * ((S + 64 * p.tt - 1) / (64 * p.tt)) < 256)
         p.tt /= 2;
+    p.spb = stage_steps(p.tt, p.terms);
     p.t_tiles = (S + 64 * p.tt - 1) / (64 * p.tt);
     p.tiles = p.t_tiles * 2 * p.tt;
-    p.steps = (K + kKB - 1) / kKB;
-    p.x_bytes = (size_t)p.steps * p.tiles * p.terms * 8 * kTileTok * kChunk;
-    p.total = (p.x_bytes + (size_t)S * 4 + 255) / 256 * 256;
+    p.stages = (K + kKB * p.spb - 1) / (kKB * p.spb);
+    p.x_bytes = (size_t)p.stages * p.spb * p.tiles * p.terms * 8 * kTileTok * kChunk;
+    /* too few tiles for the CUs: the stages are shared out, two at least each */
+    const int total = p.n_tiles * p.t_tiles;
+    p.splits = total >= kWantTiles ? 1 : max(1, min((kWantTiles + total - 1) / total, p.stages / 2));
+    p.part_at = (p.x_bytes + (size_t)S * 4 + 255) / 256 * 256;
+    p.total = p.part_at + (p.splits > 1 ? (size_t)p.splits * total * kTileN * 64 * p.tt * 4 : 0);
     return p;
 }
 
@@ -438,21 +573,34 @@ bool use_tiles(int32_t S, int32_t K)
 template <int BITS, int NT, int TT, bool GROUPED, typename TO>
 hipError_t launch_tiles_t(const LinearArgs& a, const TilePlan& p, hipStream_t s)
 {
+    constexpr int SPB = stage_steps(TT, NT);
+    TileArgs ta;
     uint8_t* xh = (uint8_t*)a.ws;
     float* xs = (float*)(xh + p.x_bytes);
-    hipLaunchKernelGGL((linear_expand<BITS, NT>), dim3(p.tiles * kTileTok), dim3(256), 0, s, a, xh, xs, p.tiles);
-    constexpr int bytes = 2 * (2 * TT * NT * 8 * kTileTok * kChunk + kTileN * (BITS / 2) * kChunk);
+    ta.xh = xh;
+    ta.xs = xs;
+    ta.part = p.splits > 1 ? (float*)((uint8_t*)a.ws + p.part_at) : nullptr;
+    ta.tiles = p.tiles;
+    ta.n_tiles = p.n_tiles;
+    ta.t_tiles = p.t_tiles;
+    ta.stages = p.stages;
+    ta.splits = p.splits;
+    const int steps = p.stages * SPB;
+    const int per = max(1, min(8, p.tiles * steps / 512));
+    hipLaunchKernelGGL((linear_expand<BITS, NT>), dim3(p.tiles, (steps + per - 1) / per), dim3(256), 0, s, a, xh, xs,
+                       p.tiles, steps, per);
+    constexpr int bytes = 2 * SPB * (2 * TT * NT * 8 * kTileTok * kChunk + kTileN * (BITS / 2) * kChunk);
+    const auto kernel = linear_tiles<BITS, NT, TT, SPB, GROUPED, TO>;
     if (bytes > 64 * 1024) {
-        const hipError_t e = hipFuncSetAttribute((const void*)linear_tiles<BITS, NT, TT, GROUPED, TO>,
-                                                 hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+        const hipError_t e =
+            hipFuncSetAttribute((const void*)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
         if (e != hipSuccess)
             return e;
     }
     const int total = p.n_tiles * p.t_tiles;
-    /* rows of whole, aligned groups of four outputs */
-    const int vec = a.N % 4 == 0 && ((uintptr_t)a.out | (uintptr_t)a.residual) % (4 * sizeof(TO)) == 0;
-    hipLaunchKernelGGL((linear_tiles<BITS, NT, TT, GROUPED, TO>), dim3((total + 7) / 8 * 8), dim3(256), bytes, s, a,
-                       xh, xs, p.tiles, p.n_tiles, p.t_tiles, vec);
+    hipLaunchKernelGGL(kernel, dim3((total * p.splits + 7) / 8 * 8), dim3(256), bytes, s, a, ta);
+    if (p.splits > 1)
+        hipLaunchKernelGGL((linear_join<TT, GROUPED, TO>), dim3(total, 2 * TT * 4), dim3(256), 0, s, a, ta);
     return hipGetLastError();
 }
 
