@@ -2,10 +2,9 @@
  * linear.hip -- quantised matrix product of Q8_0 activations with bias,
  * activation and residual in its epilogue.
  *
- * Few tokens (linear_rows_kernel): one wave per weight row and up to four
- * tokens; each lane takes whole 32-element blocks, whose exact integer dot
- * products times the two scales are summed in fp32, first in the lane and then
- * over the wave.
+ * Few tokens (linear_rows_kernel): exact integer dot products of weight and
+ * activation codes inside a 32-element block, times the two scales, summed in
+ * fp32 first in the lane and then over the wave.
  *
  * Many tokens: linear_expand writes the activations once as fp16 and
  * linear_tiles runs the product on the fp16 matrix cores.  A weight code is
@@ -39,43 +38,191 @@ __device__ __forceinline__ float activate(float v, int act)
     return v;
 }
 
-template <int BITS, typename TO>
-__global__ __launch_bounds__(256) void linear_rows_kernel(LinearArgs a)
+/* ---- few tokens ----------------------------------------------------------- */
+
+/* Sum over the wave in lane 63, by lane moves within the VALU (device_common.h's
+ * wave_reduce_u32 explains them). */
+__device__ __forceinline__ float wave_sum63(float v)
 {
-    constexpr int T = 4;
-    const int lane = threadIdx.x & 63;
-    const int n = blockIdx.x * 4 + (threadIdx.x >> 6), t0 = blockIdx.y * T;
-    if (n >= a.N)
-        return;
-    const int nb = a.K / 32, gb = a.group ? a.group / 32 : nb;
-    const uint32_t* w = (const uint32_t*)a.w + (int64_t)n * nb * BITS;
-    const float* ws = a.w_scale + (int64_t)n * (nb / gb);
-    float acc[T] = {0.f, 0.f, 0.f, 0.f};
-    for (int b = lane; b < nb; b += 64) {
-        uint32_t wb[BITS];
-        for (int i = 0; i < BITS; ++i)
-            wb[i] = w[(int64_t)b * BITS + i];
-        const float sc = ws[b / gb];
-        for (int t = 0; t < T; ++t) {
-            const int64_t row = min(t0 + t, a.S - 1);
-            uint32_t x[8], xa[8];
-            for (int i = 0; i < 8; ++i)
-                x[i] = ((const uint32_t*)(a.xq + row * a.K))[b * 8 + i];
-            prep_dot<BITS>(x, xa);
-            const float d = a.xd[row * nb + b];
-            acc[t] = __builtin_fmaf(sc * d, (float)block_dot<BITS>(wb, xa), acc[t]);
+#define COLI_ADD_DPP(ctrl, rows) \
+    v += __uint_as_float((uint32_t)__builtin_amdgcn_update_dpp(0, (int)__float_as_uint(v), ctrl, rows, 0xF, false))
+    COLI_ADD_DPP(0x111, 0xF);
+    COLI_ADD_DPP(0x112, 0xF);
+    COLI_ADD_DPP(0x114, 0xF);
+    COLI_ADD_DPP(0x118, 0xF);
+    COLI_ADD_DPP(0x142, 0xA);
+    COLI_ADD_DPP(0x143, 0xC);
+#undef COLI_ADD_DPP
+    return v;
+}
+
+constexpr int kMaxRowsWg = 256; /* weight rows of a workgroup, most */
+
+/*
+ * A wave keeps the activations of up to T tokens in registers, NU units of a
+ * weight row per lane (a unit: 16 bytes of an int8 or int4 row, 8 of an int2
+ * row; unit 64 j + lane), and streams its rows past them, one row's loads
+ * ahead of the products.  A unit lies inside one 32-element block, so its
+ * exact integer dot product takes one pair of scales.  Rows longer than 64 NU
+ * units go in several rounds, their sums kept in LDS.
+ */
+template <int BITS, int T, int NU, bool GROUPED, typename TO>
+__global__ __launch_bounds__(256) void linear_rows_kernel(LinearArgs a, int rows_wg)
+{
+    constexpr int W = BITS == 2 ? 2 : 4;      /* words of a unit */
+    constexpr int UK = W * 32 / BITS;         /* its codes: 16, 32, 32 */
+    constexpr int X = BITS == 8 ? 4 : 8;      /* its activation words */
+    __shared__ float sums[kMaxRowsWg][T];
+    const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
+    const int n0 = blockIdx.x * rows_wg, n1 = min(n0 + rows_wg, a.N), t0 = blockIdx.y * T;
+    const int nb = a.K / 32, units = a.K / UK, gpr = GROUPED ? a.K / a.group : 1;
+    const uint32_t* w = (const uint32_t*)a.w;
+
+    for (int u0 = 0; u0 < units; u0 += 64 * NU) {
+        uint32_t xa[T][NU][X];
+        float xd[T][NU];
+        int at[NU], grp[NU];
+#pragma unroll
+        for (int j = 0; j < NU; ++j) {
+            const int u = u0 + 64 * j + lane;
+            at[j] = min(u, units - 1);
+            if constexpr (GROUPED)
+                grp[j] = at[j] * UK / a.group;
+#pragma unroll
+            for (int t = 0; t < T; ++t) {
+                const int64_t tok = min(t0 + t, a.S - 1);
+                const uint32_t* x = (const uint32_t*)(a.xq + tok * a.K + (int64_t)at[j] * UK);
+                xd[t][j] = u < units ? a.xd[tok * nb + at[j] * UK / 32] : 0.0f;
+                if constexpr (BITS == 8) {
+                    const uint4 v = *(const uint4*)x;
+                    xa[t][j][0] = v.x;
+                    xa[t][j][1] = v.y;
+                    xa[t][j][2] = v.z;
+                    xa[t][j][3] = v.w;
+                } else {
+                    const uint4 lo = *(const uint4*)x, hi = *(const uint4*)(x + 4);
+                    const uint32_t v[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+                    prep_dot<BITS>(v, xa[t][j]);
+                }
+            }
+        }
+        uint32_t wb[2][NU][W];
+        float ws[2][GROUPED ? NU : 1];
+        auto load = [&](int n, int p) {
+            const int64_t row = min(n, n1 - 1);
+#pragma unroll
+            for (int j = 0; j < NU; ++j) {
+                const uint32_t* q = w + (row * units + at[j]) * W;
+                if constexpr (W == 4) {
+                    const uint4 v = *(const uint4*)q;
+                    wb[p][j][0] = v.x;
+                    wb[p][j][1] = v.y;
+                    wb[p][j][2] = v.z;
+                    wb[p][j][3] = v.w;
+                } else {
+                    const uint2 v = *(const uint2*)q;
+                    wb[p][j][0] = v.x;
+                    wb[p][j][1] = v.y;
+                }
+                if constexpr (GROUPED)
+                    ws[p][j] = a.w_scale[row * gpr + grp[j]];
+            }
+        };
+        auto row = [&](int n, int p) {
+            float acc[T];
+#pragma unroll
+            for (int t = 0; t < T; ++t) {
+                acc[t] = 0.0f;
+#pragma unroll
+                for (int j = 0; j < NU; ++j) {
+                    int32_t s = 0;
+                    if constexpr (BITS == 8) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            s = COLI_SDOT4(wb[p][j][i], xa[t][j][i], s);
+                    } else {
+                        s = block_dot<BITS>(wb[p][j], xa[t][j]);
+                    }
+                    const float d = GROUPED ? xd[t][j] * ws[p][GROUPED ? j : 0] : xd[t][j];
+                    acc[t] = __builtin_fmaf(d, (float)s, acc[t]);
+                }
+                acc[t] = wave_sum63(acc[t]);
+            }
+            if (lane == 63 && n < n1) {
+#pragma unroll
+                for (int t = 0; t < T; ++t)
+                    sums[n - n0][t] = u0 ? sums[n - n0][t] + acc[t] : acc[t];
+            }
+        };
+        load(n0 + wv, 0);
+        for (int n = n0 + wv; n < n1; n += 8) {
+            load(n + 4, 1);
+            row(n, 0);
+            load(n + 8, 0);
+            row(n + 4, 1);
         }
     }
-    for (int t = 0; t < T; ++t) {
-        const float v = wave_sum(acc[t]);
-        if (lane == t && t0 + t < a.S) {
-            const int64_t o = (int64_t)(t0 + t) * a.N + n;
-            float y = activate(v + (a.bias ? a.bias[n] : 0.0f), a.act);
-            if (a.residual)
-                y += to_f32(((const TO*)a.residual)[o]);
-            store1((TO*)a.out + o, y);
-        }
+    __syncthreads();
+    /* rows of one token together, as they are stored */
+    for (int i = threadIdx.x; i < rows_wg * T; i += 256) {
+        const int t = t0 + i / rows_wg, n = n0 + i % rows_wg;
+        if (n >= n1 || t >= a.S)
+            continue;
+        const int64_t o = (int64_t)t * a.N + n;
+        const float v = sums[n - n0][i / rows_wg];
+        float y = activate(__builtin_fmaf(v, GROUPED ? 1.0f : a.w_scale[n], a.bias ? a.bias[n] : 0.0f), a.act);
+        if (a.residual)
+            y += to_f32(((const TO*)a.residual)[o]);
+        store1((TO*)a.out + o, y);
     }
+}
+
+/* Rows of a workgroup: two or more workgroups per CU in equal shares. */
+inline int rows_per_wg(int N)
+{
+    int shares = 512;
+    while (N / shares >= 32 && shares < (1 << 20))
+        shares *= 2;
+    return max(4, min(kMaxRowsWg, (N + shares - 1) / shares));
+}
+
+template <int BITS, int T, int NU, typename TO>
+void launch_rows_nu(const LinearArgs& a, hipStream_t s)
+{
+    const int r = rows_per_wg(a.N);
+    const dim3 grid((a.N + r - 1) / r, (a.S + T - 1) / T);
+    if (a.group)
+        hipLaunchKernelGGL((linear_rows_kernel<BITS, T, NU, true, TO>), grid, dim3(256), 0, s, a, r);
+    else
+        hipLaunchKernelGGL((linear_rows_kernel<BITS, T, NU, false, TO>), grid, dim3(256), 0, s, a, r);
+}
+
+template <int BITS, int T, typename TO>
+void launch_rows_t(const LinearArgs& a, hipStream_t s)
+{
+    /* units per lane of a round: up to K = 2048, 4096 or 8192 */
+    constexpr int per = BITS == 8 ? 2 : 1;
+    const int need = (a.K / 32 + 63) / 64;
+    if (need <= 1)
+        launch_rows_nu<BITS, T, 1 * per, TO>(a, s);
+    else if (need <= 2)
+        launch_rows_nu<BITS, T, 2 * per, TO>(a, s);
+    else if (need == 3)
+        launch_rows_nu<BITS, T, 3 * per, TO>(a, s);
+    else
+        launch_rows_nu<BITS, T, 4 * per, TO>(a, s);
+}
+
+template <int BITS, typename TO>
+hipError_t launch_rows(const LinearArgs& a, hipStream_t s)
+{
+    if (a.S == 1)
+        launch_rows_t<BITS, 1, TO>(a, s);
+    else if (a.S == 2)
+        launch_rows_t<BITS, 2, TO>(a, s);
+    else
+        launch_rows_t<BITS, 4, TO>(a, s);
+    return hipGetLastError();
 }
 
 /* ---- many tokens ---------------------------------------------------------- */
@@ -622,8 +769,7 @@ hipError_t launch(const LinearArgs& a, hipStream_t s)
 {
     if (use_tiles(a.S, a.K))
         return launch_tiles<BITS, TO>(a, s);
-    hipLaunchKernelGGL((linear_rows_kernel<BITS, TO>), dim3((a.N + 3) / 4, (a.S + 3) / 4), dim3(256), 0, s, a);
-    return hipGetLastError();
+    return launch_rows<BITS, TO>(a, s);
 }
 
 template <int BITS>
