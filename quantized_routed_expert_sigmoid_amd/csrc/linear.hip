@@ -26,6 +26,8 @@ namespace {
 typedef _Float16 v2h __attribute__((ext_vector_type(2)));
 typedef _Float16 v8h __attribute__((ext_vector_type(8)));
 typedef float v16f __attribute__((ext_vector_type(16)));
+typedef int v4i __attribute__((ext_vector_type(4)));
+typedef int v16i __attribute__((ext_vector_type(16)));
 
 __device__ __forceinline__ float activate(float v, int act)
 {
@@ -306,11 +308,27 @@ __global__ __launch_bounds__(256) void linear_expand(LinearArgs a, uint8_t* xh, 
     }
 }
 
-/* Sixteen bytes per lane from memory into LDS at dst + 16 lane (dst uniform). */
+/* Sixteen bytes per lane from memory into LDS at dst + 16 lane (dst uniform).
+ * Written out because the compiler, which cannot tell the buffers apart, would
+ * wait for every such load before the next LDS read; whoever uses it waits
+ * himself (arrive_all).  M0 holds the LDS address; no other instruction of
+ * these kernels takes M0. */
 __device__ __forceinline__ void to_lds(const void* src, void* dst)
 {
-    __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)src,
-                                     (__attribute__((address_space(3))) void*)dst, 16, 0, 0);
+    const uint32_t at = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) void*)dst;
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(
+                     __builtin_amdgcn_readfirstlane(at)),
+                 "v"(src)
+                 : "memory");
+}
+
+/* Waits until at most LEFT of this wave's loads are outstanding, then for the
+ * workgroup: past it every wave's earlier loads have arrived, and every wave
+ * has left the buffer that is loaded next. */
+template <int LEFT>
+__device__ __forceinline__ void arrive_all()
+{
+    asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"(LEFT) : "memory");
 }
 
 __device__ __forceinline__ v2h as_h2(uint32_t u)
@@ -416,6 +434,40 @@ __device__ __forceinline__ void store_rows(const LinearArgs& a, int tok, int n, 
     }
 }
 
+/* A scale group's row scales for one wave: lane l loads its rows' (row n0 + l)
+ * when the group opens, in one instruction; when it closes they go through the
+ * wave's own LDS words to the lanes that hold those rows' sums. */
+template <int RR>
+struct GroupScales {
+    float mine;
+    __device__ __forceinline__ void open(const LinearArgs& a, int n0, int gpr, int g)
+    {
+        const int lane = threadIdx.x & 63;
+        mine = a.w_scale[(int64_t)min(n0 + lane % (32 * RR), a.N - 1) * gpr + min(g, gpr - 1)];
+    }
+    template <int TT, typename P, typename A>
+    __device__ __forceinline__ void close(float* words, int h, P& part, A& acc)
+    {
+        words[threadIdx.x & 63] = mine;
+        __builtin_amdgcn_wave_barrier();
+#pragma unroll
+        for (int r = 0; r < RR; ++r)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const float4 v = *(const float4*)(words + r * 32 + 8 * q + 4 * h);
+                const float s[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+#pragma unroll
+                    for (int t = 0; t < TT; ++t) {
+                        acc[r][t][4 * q + j] = __builtin_fmaf(part[r][t][4 * q + j], s[j], acc[r][t][4 * q + j]);
+                        part[r][t][4 * q + j] = 0.0f;
+                    }
+            }
+        __builtin_amdgcn_wave_barrier();
+    }
+};
+
 /* What the tile kernels share of a launch. */
 struct TileArgs {
     const uint8_t* xh;
@@ -434,15 +486,27 @@ struct TileArgs {
  * instruction stays inside one scale group.  With splits > 1 the stages are
  * shared out and linear_join adds the parts.
  */
+template <int BITS, int NT, int TT, int SPB>
+struct TileLds {
+    static constexpr int kXStep = 2 * TT * NT * 8 * kTileTok * kChunk; /* bytes of a step's activations */
+    static constexpr int kX = kXStep * SPB, kW = kTileN * (BITS / 2) * SPB * kChunk;
+    static constexpr int kStage = kX + kW;
+    /* stages in flight: as many as leave room for two workgroups in a CU's 160 KB */
+    static constexpr int kFit = 80 * 1024 / kStage;
+    static constexpr int kStages = kFit < 2 ? 2 : kFit > 4 ? 4 : kFit;
+    /* loads of a wave and stage; where the weights are fewer runs than waves,
+     * waves load the same one, so that every wave counts alike */
+    static constexpr int kLoads = kX / 4096 + (kW + 4095) / 4096;
+};
+
 template <int BITS, int NT, int TT, int SPB, bool GROUPED, typename TO>
 __global__ __launch_bounds__(256, 2) void linear_tiles(LinearArgs a, TileArgs ta)
 {
-    constexpr int XS = 2 * TT * NT * 8 * kTileTok * kChunk; /* bytes of a step's activations */
-    constexpr int XB = XS * SPB;
+    using L = TileLds<BITS, NT, TT, SPB>;
+    constexpr int XS = L::kXStep, XB = L::kX, STAGES = L::kStages;
     constexpr int CPS = BITS / 2;   /* 16-byte chunks of a row's step */
     constexpr int LPR = CPS * SPB;  /* and of its stage */
-    constexpr int WB = kTileN * LPR * kChunk;
-    constexpr int kWRuns = WB / 1024;
+    constexpr int kWRuns = L::kW / 1024;
     extern __shared__ __align__(1024) uint8_t lds[];
     const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6, h = lane >> 5, col = lane & 31;
     const int wn = wv & 1, wt = wv >> 1;
@@ -467,7 +531,9 @@ __global__ __launch_bounds__(256, 2) void linear_tiles(LinearArgs a, TileArgs ta
     constexpr int RPB = LPR >= 16 ? 1 : 16 / LPR;
     auto swz = [](int n) { return n / RPB % LPR; };
 
-    auto fetch = [&](int stage, uint8_t* buf) {
+    auto fetch = [&](int stage) {
+        uint8_t* buf = lds + (stage - s0) % STAGES * L::kStage;
+        stage = min(stage, ta.stages - 1); /* past the end: loaded and not used */
         const uint8_t* x = ta.xh + ((int64_t)stage * SPB * ta.tiles + at.tile0) * (NT * 8 * kTileTok * kChunk);
         const int64_t x_step = (int64_t)ta.tiles * (NT * 8 * kTileTok * kChunk);
 #pragma unroll
@@ -479,9 +545,7 @@ __global__ __launch_bounds__(256, 2) void linear_tiles(LinearArgs a, TileArgs ta
             }
 #pragma unroll
         for (int i = 0; i < (kWRuns + 3) / 4; ++i) {
-            const int run = i * 4 + wv;
-            if (kWRuns % 4 && run >= kWRuns)
-                break;
+            const int run = (i * 4 + wv) % kWRuns;
             const int slot = run * 64 + lane, n = slot / LPR, c = slot % LPR ^ swz(n);
             const int64_t kb = (int64_t)min((stage * SPB + c / CPS) * kKB, a.K - kKB) * BITS / 8;
             to_lds(w + min(nw0 + n, a.N - 1) * row_bytes + kb + c % CPS * kChunk, buf + XB + run * 1024);
@@ -502,35 +566,21 @@ __global__ __launch_bounds__(256, 2) void linear_tiles(LinearArgs a, TileArgs ta
             }
 
     const int gpr = GROUPED ? a.K / a.group : 1;
-    /* part *= scales of group g, added to acc */
-    auto fold = [&](int g) {
-        if constexpr (GROUPED) {
-#pragma unroll
-            for (int r = 0; r < 2; ++r)
-#pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    const int n = min(at.n0 + r * 32 + 8 * (i / 4) + 4 * h + i % 4, a.N - 1);
-                    const float s = a.w_scale[(int64_t)n * gpr + g];
-#pragma unroll
-                    for (int t = 0; t < TT; ++t) {
-                        acc[r][t][i] = __builtin_fmaf(part[r][t][i], s, acc[r][t][i]);
-                        part[r][t][i] = 0.0f;
-                    }
-                }
-        }
-    };
+    __shared__ float scale_words[GROUPED ? 4 : 1][64];
+    GroupScales<2> scales;
     auto group_of = [&](int step, int i) { return (min(step * kKB, a.K - kKB) + 16 * i) / a.group; };
 
     int g = GROUPED ? group_of(s0 * SPB, 0) : 0;
-    if (s0 < s1)
-        fetch(s0, lds);
+    if constexpr (GROUPED)
+        scales.open(a, at.n0, gpr, g);
+#pragma unroll
+    for (int i = 0; i < STAGES - 1; ++i)
+        fetch(s0 + i);
     for (int stage = s0; stage < s1; ++stage) {
-        /* past the barrier this stage's loads have arrived in every wave, and every
-         * wave has left the buffer that is loaded next */
-        __syncthreads();
-        if (stage + 1 < s1)
-            fetch(stage + 1, lds + ((stage - s0 + 1) & 1) * (XB + WB));
-        const uint8_t* buf = lds + ((stage - s0) & 1) * (XB + WB);
+        /* all but the loads of the STAGES - 2 stages behind this one */
+        arrive_all<L::kLoads*(STAGES - 2)>();
+        fetch(stage + STAGES - 1);
+        const uint8_t* buf = lds + (stage - s0) % STAGES * L::kStage;
         /* Instruction i multiplies what was read two and unpacked one
          * instruction ago, so that reads and unpacking run in the shadow of the
          * matrix cores. */
@@ -581,8 +631,9 @@ __global__ __launch_bounds__(256, 2) void linear_tiles(LinearArgs a, TileArgs ta
                 if (!(i & 1)) {
                     const int now = group_of(stage * SPB + (i >> 2), i & 3);
                     if (now > g) {
-                        fold(g);
+                        scales.template close<TT>(scale_words[wv], h, part, acc);
                         g = now;
+                        scales.open(a, at.n0, gpr, g);
                     }
                 }
             }
@@ -610,8 +661,10 @@ __global__ __launch_bounds__(256, 2) void linear_tiles(LinearArgs a, TileArgs ta
             __builtin_amdgcn_sched_barrier(0);
         }
     }
-    fold(g);
+    if constexpr (GROUPED)
+        scales.template close<TT>(scale_words[wv], h, part, acc);
 
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); /* no load outlives the workgroup's LDS */
     if (ta.splits == 1) {
         float v[2][TT][16], xscale[TT];
 #pragma unroll
@@ -648,32 +701,328 @@ __global__ __launch_bounds__(256, 2) void linear_tiles(LinearArgs a, TileArgs ta
                     make_float4(acc[r][t][4 * i], acc[r][t][4 * i + 1], acc[r][t][4 * i + 2], acc[r][t][4 * i + 3]);
 }
 
+/*
+ * The same product on the int8 matrix cores, exact up to the fp32 fold: one
+ * v_mfma_i32_32x32x32_i8 is one 32-element block of 32 rows x 32 tokens, its
+ * result times the token's scale is added in fp32 (with group scales, into the
+ * group's sum).  A wave takes 32 RR rows x 32 TT tokens, the workgroup's four
+ * waves WN x 4 / WN of these, in stages of four blocks; weights and codes
+ * travel packed from memory to LDS one stage ahead.  Codes of fewer bits are
+ * unpacked to the top of their bytes, 2^(8 - bits) times their value, which
+ * the row's scale takes out again.
+ */
+#ifndef MIDT
+#define MIDT 512
+#endif
+#ifndef WANTF
+#define WANTF 512
+#endif
+#ifndef FOLDST
+#define FOLDST 4
+#endif
+constexpr int kStageK = 128;
+
+/* A lane's sixteen codes of a block as they lie in LDS, and as int8. */
+template <int BITS>
+struct RawCodes {
+    uint32_t w[BITS / 2];
+};
+
+template <int BITS>
+__device__ __forceinline__ RawCodes<BITS> read_codes(const uint8_t* p, int half, int h)
+{
+    RawCodes<BITS> r;
+    if constexpr (BITS == 8) {
+        const uint4 v = *(const uint4*)p;
+        r.w[0] = v.x;
+        r.w[1] = v.y;
+        r.w[2] = v.z;
+        r.w[3] = v.w;
+    } else if constexpr (BITS == 4) {
+        const uint2 v = *(const uint2*)(p + h * 8);
+        r.w[0] = v.x;
+        r.w[1] = v.y;
+    } else {
+        r.w[0] = *(const uint32_t*)(p + half * 8 + h * 4);
+    }
+    return r;
+}
+
+template <int BITS>
+__device__ __forceinline__ v4i codes_i8(const RawCodes<BITS>& r)
+{
+    if constexpr (BITS == 8) {
+        return v4i{(int)r.w[0], (int)r.w[1], (int)r.w[2], (int)r.w[3]};
+    } else if constexpr (BITS == 4) {
+        const uint32_t e0 = r.w[0] & 0xF0F0F0F0u, o0 = (r.w[0] << 4) & 0xF0F0F0F0u;
+        const uint32_t e1 = r.w[1] & 0xF0F0F0F0u, o1 = (r.w[1] << 4) & 0xF0F0F0F0u;
+        return v4i{(int)__builtin_amdgcn_perm(o0, e0, 0x05010400u), (int)__builtin_amdgcn_perm(o0, e0, 0x07030602u),
+                   (int)__builtin_amdgcn_perm(o1, e1, 0x05010400u), (int)__builtin_amdgcn_perm(o1, e1, 0x07030602u)};
+    } else {
+        /* byte j of the word holds elements 4 j .. 4 j + 3, the first in bits 7..6 */
+        const uint32_t w = r.w[0];
+        const uint32_t a = w & 0xC0C0C0C0u, b = (w << 2) & 0xC0C0C0C0u, c = (w << 4) & 0xC0C0C0C0u,
+                       d = (w << 6) & 0xC0C0C0C0u;
+        const uint32_t ab0 = __builtin_amdgcn_perm(b, a, 0x05010400u), ab1 = __builtin_amdgcn_perm(b, a, 0x07030602u);
+        const uint32_t cd0 = __builtin_amdgcn_perm(d, c, 0x05010400u), cd1 = __builtin_amdgcn_perm(d, c, 0x07030602u);
+        return v4i{(int)__builtin_amdgcn_perm(cd0, ab0, 0x05040100u), (int)__builtin_amdgcn_perm(cd0, ab0, 0x07060302u),
+                   (int)__builtin_amdgcn_perm(cd1, ab1, 0x05040100u), (int)__builtin_amdgcn_perm(cd1, ab1, 0x07060302u)};
+    }
+}
+
+template <int RR, int TT, int WN>
+struct FoldShape {
+    static constexpr int kRows = 32 * RR * WN, kTok = 32 * TT * (4 / WN);
+};
+
+template <int RR, int TT, int WN>
+__device__ __forceinline__ TileAt fold_at(int id, int n_tiles, int t_tiles, int wv)
+{
+    using F = FoldShape<RR, TT, WN>;
+    constexpr int GT = 8;
+    const int band = id / (GT * n_tiles), in = id % (GT * n_tiles), wide = min(GT, t_tiles - band * GT);
+    TileAt t;
+    t.n0 = in / wide * F::kRows + wv % WN * 32 * RR;
+    t.tile0 = 0;
+    t.tok0 = (band * GT + in % wide) * F::kTok + wv / WN * 32 * TT;
+    return t;
+}
+
+/* LDS of a stage: codes, weights, scales; and the stages in flight, as many as
+ * leave room for two workgroups in a CU's 160 KB. */
+template <int BITS, int RR, int TT, int WN>
+struct FoldLds {
+    using F = FoldShape<RR, TT, WN>;
+    static constexpr int kX = F::kTok * kStageK, kW = F::kRows * kStageK * BITS / 8;
+    static constexpr int kRunsD = (F::kTok * kChunk + 1023) / 1024;
+    static constexpr int kStage = kX + kW + kRunsD * 1024;
+    static constexpr int kFit = 79 * 1024 / kStage;
+    static constexpr int kStages = kFit < 2 ? 2 : kFit > FOLDST ? FOLDST : kFit;
+    /* loads of a wave and stage; where there are fewer runs than waves, waves
+     * load the same one, so that every wave counts alike */
+    static constexpr int kLoads = kX / 4096 + (kW + 4095) / 4096 + 1;
+};
+
+template <int BITS, int RR, int TT, int WN, bool GROUPED, typename TO>
+__global__ __launch_bounds__(256, 2) void linear_fold(LinearArgs a, TileArgs ta)
+{
+    constexpr int XC = kStageK / kChunk;       /* chunks of a token's stage */
+    constexpr int WC = kStageK * BITS / 128;   /* chunks of a row's stage: 8, 4, 2 */
+    using L = FoldLds<BITS, RR, TT, WN>;
+    constexpr int XB = L::kX, WB = L::kW, STAGES = L::kStages;
+    extern __shared__ __align__(1024) uint8_t lds[];
+    const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6, h = lane >> 5, col = lane & 31;
+
+    const int per = (int)gridDim.x >> 3, total = ta.n_tiles * ta.t_tiles;
+    const int unit = (int)(blockIdx.x & 7) * per + (int)(blockIdx.x >> 3);
+    if (unit >= total * ta.splits)
+        return;
+    const int id = unit / ta.splits, split = unit % ta.splits;
+    const TileAt at = fold_at<RR, TT, WN>(id, ta.n_tiles, ta.t_tiles, wv);
+    const int nw0 = at.n0 - wv % WN * 32 * RR, tw0 = at.tok0 - wv / WN * 32 * TT;
+    const int share = (ta.stages + ta.splits - 1) / ta.splits;
+    const int s0 = split * share, s1 = min(s0 + share, ta.stages);
+    const int nb = a.K / 32;
+    const int64_t row_bytes = (int64_t)a.K * BITS / 8;
+
+    /* Slot s of a token's or row's chunks holds chunk s ^ f, so that 16 of them
+     * read at one chunk fall into different banks.  Chunks past the row's end
+     * are its last one: their blocks' scales are taken as 0. */
+    auto xswz = [](int t) { return t / 2 % 8; };
+    auto wswz = [](int n) { return n / (16 / WC) % WC; };
+    auto fetch = [&](int stage) {
+        uint8_t* buf = lds + (stage - s0) % STAGES * L::kStage;
+        stage = min(stage, ta.stages - 1); /* past the end: loaded and not used */
+#pragma unroll
+        for (int i = 0; i < XB / 4096; ++i) {
+            const int slot = (i * 4 + wv) * 64 + lane, t = slot / XC, c = slot % XC ^ xswz(t);
+            const int k = min(stage * kStageK + c * kChunk, a.K - kChunk);
+            to_lds(a.xq + (int64_t)min(tw0 + t, a.S - 1) * a.K + k, buf + (i * 4 + wv) * 1024);
+        }
+#pragma unroll
+        for (int i = 0; i < (WB + 4095) / 4096; ++i) {
+            const int run = (i * 4 + wv) % (WB / 1024);
+            const int slot = run * 64 + lane, n = slot / WC, c = slot % WC ^ wswz(n);
+            const int64_t o = min((int64_t)(stage * WC + c) * kChunk, row_bytes - kChunk);
+            to_lds((const uint8_t*)a.w + min(nw0 + n, a.N - 1) * row_bytes + o, buf + XB + run * 1024);
+        }
+        /* the four scales of each token's stage, at a row's end its last four */
+        const int run = wv % L::kRunsD;
+        to_lds(a.xd + (int64_t)min(tw0 + run * 64 + lane, a.S - 1) * nb + min(stage * 4, nb - 4),
+               buf + XB + WB + run * 1024);
+    };
+
+    float acc[RR][TT][16], part[GROUPED ? RR : 1][GROUPED ? TT : 1][16];
+#pragma unroll
+    for (int r = 0; r < RR; ++r)
+#pragma unroll
+        for (int t = 0; t < TT; ++t)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                acc[r][t][i] = 0.0f;
+                if constexpr (GROUPED)
+                    part[r][t][i] = 0.0f;
+            }
+    const int gpr = GROUPED ? a.K / a.group : 1, gb = GROUPED ? a.group / 32 : 1;
+    __shared__ float scale_words[GROUPED ? 4 : 1][64];
+    GroupScales<RR> scales;
+    int g = s0 * 4 / gb;
+    if constexpr (GROUPED)
+        scales.open(a, at.n0, gpr, g);
+#pragma unroll
+    for (int i = 0; i < STAGES - 1; ++i)
+        fetch(s0 + i);
+    for (int stage = s0; stage < s1; ++stage) {
+        /* all but the loads of the STAGES - 2 stages behind this one */
+        arrive_all<L::kLoads*(STAGES - 2)>();
+        fetch(stage + STAGES - 1);
+        const uint8_t* buf = lds + (stage - s0) % STAGES * L::kStage;
+        float d[TT][4];
+#pragma unroll
+        for (int t = 0; t < TT; ++t) {
+            const float4 v = *(const float4*)(buf + XB + WB + (at.tok0 - tw0 + t * 32 + col) * kChunk);
+            const float e[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int b = 0; b < 4; ++b)
+                d[t][b] = e[b];
+            const int over = stage * 4 + 4 - nb; /* blocks of the last stage past the row's end */
+            if (over > 0) {
+#pragma unroll
+                for (int b = 0; b < 4; ++b)
+                    d[t][b] = b + over < 4 ? e[b + over < 4 ? b + over : 3] : 0.0f;
+            }
+        }
+        /* the whole stage's operands are read ahead of its products */
+        RawCodes<BITS> wr[4][RR];
+        v4i xf[4][TT];
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+#pragma unroll
+            for (int r = 0; r < RR; ++r) {
+                const int n = at.n0 - nw0 + r * 32 + col;
+                const int c = BITS == 8 ? 2 * b + h : BITS == 4 ? b : b / 2;
+                /* an odd last block of an int2 row was loaded with the block before it */
+                const int half = BITS == 2 && stage * 4 + b == nb - 1 && (nb & 1) ? 1 : b & 1;
+                wr[b][r] = read_codes<BITS>(buf + XB + (n * WC + (c ^ wswz(n))) * kChunk, half, h);
+            }
+#pragma unroll
+            for (int t = 0; t < TT; ++t) {
+                const int tok = at.tok0 - tw0 + t * 32 + col;
+                xf[b][t] = *(const v4i*)(buf + (tok * XC + ((2 * b + h) ^ xswz(tok))) * kChunk);
+            }
+        }
+        __builtin_amdgcn_sched_barrier(0);
+        /* the product of one tile runs under the fold of the one before it */
+        v16i z[2];
+        auto fold = [&](int m) {
+            const int b2 = m / (RR * TT), r = m / TT % RR, t = m % TT;
+            float* o = GROUPED ? part[GROUPED ? r : 0][GROUPED ? t : 0] : acc[r][t];
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                o[i] = __builtin_fmaf((float)z[m & 1][i], d[t][b2], o[i]);
+        };
+        v4i wf[RR];
+#pragma unroll
+        for (int m = 0; m < 4 * RR * TT; ++m) {
+            const int b = m / (RR * TT), r = m / TT % RR, t = m % TT;
+            if (t == 0)
+                wf[r] = codes_i8<BITS>(wr[b][r]);
+            const v16i zero = {0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0};
+            z[m & 1] = __builtin_amdgcn_mfma_i32_32x32x32_i8(wf[r], xf[b][t], zero, 0, 0, 0);
+            __builtin_amdgcn_sched_barrier(0);
+            if (m)
+                fold(m - 1);
+            if constexpr (GROUPED) {
+                /* every fold of the blocks before this one is done */
+                if (m % (RR * TT) == 0) {
+                    const int now = min(stage * 4 + b, nb - 1) / gb;
+                    if (now > g) {
+                        scales.template close<TT>(scale_words[wv], h, part, acc);
+                        g = now;
+                        scales.open(a, at.n0, gpr, g);
+                    }
+                }
+            }
+        }
+        fold(4 * RR * TT - 1);
+    }
+    if constexpr (GROUPED)
+        scales.template close<TT>(scale_words[wv], h, part, acc);
+
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); /* no load outlives the workgroup's LDS */
+    constexpr float unit_w = 1.0f / (float)(1 << (8 - BITS));
+    if (ta.splits == 1) {
+#pragma unroll
+        for (int r = 0; r < RR; ++r)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                const int n = min(at.n0 + r * 32 + 8 * (i / 4) + 4 * h + i % 4, a.N - 1);
+                const float ws = GROUPED ? unit_w : unit_w * a.w_scale[n], bias = a.bias ? a.bias[n] : 0.0f;
+#pragma unroll
+                for (int t = 0; t < TT; ++t)
+                    acc[r][t][i] = __builtin_fmaf(acc[r][t][i], ws, bias);
+            }
+        activate_all<RR * TT * 16>(&acc[0][0][0], a.act);
+#pragma unroll
+        for (int t = 0; t < TT; ++t)
+#pragma unroll
+            for (int r = 0; r < RR; ++r)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    store_rows<TO>(a, at.tok0 + t * 32 + col, at.n0 + r * 32 + 8 * i + 4 * h, &acc[r][t][4 * i]);
+        return;
+    }
+    float4* o = (float4*)ta.part + (((int64_t)split * total + id) * 4 + wv) * (RR * TT * 4 * 64) + lane;
+#pragma unroll
+    for (int r = 0; r < RR; ++r)
+#pragma unroll
+        for (int t = 0; t < TT; ++t)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                o[((r * TT + t) * 4 + i) * 64] =
+                    make_float4(acc[r][t][4 * i], acc[r][t][4 * i + 1], acc[r][t][4 * i + 2], acc[r][t][4 * i + 3]);
+}
+
 /* Adds the splits' sums in their order and finishes them: a workgroup takes
- * one of a tile's 2 TT * 4 groups of four rows, in the tile kernel's layout. */
-template <int TT, bool GROUPED, typename TO>
-__global__ __launch_bounds__(256) void linear_join(LinearArgs a, TileArgs ta)
+ * one of a tile's groups of four rows, in the tile kernel's layout. */
+template <int RR, int TT, typename AT, typename TO>
+__device__ __forceinline__ void join_splits(const LinearArgs& a, const TileArgs& ta, bool grouped, float unit, AT tile_of)
 {
     const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6, total = ta.n_tiles * ta.t_tiles;
     const int id = blockIdx.x, q = blockIdx.y, i = q & 3, t = (q >> 2) % TT, r = (q >> 2) / TT;
-    const float4* o = (const float4*)ta.part + (((int64_t)id * 4 + wv) * (2 * TT * 4) + q) * 64 + lane;
-    const int64_t step = (int64_t)total * 4 * (2 * TT * 4) * 64;
+    const float4* o = (const float4*)ta.part + (((int64_t)id * 4 + wv) * (RR * TT * 4) + q) * 64 + lane;
+    const int64_t step = (int64_t)total * 4 * (RR * TT * 4) * 64;
     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
     for (int s = 0; s < ta.splits; ++s) {
         const float4 x = o[s * step];
         v = make_float4(v.x + x.x, v.y + x.y, v.z + x.z, v.w + x.w);
     }
-    const TileAt at = tile_at<TT>(id, ta.n_tiles, ta.t_tiles, wv);
+    const TileAt at = tile_of(id, wv);
     const int tok = at.tok0 + t * kTileTok + (lane & 31), n = at.n0 + r * 32 + 8 * i + 4 * (lane >> 5);
-    const float xscale = ta.xs[min(tok, a.S - 1)];
+    const float xscale = ta.xs ? ta.xs[min(tok, a.S - 1)] : unit;
     float e[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
         const int m = min(n + j, a.N - 1);
-        e[j] = __builtin_fmaf(e[j], GROUPED ? xscale : xscale * a.w_scale[m], a.bias ? a.bias[m] : 0.0f);
+        e[j] = __builtin_fmaf(e[j], grouped ? xscale : xscale * a.w_scale[m], a.bias ? a.bias[m] : 0.0f);
     }
     activate_all<4>(e, a.act);
     store_rows<TO>(a, tok, n, e);
+}
+
+template <int TT, bool GROUPED, typename TO>
+__global__ __launch_bounds__(256) void linear_join(LinearArgs a, TileArgs ta)
+{
+    auto at = [&](int id, int wv) { return tile_at<TT>(id, ta.n_tiles, ta.t_tiles, wv); };
+    join_splits<2, TT, decltype(at), TO>(a, ta, GROUPED, 1.0f, at);
+}
+
+template <int RR, int TT, int WN, typename TO>
+__global__ __launch_bounds__(256) void linear_fold_join(LinearArgs a, TileArgs ta, float unit)
+{
+    auto at = [&](int id, int wv) { return fold_at<RR, TT, WN>(id, ta.n_tiles, ta.t_tiles, wv); };
+    join_splits<RR, TT, decltype(at), TO>(a, ta, a.group > 0, unit, at);
 }
 
 struct TilePlan {
@@ -704,12 +1053,92 @@ TilePlan tile_plan(int32_t S, int32_t N, int32_t K, int32_t group, int32_t out_t
     p.tiles = p.t_tiles * 2 * p.tt;
     p.stages = (K + kKB * p.spb - 1) / (kKB * p.spb);
     p.x_bytes = (size_t)p.stages * p.spb * p.tiles * p.terms * 8 * kTileTok * kChunk;
-    /* too few tiles for the CUs: the stages are shared out, two at least each */
+    /* tiles for half the CUs or fewer: the stages are shared out, two at least each */
     const int total = p.n_tiles * p.t_tiles;
-    p.splits = total >= kWantTiles ? 1 : max(1, min((kWantTiles + total - 1) / total, p.stages / 2));
+    p.splits = max(1, min(kWantTiles / total, p.stages / 2));
     p.part_at = (p.x_bytes + (size_t)S * 4 + 255) / 256 * 256;
     p.total = p.part_at + (p.splits > 1 ? (size_t)p.splits * total * kTileN * 64 * p.tt * 4 : 0);
     return p;
+}
+
+/* Shapes of the fold kernel: rows and tokens of a workgroup. */
+struct FoldPlan {
+    int shape, rows, toks, n_tiles, t_tiles, stages, splits;
+    size_t total;
+};
+
+FoldPlan fold_plan(int32_t S, int32_t N, int32_t K)
+{
+    FoldPlan p;
+    p.stages = (K + kStageK - 1) / kStageK;
+    auto tiles = [&](int rows, int toks) { return (int64_t)((N + rows - 1) / rows) * ((S + toks - 1) / toks); };
+    /* the largest tile that still gives every CU a workgroup, the smallest
+     * otherwise */
+    p.shape = S <= 32 ? 2 : tiles(128, 128) >= kWantTiles ? 0 : tiles(128, 64) >= MIDT ? 1 : 3;
+    p.rows = p.shape == 3 ? 64 : 128;
+    p.toks = p.shape == 0 ? 128 : p.shape == 2 ? 32 : 64;
+    p.n_tiles = (N + p.rows - 1) / p.rows;
+    p.t_tiles = (S + p.toks - 1) / p.toks;
+    const int total = p.n_tiles * p.t_tiles;
+    p.splits = max(1, min(WANTF / total, p.stages / 2));
+    p.total = p.splits > 1 ? (size_t)p.splits * total * p.rows * p.toks * 4 : 256;
+    return p;
+}
+
+template <int BITS, int RR, int TT, int WN, bool GROUPED, typename TO>
+hipError_t launch_fold_g(const LinearArgs& a, const FoldPlan& p, hipStream_t s)
+{
+    TileArgs ta;
+    ta.xh = nullptr;
+    ta.xs = nullptr;
+    ta.part = (float*)a.ws;
+    ta.tiles = 0;
+    ta.n_tiles = p.n_tiles;
+    ta.t_tiles = p.t_tiles;
+    ta.stages = p.stages;
+    ta.splits = p.splits;
+    constexpr int bytes = FoldLds<BITS, RR, TT, WN>::kStage * FoldLds<BITS, RR, TT, WN>::kStages;
+    if (bytes > 64 * 1024) {
+        const hipError_t e = hipFuncSetAttribute((const void*)linear_fold<BITS, RR, TT, WN, GROUPED, TO>,
+                                                 hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+        if (e != hipSuccess)
+            return e;
+    }
+    const int total = p.n_tiles * p.t_tiles;
+    hipLaunchKernelGGL((linear_fold<BITS, RR, TT, WN, GROUPED, TO>), dim3((total * p.splits + 7) / 8 * 8), dim3(256),
+                       bytes, s, a, ta);
+    if (p.splits > 1)
+        hipLaunchKernelGGL((linear_fold_join<RR, TT, WN, TO>), dim3(total, RR * TT * 4), dim3(256), 0, s, a, ta,
+                           1.0f / (float)(1 << (8 - BITS)));
+    return hipGetLastError();
+}
+
+template <int BITS, int RR, int TT, int WN, typename TO>
+hipError_t launch_fold_shape(const LinearArgs& a, const FoldPlan& p, hipStream_t s)
+{
+    return a.group ? launch_fold_g<BITS, RR, TT, WN, true, TO>(a, p, s)
+                   : launch_fold_g<BITS, RR, TT, WN, false, TO>(a, p, s);
+}
+
+template <int BITS, typename TO>
+hipError_t launch_fold(const LinearArgs& a, hipStream_t s)
+{
+    const FoldPlan p = fold_plan(a.S, a.N, a.K);
+    if (p.shape == 0)
+        return launch_fold_shape<BITS, 2, 2, 2, TO>(a, p, s);
+    if (p.shape == 1)
+        return launch_fold_shape<BITS, 2, 1, 2, TO>(a, p, s);
+    if (p.shape == 3)
+        return launch_fold_shape<BITS, 1, 1, 2, TO>(a, p, s);
+    return launch_fold_shape<BITS, 1, 1, 4, TO>(a, p, s);
+}
+
+#ifndef FOLDMAX
+#define FOLDMAX (1 << 30)
+#endif
+bool use_fold(int32_t S, int32_t K, int32_t out_type)
+{
+    return S > 4 && K >= kStageK && S <= FOLDMAX;
 }
 
 bool use_tiles(int32_t S, int32_t K)
@@ -736,7 +1165,7 @@ hipError_t launch_tiles_t(const LinearArgs& a, const TilePlan& p, hipStream_t s)
     const int per = max(1, min(8, p.tiles * steps / 512));
     hipLaunchKernelGGL((linear_expand<BITS, NT>), dim3(p.tiles, (steps + per - 1) / per), dim3(256), 0, s, a, xh, xs,
                        p.tiles, steps, per);
-    constexpr int bytes = 2 * SPB * (2 * TT * NT * 8 * kTileTok * kChunk + kTileN * (BITS / 2) * kChunk);
+    constexpr int bytes = TileLds<BITS, NT, TT, SPB>::kStage * TileLds<BITS, NT, TT, SPB>::kStages;
     const auto kernel = linear_tiles<BITS, NT, TT, SPB, GROUPED, TO>;
     if (bytes > 64 * 1024) {
         const hipError_t e =
@@ -767,6 +1196,8 @@ hipError_t launch_tiles(const LinearArgs& a, hipStream_t s)
 template <int BITS, typename TO>
 hipError_t launch(const LinearArgs& a, hipStream_t s)
 {
+    if (use_fold(a.S, a.K, a.out_type))
+        return launch_fold<BITS, TO>(a, s);
     if (use_tiles(a.S, a.K))
         return launch_tiles<BITS, TO>(a, s);
     return launch_rows<BITS, TO>(a, s);
@@ -782,7 +1213,8 @@ hipError_t launch_type(const LinearArgs& a, hipStream_t s)
 
 size_t linear_workspace_bytes(int32_t S, int32_t N, int32_t K, int32_t qtype, int32_t group, int32_t out_type)
 {
-    return use_tiles(S, K) ? tile_plan(S, N, K, group, out_type).total : 256;
+    return use_fold(S, K, out_type) ? fold_plan(S, N, K).total
+           : use_tiles(S, K)        ? tile_plan(S, N, K, group, out_type).total : 256;
 }
 
 hipError_t launch_linear_q(const LinearArgs& a, hipStream_t s)
