@@ -1,21 +1,22 @@
 /*
  * linear.hip -- quantised matrix product of Q8_0 activations with bias,
- * activation and residual in its epilogue.
+ * activation and residual in its epilogue:
  *
- * Few tokens (linear_rows_kernel): exact integer dot products of weight and
- * activation codes inside a 32-element block, times the two scales, summed in
- * fp32 first in the lane and then over the wave.
+ *   out[t][n] = act(sum_b s(n, b) d(t, b) sum_(k in b) w[n][k] q[t][k] + bias[n]) + residual[t][n]
  *
- * Many tokens: linear_expand writes the activations once as fp16 and
- * linear_tiles runs the product on the fp16 matrix cores.  A weight code is
- * exact in fp16, so the matrix cores sum code * x in fp32 over a whole row (or
- * a group of one scale) with nothing to fold per 32-element block: the
- * per-block form on the int8 cores needs a conversion and an fma per block and
- * output, 32 VALU cycles beside 19 of the matrix core.  x = code * d is scaled
- * per token by a power of two so that its largest value lies in [2^14, 2^15)
- * and rounded to fp16 (2^-12 of each value) for bf16 outputs, an eighth of the
- * output's own rounding; for fp32 outputs a second fp16 term takes the
- * remainder (2^-22).
+ * over 32-element blocks b, w and q small integers.  Three forms:
+ *
+ * - linear_rows_kernel, up to four tokens: the weights are read once and
+ *   nothing else matters, so integer dot products on the VALU keep up.
+ * - linear_fold, more tokens: the int8 matrix cores form the block products
+ *   exactly, the VALU adds them in fp32 (a conversion and an fma per block and
+ *   output, which bounds it: 32 VALU instructions, 128 cycles, beside 32 of the
+ *   matrix core per 32 x 32 x 32 block).
+ * - linear_tiles, bf16 outputs of very many tokens with one scale per row: the
+ *   activations are written once as fp16 (linear_expand) and the fp16 matrix
+ *   cores sum a whole row in fp32 with nothing to fold.  x = q d is scaled per
+ *   token by a power of two and rounded to fp16, 2^-12 of each value, an eighth
+ *   of what the output's own rounding to bf16 takes; a weight code is exact.
  */
 #include "block_device.h"
 
@@ -248,13 +249,13 @@ __device__ __forceinline__ int k_order(int i)
 }
 
 /*
- * Activations as fp16 operands: [step][tile of 32 tokens][term][chunk of 8 k][token] of 16 bytes, so that
+ * Activations as fp16 operands: [step][tile of 32 tokens][chunk of 8 k][token] of 16 bytes, so that
  * a wave's operand load is one run of 1 KB.  Steps past the row's end cover k = K - 64 .. K - 1; what an
  * earlier step has covered already is zero in them, as are tokens from S on.  A workgroup takes a tile of 32 tokens and
  * per steps: eight threads find a token's largest scale, then 32 threads write the tokens of one
  * chunk as a run of 512 bytes.
  */
-template <int BITS, int NT>
+template <int BITS>
 __global__ __launch_bounds__(256) void linear_expand(LinearArgs a, uint8_t* xh, float* xs, int tiles, int steps, int per)
 {
     __shared__ float up_of[kTileTok];
@@ -290,21 +291,13 @@ __global__ __launch_bounds__(256) void linear_expand(LinearArgs a, uint8_t* xh, 
         const int at = min(step * kKB, a.K - kKB) + c * 8;
         const uint2 w = *(const uint2*)(q + at);
         const float s = at >= step * kKB ? d[at >> 5] * up : 0.0f;
-        v8h hi, lo;
+        v8h x;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             const int k = k_order<BITS>(i);
-            float x = (float)(int8_t)((k < 4 ? w.x : w.y) >> (8 * (k & 3))) * s;
-            /* pinned: the compiler may otherwise take hi from the unrounded
-             * product in one of its two uses, and a tie both ways */
-            asm("" : "+v"(x));
-            hi[i] = (_Float16)x;
-            lo[i] = (_Float16)(x - (float)hi[i]);
+            x[i] = (_Float16)((float)(int8_t)((k < 4 ? w.x : w.y) >> (8 * (k & 3))) * s);
         }
-        uint8_t* o = xh + ((((int64_t)step * tiles + tile) * NT * 8 + c) * kTileTok + (threadIdx.x & 31)) * kChunk;
-        *(v8h*)o = hi;
-        if constexpr (NT == 2)
-            *(v8h*)(o + 8 * kTileTok * kChunk) = lo;
+        *(v8h*)(xh + ((((int64_t)step * tiles + tile) * 8 + c) * kTileTok + (threadIdx.x & 31)) * kChunk) = x;
     }
 }
 
@@ -374,24 +367,29 @@ __device__ __forceinline__ v8h codes_f16(uint32_t w0, uint32_t w1)
     return v;
 }
 
-/* Where a workgroup's tile lies, and a wave's part of it: rows n0 + 32 r,
- * r < 2, tokens tok0 + 32 t, t < TT; lane (col, h) of a tile holds the token
- * col and the rows 8 (i / 4) + 4 h + i % 4 of accumulator register i. */
+/* Where a wave's part of a tile lies: rows n0 + 32 r, tokens tok0 + 32 t; lane
+ * (col = l % 32, h = l / 32) of a 32 x 32 part holds token col and the rows 8 (i
+ * / 4) + 4 h + i % 4 of accumulator register i. */
 struct TileAt {
-    int n0, tok0, tile0; /* tile0: the workgroup's first tile of 32 tokens */
+    int n0, tok0;
 };
 
-template <int TT>
-__device__ __forceinline__ TileAt tile_at(int id, int n_tiles, int t_tiles, int wv)
+/* Tile id of a grid of n_tiles x t_tiles tiles of ROWS rows x TOKS tokens: bands
+ * of eight token tiles, column by column of weight tiles, so that neighbours
+ * share operands. */
+template <int ROWS, int TOKS>
+__device__ __forceinline__ TileAt tile_at(int id, int n_tiles, int t_tiles)
 {
-    /* bands of eight token tiles, column by column of weight tiles */
     constexpr int GT = 8;
     const int band = id / (GT * n_tiles), in = id % (GT * n_tiles), wide = min(GT, t_tiles - band * GT);
-    TileAt t;
-    t.n0 = in / wide * kTileN + (wv & 1) * 64;
-    t.tile0 = (band * GT + in % wide) * 2 * TT;
-    t.tok0 = (t.tile0 + (wv >> 1) * TT) * kTileTok;
-    return t;
+    return TileAt{in / wide * ROWS, (band * GT + in % wide) * TOKS};
+}
+
+/* Workgroups go to the eight XCDs in turn; each XCD takes a contiguous run of
+ * units, so that what it works on at a time shares its L2. */
+__device__ __forceinline__ int xcd_unit()
+{
+    return (int)(blockIdx.x & 7) * ((int)gridDim.x >> 3) + (int)(blockIdx.x >> 3);
 }
 
 /* One uniform branch on the activation for N values. */
@@ -468,62 +466,44 @@ struct GroupScales {
     }
 };
 
-/* What the tile kernels share of a launch. */
+/* What the tile kernels take of a launch. */
 struct TileArgs {
-    const uint8_t* xh;
+    const uint8_t* xh; /* linear_tiles: the expanded activations and their scales */
     const float* xs;
-    float* part; /* [split][tile][wave][r][t][i / 4][lane] of four sums, or null */
+    float* part; /* linear_fold: [split][tile][wave][r][t][i / 4][lane] of four sums */
     int tiles, n_tiles, t_tiles, stages, splits;
 };
 
 /*
- * A workgroup of 2 x 2 waves takes 128 weight rows x 64 TT tokens, a wave 64
- * rows x 32 TT tokens of them (2 x TT tiles of v_mfma_f32_32x32x16_f16), in
- * stages of SPB steps of 64 k: the next stage's operands travel from memory to
- * LDS under this stage's products.  Weights stay packed in LDS and are
- * unpacked by the waves that multiply them.  Lane (l % 32, h = l / 32) of
- * instruction i of a step takes k = 16 i + 8 h .. + 7 of the step, so that one
- * instruction stays inside one scale group.  With splits > 1 the stages are
- * shared out and linear_join adds the parts.
+ * A workgroup of 2 x 2 waves takes 128 weight rows x 256 tokens, a wave 64 rows
+ * x 128 tokens of them (2 x 4 tiles of v_mfma_f32_32x32x16_f16), in steps of 64
+ * k: the next step's operands travel from memory to LDS under this step's
+ * products, 36 KB of an int4 step, so that two workgroups share a CU.  Weights
+ * stay packed in LDS and are unpacked by the waves that multiply them.  Lane
+ * (l % 32, h = l / 32) of instruction i of a step takes k = 16 i + 8 h .. + 7.
  */
-template <int BITS, int NT, int TT, int SPB>
+constexpr int kTileTT = 4;
+
+template <int BITS>
 struct TileLds {
-    static constexpr int kXStep = 2 * TT * NT * 8 * kTileTok * kChunk; /* bytes of a step's activations */
-    static constexpr int kX = kXStep * SPB, kW = kTileN * (BITS / 2) * SPB * kChunk;
+    static constexpr int kX = 2 * kTileTT * 8 * kTileTok * kChunk, kW = kTileN * (BITS / 2) * kChunk;
     static constexpr int kStage = kX + kW;
-    /* stages in flight: as many as leave room for two workgroups in a CU's 160 KB */
-    static constexpr int kFit = 80 * 1024 / kStage;
-    static constexpr int kStages = kFit < 2 ? 2 : kFit > 4 ? 4 : kFit;
-    /* loads of a wave and stage; where the weights are fewer runs than waves,
-     * waves load the same one, so that every wave counts alike */
-    static constexpr int kLoads = kX / 4096 + (kW + 4095) / 4096;
 };
 
-template <int BITS, int NT, int TT, int SPB, bool GROUPED, typename TO>
+template <int BITS>
 __global__ __launch_bounds__(256, 2) void linear_tiles(LinearArgs a, TileArgs ta)
 {
-    using L = TileLds<BITS, NT, TT, SPB>;
-    constexpr int XS = L::kXStep, XB = L::kX, STAGES = L::kStages;
-    constexpr int CPS = BITS / 2;   /* 16-byte chunks of a row's step */
-    constexpr int LPR = CPS * SPB;  /* and of its stage */
+    using L = TileLds<BITS>;
+    constexpr int TT = kTileTT, XB = L::kX, LPR = BITS / 2; /* 16-byte chunks of a row's step */
     constexpr int kWRuns = L::kW / 1024;
     extern __shared__ __align__(1024) uint8_t lds[];
     const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6, h = lane >> 5, col = lane & 31;
     const int wn = wv & 1, wt = wv >> 1;
-
-    /* Workgroups go to the eight XCDs in turn; each XCD takes a contiguous run
-     * of tiles, so that the tiles it works on at a time share operands in its
-     * L2. */
-    const int per = (int)gridDim.x >> 3, total = ta.n_tiles * ta.t_tiles;
-    const int unit = (int)(blockIdx.x & 7) * per + (int)(blockIdx.x >> 3);
-    if (unit >= total * ta.splits)
+    const int unit = xcd_unit();
+    if (unit >= ta.n_tiles * ta.t_tiles)
         return;
-    const int id = unit / ta.splits, split = unit % ta.splits;
-    const TileAt at = tile_at<TT>(id, ta.n_tiles, ta.t_tiles, wv);
-    const int nw0 = at.n0 - wn * 64; /* the workgroup's first row */
-    const int each = (ta.stages + ta.splits - 1) / ta.splits;
-    const int s0 = split * each, s1 = min(s0 + each, ta.stages);
-
+    const TileAt wg = tile_at<kTileN, 64 * TT>(unit, ta.n_tiles, ta.t_tiles);
+    const TileAt at = {wg.n0 + wn * 64, wg.tok0 + wt * TT * kTileTok};
     const int64_t row_bytes = (int64_t)a.K * BITS / 8;
     const uint8_t* w = (const uint8_t*)a.w;
     /* Chunk c of row n of a stage lies in LDS slot c ^ f(n) of the row's LPR, so
@@ -531,82 +511,62 @@ __global__ __launch_bounds__(256, 2) void linear_tiles(LinearArgs a, TileArgs ta
     constexpr int RPB = LPR >= 16 ? 1 : 16 / LPR;
     auto swz = [](int n) { return n / RPB % LPR; };
 
-    auto fetch = [&](int stage) {
-        uint8_t* buf = lds + (stage - s0) % STAGES * L::kStage;
-        stage = min(stage, ta.stages - 1); /* past the end: loaded and not used */
-        const uint8_t* x = ta.xh + ((int64_t)stage * SPB * ta.tiles + at.tile0) * (NT * 8 * kTileTok * kChunk);
-        const int64_t x_step = (int64_t)ta.tiles * (NT * 8 * kTileTok * kChunk);
+    auto fetch = [&](int step) {
+        uint8_t* buf = lds + (step & 1) * L::kStage;
+        step = min(step, ta.stages - 1); /* past the end: loaded and not used */
+        const uint8_t* x = ta.xh + ((int64_t)step * ta.tiles + wg.tok0 / kTileTok) * (8 * kTileTok * kChunk);
 #pragma unroll
-        for (int j = 0; j < SPB; ++j)
-#pragma unroll
-            for (int i = 0; i < XS / 4096; ++i) {
-                const int o = (i * 4 + wv) * 1024;
-                to_lds(x + j * x_step + o + lane * 16, buf + j * XS + o);
-            }
+        for (int i = 0; i < XB / 4096; ++i) {
+            const int o = (i * 4 + wv) * 1024;
+            to_lds(x + o + lane * 16, buf + o);
+        }
+        const int64_t kb = (int64_t)min(step * kKB, a.K - kKB) * BITS / 8;
+        /* where the weights are fewer runs than waves, waves load the same one */
 #pragma unroll
         for (int i = 0; i < (kWRuns + 3) / 4; ++i) {
             const int run = (i * 4 + wv) % kWRuns;
             const int slot = run * 64 + lane, n = slot / LPR, c = slot % LPR ^ swz(n);
-            const int64_t kb = (int64_t)min((stage * SPB + c / CPS) * kKB, a.K - kKB) * BITS / 8;
-            to_lds(w + min(nw0 + n, a.N - 1) * row_bytes + kb + c % CPS * kChunk, buf + XB + run * 1024);
+            to_lds(w + min(wg.n0 + n, a.N - 1) * row_bytes + kb + c * kChunk, buf + XB + run * 1024);
         }
     };
 
     v16f acc[2][TT];
-    v16f part[GROUPED ? 2 : 1][GROUPED ? TT : 1];
 #pragma unroll
     for (int r = 0; r < 2; ++r)
 #pragma unroll
         for (int t = 0; t < TT; ++t)
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
+            for (int i = 0; i < 16; ++i)
                 acc[r][t][i] = 0.0f;
-                if constexpr (GROUPED)
-                    part[r][t][i] = 0.0f;
-            }
 
-    const int gpr = GROUPED ? a.K / a.group : 1;
-    __shared__ float scale_words[GROUPED ? 4 : 1][64];
-    GroupScales<2> scales;
-    auto group_of = [&](int step, int i) { return (min(step * kKB, a.K - kKB) + 16 * i) / a.group; };
-
-    int g = GROUPED ? group_of(s0 * SPB, 0) : 0;
-    if constexpr (GROUPED)
-        scales.open(a, at.n0, gpr, g);
-#pragma unroll
-    for (int i = 0; i < STAGES - 1; ++i)
-        fetch(s0 + i);
-    for (int stage = s0; stage < s1; ++stage) {
-        /* all but the loads of the STAGES - 2 stages behind this one */
-        arrive_all<L::kLoads*(STAGES - 2)>();
-        fetch(stage + STAGES - 1);
-        const uint8_t* buf = lds + (stage - s0) % STAGES * L::kStage;
+    fetch(0);
+    for (int step = 0; step < ta.stages; ++step) {
+        arrive_all<0>();
+        fetch(step + 1);
+        const uint8_t* buf = lds + (step & 1) * L::kStage;
         /* Instruction i multiplies what was read two and unpacked one
          * instruction ago, so that reads and unpacking run in the shadow of the
          * matrix cores. */
-        constexpr int I = 4 * SPB;
         uint2 wraw[2][2];
-        v8h xf[2][TT * NT], wf[2][2];
+        v8h xf[2][TT], wf[2][2];
         auto read_w = [&](int i) {
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
                 const int n = wn * 64 + r * 32 + col;
                 const uint8_t* p = buf + XB + n * (LPR * kChunk);
-                const int k = i & 3;
-                auto slot = [&](int c) { return ((i >> 2) * CPS + c ^ swz(n)) * kChunk; };
+                auto slot = [&](int c) { return (c ^ swz(n)) * kChunk; };
                 if constexpr (BITS == 8)
-                    wraw[i & 1][r] = *(const uint2*)(p + slot(k) + h * 8);
+                    wraw[i & 1][r] = *(const uint2*)(p + slot(i) + h * 8);
                 else if constexpr (BITS == 4)
-                    wraw[i & 1][r].x = *(const uint32_t*)(p + slot(k >> 1) + (k & 1) * 8 + h * 4);
+                    wraw[i & 1][r].x = *(const uint32_t*)(p + slot(i >> 1) + (i & 1) * 8 + h * 4);
                 else
-                    wraw[i & 1][r].x = *(const uint32_t*)(p + slot(0) + k * 4);
+                    wraw[i & 1][r].x = *(const uint32_t*)(p + slot(0) + i * 4);
             }
         };
         auto read_x = [&](int i) {
 #pragma unroll
-            for (int t = 0; t < TT * NT; ++t)
-                xf[i & 1][t] = *(const v8h*)(buf + (i >> 2) * XS +
-                                             ((wt * TT * NT + t) * 8 + 2 * (i & 3)) * (kTileTok * kChunk) + lane * 16);
+            for (int t = 0; t < TT; ++t)
+                xf[i & 1][t] = *(const v8h*)(buf + ((wt * TT + t) * 8 + 2 * i) * (kTileTok * kChunk) + lane * 16);
         };
         auto unpack = [&](int i) {
 #pragma unroll
@@ -624,36 +584,20 @@ __global__ __launch_bounds__(256, 2) void linear_tiles(LinearArgs a, TileArgs ta
         unpack(0);
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-        for (int i = 0; i < I; ++i) {
-            if constexpr (GROUPED) {
-                /* the last step may start in an earlier group than the one before
-                 * ended in: its activations there are zero */
-                if (!(i & 1)) {
-                    const int now = group_of(stage * SPB + (i >> 2), i & 3);
-                    if (now > g) {
-                        scales.template close<TT>(scale_words[wv], h, part, acc);
-                        g = now;
-                        scales.open(a, at.n0, gpr, g);
-                    }
-                }
-            }
-            if (i + 1 < I) {
+        for (int i = 0; i < 4; ++i) {
+            if (i + 1 < 4) {
                 read_x(i + 1);
                 unpack(i + 1);
             }
-            if (i + 2 < I)
+            if (i + 2 < 4)
                 read_w(i + 2);
 #pragma unroll
             for (int t = 0; t < TT; ++t)
 #pragma unroll
-                for (int e = 0; e < NT; ++e)
+                for (int r = 0; r < 2; ++r)
+                    acc[r][t] = __builtin_amdgcn_mfma_f32_32x32x16_f16(wf[i & 1][r], xf[i & 1][t], acc[r][t], 0, 0, 0);
 #pragma unroll
-                    for (int r = 0; r < 2; ++r) {
-                        v16f& o = GROUPED ? part[GROUPED ? r : 0][GROUPED ? t : 0] : acc[r][t];
-                        o = __builtin_amdgcn_mfma_f32_32x32x16_f16(wf[i & 1][r], xf[i & 1][t * NT + e], o, 0, 0, 0);
-                    }
-#pragma unroll
-            for (int k = 0; k < 2 * TT * NT; ++k) {
+            for (int k = 0; k < 2 * TT; ++k) {
                 __builtin_amdgcn_sched_group_barrier(0x008, 1, 0); /* a matrix instruction, */
                 __builtin_amdgcn_sched_group_barrier(0x100, 1, 0); /* an LDS read and */
                 __builtin_amdgcn_sched_group_barrier(0x002, 4, 0); /* four VALU under it */
@@ -661,44 +605,29 @@ __global__ __launch_bounds__(256, 2) void linear_tiles(LinearArgs a, TileArgs ta
             __builtin_amdgcn_sched_barrier(0);
         }
     }
-    if constexpr (GROUPED)
-        scales.template close<TT>(scale_words[wv], h, part, acc);
-
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); /* no load outlives the workgroup's LDS */
-    if (ta.splits == 1) {
-        float v[2][TT][16], xscale[TT];
+    float v[2][TT][16], xscale[TT];
 #pragma unroll
-        for (int t = 0; t < TT; ++t)
-            xscale[t] = ta.xs[min(at.tok0 + t * kTileTok + col, a.S - 1)];
-#pragma unroll
-        for (int r = 0; r < 2; ++r)
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                const int n = min(at.n0 + r * 32 + 8 * (i / 4) + 4 * h + i % 4, a.N - 1);
-                const float ws = GROUPED ? 1.0f : a.w_scale[n], bias = a.bias ? a.bias[n] : 0.0f;
-#pragma unroll
-                for (int t = 0; t < TT; ++t)
-                    v[r][t][i] = __builtin_fmaf(acc[r][t][i], xscale[t] * ws, bias);
-            }
-        activate_all<2 * TT * 16>(&v[0][0][0], a.act);
-#pragma unroll
-        for (int t = 0; t < TT; ++t)
-#pragma unroll
-            for (int r = 0; r < 2; ++r)
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    store_rows<TO>(a, at.tok0 + t * kTileTok + col, at.n0 + r * 32 + 8 * i + 4 * h, &v[r][t][4 * i]);
-        return;
-    }
-    float4* o = (float4*)ta.part + (((int64_t)split * total + id) * 4 + wv) * (2 * TT * 4 * 64) + lane;
+    for (int t = 0; t < TT; ++t)
+        xscale[t] = ta.xs[min(at.tok0 + t * kTileTok + col, a.S - 1)];
 #pragma unroll
     for (int r = 0; r < 2; ++r)
 #pragma unroll
-        for (int t = 0; t < TT; ++t)
+        for (int i = 0; i < 16; ++i) {
+            const int n = min(at.n0 + r * 32 + 8 * (i / 4) + 4 * h + i % 4, a.N - 1);
+            const float ws = a.w_scale[n], bias = a.bias ? a.bias[n] : 0.0f;
+#pragma unroll
+            for (int t = 0; t < TT; ++t)
+                v[r][t][i] = __builtin_fmaf(acc[r][t][i], xscale[t] * ws, bias);
+        }
+    activate_all<2 * TT * 16>(&v[0][0][0], a.act);
+#pragma unroll
+    for (int t = 0; t < TT; ++t)
+#pragma unroll
+        for (int r = 0; r < 2; ++r)
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                o[((r * TT + t) * 4 + i) * 64] =
-                    make_float4(acc[r][t][4 * i], acc[r][t][4 * i + 1], acc[r][t][4 * i + 2], acc[r][t][4 * i + 3]);
+                store_rows<bf16>(a, at.tok0 + t * kTileTok + col, at.n0 + r * 32 + 8 * i + 4 * h, &v[r][t][4 * i]);
 }
 
 /*
@@ -711,15 +640,6 @@ __global__ __launch_bounds__(256, 2) void linear_tiles(LinearArgs a, TileArgs ta
  * unpacked to the top of their bytes, 2^(8 - bits) times their value, which
  * the row's scale takes out again.
  */
-#ifndef MIDT
-#define MIDT 512
-#endif
-#ifndef WANTF
-#define WANTF 512
-#endif
-#ifndef FOLDST
-#define FOLDST 4
-#endif
 constexpr int kStageK = 128;
 
 /* A lane's sixteen codes of a block as they lie in LDS, and as int8. */
@@ -775,19 +695,6 @@ struct FoldShape {
     static constexpr int kRows = 32 * RR * WN, kTok = 32 * TT * (4 / WN);
 };
 
-template <int RR, int TT, int WN>
-__device__ __forceinline__ TileAt fold_at(int id, int n_tiles, int t_tiles, int wv)
-{
-    using F = FoldShape<RR, TT, WN>;
-    constexpr int GT = 8;
-    const int band = id / (GT * n_tiles), in = id % (GT * n_tiles), wide = min(GT, t_tiles - band * GT);
-    TileAt t;
-    t.n0 = in / wide * F::kRows + wv % WN * 32 * RR;
-    t.tile0 = 0;
-    t.tok0 = (band * GT + in % wide) * F::kTok + wv / WN * 32 * TT;
-    return t;
-}
-
 /* LDS of a stage: codes, weights, scales; and the stages in flight, as many as
  * leave room for two workgroups in a CU's 160 KB. */
 template <int BITS, int RR, int TT, int WN>
@@ -797,7 +704,7 @@ struct FoldLds {
     static constexpr int kRunsD = (F::kTok * kChunk + 1023) / 1024;
     static constexpr int kStage = kX + kW + kRunsD * 1024;
     static constexpr int kFit = 79 * 1024 / kStage;
-    static constexpr int kStages = kFit < 2 ? 2 : kFit > FOLDST ? FOLDST : kFit;
+    static constexpr int kStages = kFit < 2 ? 2 : kFit > 4 ? 4 : kFit;
     /* loads of a wave and stage; where there are fewer runs than waves, waves
      * load the same one, so that every wave counts alike */
     static constexpr int kLoads = kX / 4096 + (kW + 4095) / 4096 + 1;
@@ -808,18 +715,18 @@ __global__ __launch_bounds__(256, 2) void linear_fold(LinearArgs a, TileArgs ta)
 {
     constexpr int XC = kStageK / kChunk;       /* chunks of a token's stage */
     constexpr int WC = kStageK * BITS / 128;   /* chunks of a row's stage: 8, 4, 2 */
+    using F = FoldShape<RR, TT, WN>;
     using L = FoldLds<BITS, RR, TT, WN>;
     constexpr int XB = L::kX, WB = L::kW, STAGES = L::kStages;
     extern __shared__ __align__(1024) uint8_t lds[];
     const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6, h = lane >> 5, col = lane & 31;
 
-    const int per = (int)gridDim.x >> 3, total = ta.n_tiles * ta.t_tiles;
-    const int unit = (int)(blockIdx.x & 7) * per + (int)(blockIdx.x >> 3);
+    const int unit = xcd_unit(), total = ta.n_tiles * ta.t_tiles;
     if (unit >= total * ta.splits)
         return;
     const int id = unit / ta.splits, split = unit % ta.splits;
-    const TileAt at = fold_at<RR, TT, WN>(id, ta.n_tiles, ta.t_tiles, wv);
-    const int nw0 = at.n0 - wv % WN * 32 * RR, tw0 = at.tok0 - wv / WN * 32 * TT;
+    const TileAt wg = tile_at<F::kRows, F::kTok>(id, ta.n_tiles, ta.t_tiles);
+    const TileAt at = {wg.n0 + wv % WN * 32 * RR, wg.tok0 + wv / WN * 32 * TT};
     const int share = (ta.stages + ta.splits - 1) / ta.splits;
     const int s0 = split * share, s1 = min(s0 + share, ta.stages);
     const int nb = a.K / 32;
@@ -837,18 +744,18 @@ __global__ __launch_bounds__(256, 2) void linear_fold(LinearArgs a, TileArgs ta)
         for (int i = 0; i < XB / 4096; ++i) {
             const int slot = (i * 4 + wv) * 64 + lane, t = slot / XC, c = slot % XC ^ xswz(t);
             const int k = min(stage * kStageK + c * kChunk, a.K - kChunk);
-            to_lds(a.xq + (int64_t)min(tw0 + t, a.S - 1) * a.K + k, buf + (i * 4 + wv) * 1024);
+            to_lds(a.xq + (int64_t)min(wg.tok0 + t, a.S - 1) * a.K + k, buf + (i * 4 + wv) * 1024);
         }
 #pragma unroll
         for (int i = 0; i < (WB + 4095) / 4096; ++i) {
             const int run = (i * 4 + wv) % (WB / 1024);
             const int slot = run * 64 + lane, n = slot / WC, c = slot % WC ^ wswz(n);
             const int64_t o = min((int64_t)(stage * WC + c) * kChunk, row_bytes - kChunk);
-            to_lds((const uint8_t*)a.w + min(nw0 + n, a.N - 1) * row_bytes + o, buf + XB + run * 1024);
+            to_lds((const uint8_t*)a.w + min(wg.n0 + n, a.N - 1) * row_bytes + o, buf + XB + run * 1024);
         }
         /* the four scales of each token's stage, at a row's end its last four */
         const int run = wv % L::kRunsD;
-        to_lds(a.xd + (int64_t)min(tw0 + run * 64 + lane, a.S - 1) * nb + min(stage * 4, nb - 4),
+        to_lds(a.xd + (int64_t)min(wg.tok0 + run * 64 + lane, a.S - 1) * nb + min(stage * 4, nb - 4),
                buf + XB + WB + run * 1024);
     };
 
@@ -880,7 +787,7 @@ __global__ __launch_bounds__(256, 2) void linear_fold(LinearArgs a, TileArgs ta)
         float d[TT][4];
 #pragma unroll
         for (int t = 0; t < TT; ++t) {
-            const float4 v = *(const float4*)(buf + XB + WB + (at.tok0 - tw0 + t * 32 + col) * kChunk);
+            const float4 v = *(const float4*)(buf + XB + WB + (at.tok0 - wg.tok0 + t * 32 + col) * kChunk);
             const float e[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
             for (int b = 0; b < 4; ++b)
@@ -899,7 +806,7 @@ __global__ __launch_bounds__(256, 2) void linear_fold(LinearArgs a, TileArgs ta)
         for (int b = 0; b < 4; ++b) {
 #pragma unroll
             for (int r = 0; r < RR; ++r) {
-                const int n = at.n0 - nw0 + r * 32 + col;
+                const int n = at.n0 - wg.n0 + r * 32 + col;
                 const int c = BITS == 8 ? 2 * b + h : BITS == 4 ? b : b / 2;
                 /* an odd last block of an int2 row was loaded with the block before it */
                 const int half = BITS == 2 && stage * 4 + b == nb - 1 && (nb & 1) ? 1 : b & 1;
@@ -907,7 +814,7 @@ __global__ __launch_bounds__(256, 2) void linear_fold(LinearArgs a, TileArgs ta)
             }
 #pragma unroll
             for (int t = 0; t < TT; ++t) {
-                const int tok = at.tok0 - tw0 + t * 32 + col;
+                const int tok = at.tok0 - wg.tok0 + t * 32 + col;
                 xf[b][t] = *(const v4i*)(buf + (tok * XC + ((2 * b + h) ^ xswz(tok))) * kChunk);
             }
         }
@@ -984,10 +891,11 @@ __global__ __launch_bounds__(256, 2) void linear_fold(LinearArgs a, TileArgs ta)
 }
 
 /* Adds the splits' sums in their order and finishes them: a workgroup takes
- * one of a tile's groups of four rows, in the tile kernel's layout. */
-template <int RR, int TT, typename AT, typename TO>
-__device__ __forceinline__ void join_splits(const LinearArgs& a, const TileArgs& ta, bool grouped, float unit, AT tile_of)
+ * one of a tile's groups of four rows, in the fold kernel's layout. */
+template <int RR, int TT, int WN, typename TO>
+__global__ __launch_bounds__(256) void linear_join(LinearArgs a, TileArgs ta, float unit_w)
 {
+    using F = FoldShape<RR, TT, WN>;
     const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6, total = ta.n_tiles * ta.t_tiles;
     const int id = blockIdx.x, q = blockIdx.y, i = q & 3, t = (q >> 2) % TT, r = (q >> 2) / TT;
     const float4* o = (const float4*)ta.part + (((int64_t)id * 4 + wv) * (RR * TT * 4) + q) * 64 + lane;
@@ -998,89 +906,109 @@ __device__ __forceinline__ void join_splits(const LinearArgs& a, const TileArgs&
         const float4 x = o[s * step];
         v = make_float4(v.x + x.x, v.y + x.y, v.z + x.z, v.w + x.w);
     }
-    const TileAt at = tile_of(id, wv);
-    const int tok = at.tok0 + t * kTileTok + (lane & 31), n = at.n0 + r * 32 + 8 * i + 4 * (lane >> 5);
-    const float xscale = ta.xs ? ta.xs[min(tok, a.S - 1)] : unit;
+    const TileAt wg = tile_at<F::kRows, F::kTok>(id, ta.n_tiles, ta.t_tiles);
+    const int tok = wg.tok0 + wv / WN * 32 * TT + t * 32 + (lane & 31);
+    const int n = wg.n0 + wv % WN * 32 * RR + r * 32 + 8 * i + 4 * (lane >> 5);
     float e[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
         const int m = min(n + j, a.N - 1);
-        e[j] = __builtin_fmaf(e[j], grouped ? xscale : xscale * a.w_scale[m], a.bias ? a.bias[m] : 0.0f);
+        e[j] = __builtin_fmaf(e[j], a.group ? unit_w : unit_w * a.w_scale[m], a.bias ? a.bias[m] : 0.0f);
     }
     activate_all<4>(e, a.act);
     store_rows<TO>(a, tok, n, e);
 }
 
-template <int TT, bool GROUPED, typename TO>
-__global__ __launch_bounds__(256) void linear_join(LinearArgs a, TileArgs ta)
+/* ---- which form, and its shape ------------------------------------------- */
+
+int64_t n_tiles_of(int32_t S, int32_t N, int rows, int toks)
 {
-    auto at = [&](int id, int wv) { return tile_at<TT>(id, ta.n_tiles, ta.t_tiles, wv); };
-    join_splits<2, TT, decltype(at), TO>(a, ta, GROUPED, 1.0f, at);
+    return (int64_t)((N + rows - 1) / rows) * ((S + toks - 1) / toks);
 }
 
-template <int RR, int TT, int WN, typename TO>
-__global__ __launch_bounds__(256) void linear_fold_join(LinearArgs a, TileArgs ta, float unit)
+/* linear_rows_kernel's weight reads are the whole cost up to four tokens (S = 4,
+ * N = 10240, K = 6144, int4: 11.3 us against 15.9 on the matrix cores; S = 8:
+ * 17.4 against 15.9); shorter rows than a stage of the fold stay with it. */
+bool use_rows(int32_t S, int32_t K)
 {
-    auto at = [&](int id, int wv) { return fold_at<RR, TT, WN>(id, ta.n_tiles, ta.t_tiles, wv); };
-    join_splits<RR, TT, decltype(at), TO>(a, ta, a.group > 0, unit, at);
+    return S <= 4 || K < kStageK;
+}
+
+/* linear_tiles pays for the expansion where every CU has two of its tiles or
+ * more (int4, bf16: 4096 x 10240 x 6144 523 us against 602 on the int8 cores;
+ * 2048 x 4096 x 4096, one tile a CU, 94 against 90). */
+bool use_tiles(int32_t S, int32_t N, int32_t K, int32_t group, int32_t out_type)
+{
+    return !use_rows(S, K) && out_type == COLI_BF16 && !group && n_tiles_of(S, N, kTileN, 64 * kTileTT) >= 512;
 }
 
 struct TilePlan {
-    int tt, spb, tiles, n_tiles, t_tiles, stages, splits, terms;
-    size_t x_bytes, part_at, total;
+    int tiles, n_tiles, t_tiles, stages;
+    size_t x_bytes, total;
 };
 
-constexpr int kWantTiles = 256; /* workgroups that a launch should have: one per CU */
-
-/* steps per stage of a tile width */
-constexpr int stage_steps(int tt, int terms)
-{
-    return tt == 4 ? 1 : tt == 2 ? (terms == 1 ? 2 : 1) : (terms == 1 ? 4 : 2);
-}
-
-TilePlan tile_plan(int32_t S, int32_t N, int32_t K, int32_t group, int32_t out_type)
+TilePlan tile_plan(int32_t S, int32_t N, int32_t K)
 {
     TilePlan p;
-    p.terms = out_type == COLI_F32 ? 2 : 1;
     p.n_tiles = (N + kTileN - 1) / kTileN;
-    const int most = p.terms == 1 && !group ? 4 : 2;
-    /* the widest token tile that still gives every CU a workgroup or two */
-    p.tt = most;
-    while (p.tt > 1 && (int64_t)p.n_tiles * ((S + 64 * p.tt - 1) / (64 * p.tt)) < 256)
-        p.tt /= 2;
-    p.spb = stage_steps(p.tt, p.terms);
-    p.t_tiles = (S + 64 * p.tt - 1) / (64 * p.tt);
-    p.tiles = p.t_tiles * 2 * p.tt;
-    p.stages = (K + kKB * p.spb - 1) / (kKB * p.spb);
-    p.x_bytes = (size_t)p.stages * p.spb * p.tiles * p.terms * 8 * kTileTok * kChunk;
-    /* tiles for half the CUs or fewer: the stages are shared out, two at least each */
-    const int total = p.n_tiles * p.t_tiles;
-    p.splits = max(1, min(kWantTiles / total, p.stages / 2));
-    p.part_at = (p.x_bytes + (size_t)S * 4 + 255) / 256 * 256;
-    p.total = p.part_at + (p.splits > 1 ? (size_t)p.splits * total * kTileN * 64 * p.tt * 4 : 0);
+    p.t_tiles = (S + 64 * kTileTT - 1) / (64 * kTileTT);
+    p.tiles = p.t_tiles * 2 * kTileTT;
+    p.stages = (K + kKB - 1) / kKB;
+    p.x_bytes = (size_t)p.stages * p.tiles * 8 * kTileTok * kChunk;
+    p.total = (p.x_bytes + (size_t)S * 4 + 255) / 256 * 256;
     return p;
 }
 
-/* Shapes of the fold kernel: rows and tokens of a workgroup. */
+template <int BITS>
+hipError_t launch_tiles(const LinearArgs& a, hipStream_t s)
+{
+    const TilePlan p = tile_plan(a.S, a.N, a.K);
+    TileArgs ta = {};
+    uint8_t* xh = (uint8_t*)a.ws;
+    float* xs = (float*)(xh + p.x_bytes);
+    ta.xh = xh;
+    ta.xs = xs;
+    ta.tiles = p.tiles;
+    ta.n_tiles = p.n_tiles;
+    ta.t_tiles = p.t_tiles;
+    ta.stages = p.stages;
+    const int per = max(1, min(8, p.tiles * p.stages / 512));
+    hipLaunchKernelGGL((linear_expand<BITS>), dim3(p.tiles, (p.stages + per - 1) / per), dim3(256), 0, s, a, xh, xs,
+                       p.tiles, p.stages, per);
+    constexpr int bytes = 2 * TileLds<BITS>::kStage;
+    const hipError_t e = hipFuncSetAttribute((const void*)linear_tiles<BITS>,
+                                             hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e != hipSuccess)
+        return e;
+    hipLaunchKernelGGL((linear_tiles<BITS>), dim3((p.n_tiles * p.t_tiles + 7) / 8 * 8), dim3(256), bytes, s, a, ta);
+    return hipGetLastError();
+}
+
+/* Shapes of the fold kernel, rows and tokens of a workgroup: 128 x 128 where
+ * every CU gets one, else 64 x 64 (S = 512, N = K = 4096: 34.8 us, 46.7 with 128 x
+ * 64), for up to 32 tokens 128 x 32.  A scale group's own sums take as many
+ * registers again, so 128 x 128 is 128 x 64 with groups.  With fewer tiles than 512 the
+ * stages are shared out as well, two at least each, and linear_join adds the
+ * parts (S = 64, N = 10240, K = 6144, int8: 23.4 us against 33.4 with one
+ * workgroup per CU). */
 struct FoldPlan {
     int shape, rows, toks, n_tiles, t_tiles, stages, splits;
     size_t total;
 };
 
-FoldPlan fold_plan(int32_t S, int32_t N, int32_t K)
+constexpr int kWantTiles = 512;
+
+FoldPlan fold_plan(int32_t S, int32_t N, int32_t K, int32_t group)
 {
     FoldPlan p;
     p.stages = (K + kStageK - 1) / kStageK;
-    auto tiles = [&](int rows, int toks) { return (int64_t)((N + rows - 1) / rows) * ((S + toks - 1) / toks); };
-    /* the largest tile that still gives every CU a workgroup, the smallest
-     * otherwise */
-    p.shape = S <= 32 ? 2 : tiles(128, 128) >= kWantTiles ? 0 : tiles(128, 64) >= MIDT ? 1 : 3;
-    p.rows = p.shape == 3 ? 64 : 128;
-    p.toks = p.shape == 0 ? 128 : p.shape == 2 ? 32 : 64;
+    p.shape = S <= 32 ? 2 : n_tiles_of(S, N, 128, 128) >= 256 ? 0 : 1;
+    p.rows = p.shape == 1 ? 64 : 128;
+    p.toks = p.shape == 0 && !group ? 128 : p.shape <= 1 ? 64 : 32;
     p.n_tiles = (N + p.rows - 1) / p.rows;
     p.t_tiles = (S + p.toks - 1) / p.toks;
     const int total = p.n_tiles * p.t_tiles;
-    p.splits = max(1, min(WANTF / total, p.stages / 2));
+    p.splits = max(1, min(kWantTiles / total, p.stages / 2));
     p.total = p.splits > 1 ? (size_t)p.splits * total * p.rows * p.toks * 4 : 256;
     return p;
 }
@@ -1088,11 +1016,8 @@ FoldPlan fold_plan(int32_t S, int32_t N, int32_t K)
 template <int BITS, int RR, int TT, int WN, bool GROUPED, typename TO>
 hipError_t launch_fold_g(const LinearArgs& a, const FoldPlan& p, hipStream_t s)
 {
-    TileArgs ta;
-    ta.xh = nullptr;
-    ta.xs = nullptr;
+    TileArgs ta = {};
     ta.part = (float*)a.ws;
-    ta.tiles = 0;
     ta.n_tiles = p.n_tiles;
     ta.t_tiles = p.t_tiles;
     ta.stages = p.stages;
@@ -1108,7 +1033,7 @@ hipError_t launch_fold_g(const LinearArgs& a, const FoldPlan& p, hipStream_t s)
     hipLaunchKernelGGL((linear_fold<BITS, RR, TT, WN, GROUPED, TO>), dim3((total * p.splits + 7) / 8 * 8), dim3(256),
                        bytes, s, a, ta);
     if (p.splits > 1)
-        hipLaunchKernelGGL((linear_fold_join<RR, TT, WN, TO>), dim3(total, RR * TT * 4), dim3(256), 0, s, a, ta,
+        hipLaunchKernelGGL((linear_join<RR, TT, WN, TO>), dim3(total, RR * TT * 4), dim3(256), 0, s, a, ta,
                            1.0f / (float)(1 << (8 - BITS)));
     return hipGetLastError();
 }
@@ -1123,105 +1048,39 @@ hipError_t launch_fold_shape(const LinearArgs& a, const FoldPlan& p, hipStream_t
 template <int BITS, typename TO>
 hipError_t launch_fold(const LinearArgs& a, hipStream_t s)
 {
-    const FoldPlan p = fold_plan(a.S, a.N, a.K);
-    if (p.shape == 0)
-        return launch_fold_shape<BITS, 2, 2, 2, TO>(a, p, s);
-    if (p.shape == 1)
-        return launch_fold_shape<BITS, 2, 1, 2, TO>(a, p, s);
-    if (p.shape == 3)
-        return launch_fold_shape<BITS, 1, 1, 2, TO>(a, p, s);
-    return launch_fold_shape<BITS, 1, 1, 4, TO>(a, p, s);
-}
-
-#ifndef FOLDMAX
-#define FOLDMAX (1 << 30)
-#endif
-bool use_fold(int32_t S, int32_t K, int32_t out_type)
-{
-    return S > 4 && K >= kStageK && S <= FOLDMAX;
-}
-
-bool use_tiles(int32_t S, int32_t K)
-{
-    return S > 16 && K >= kKB;
-}
-
-template <int BITS, int NT, int TT, bool GROUPED, typename TO>
-hipError_t launch_tiles_t(const LinearArgs& a, const TilePlan& p, hipStream_t s)
-{
-    constexpr int SPB = stage_steps(TT, NT);
-    TileArgs ta;
-    uint8_t* xh = (uint8_t*)a.ws;
-    float* xs = (float*)(xh + p.x_bytes);
-    ta.xh = xh;
-    ta.xs = xs;
-    ta.part = p.splits > 1 ? (float*)((uint8_t*)a.ws + p.part_at) : nullptr;
-    ta.tiles = p.tiles;
-    ta.n_tiles = p.n_tiles;
-    ta.t_tiles = p.t_tiles;
-    ta.stages = p.stages;
-    ta.splits = p.splits;
-    const int steps = p.stages * SPB;
-    const int per = max(1, min(8, p.tiles * steps / 512));
-    hipLaunchKernelGGL((linear_expand<BITS, NT>), dim3(p.tiles, (steps + per - 1) / per), dim3(256), 0, s, a, xh, xs,
-                       p.tiles, steps, per);
-    constexpr int bytes = TileLds<BITS, NT, TT, SPB>::kStage * TileLds<BITS, NT, TT, SPB>::kStages;
-    const auto kernel = linear_tiles<BITS, NT, TT, SPB, GROUPED, TO>;
-    if (bytes > 64 * 1024) {
-        const hipError_t e =
-            hipFuncSetAttribute((const void*)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
-        if (e != hipSuccess)
-            return e;
+    const FoldPlan p = fold_plan(a.S, a.N, a.K, a.group);
+    switch (p.shape) {
+    case 0:
+        return a.group ? launch_fold_g<BITS, 2, 1, 2, true, TO>(a, p, s)
+                       : launch_fold_g<BITS, 2, 2, 2, false, TO>(a, p, s);
+    case 1: return launch_fold_shape<BITS, 1, 1, 2, TO>(a, p, s);
+    default: return launch_fold_shape<BITS, 1, 1, 4, TO>(a, p, s);
     }
-    const int total = p.n_tiles * p.t_tiles;
-    hipLaunchKernelGGL(kernel, dim3((total * p.splits + 7) / 8 * 8), dim3(256), bytes, s, a, ta);
-    if (p.splits > 1)
-        hipLaunchKernelGGL((linear_join<TT, GROUPED, TO>), dim3(total, 2 * TT * 4), dim3(256), 0, s, a, ta);
-    return hipGetLastError();
-}
-
-template <int BITS, typename TO>
-hipError_t launch_tiles(const LinearArgs& a, hipStream_t s)
-{
-    constexpr int NT = sizeof(TO) == 4 ? 2 : 1;
-    const TilePlan p = tile_plan(a.S, a.N, a.K, a.group, a.out_type);
-    if (a.group)
-        return p.tt == 2 ? launch_tiles_t<BITS, NT, 2, true, TO>(a, p, s) : launch_tiles_t<BITS, NT, 1, true, TO>(a, p, s);
-    if constexpr (NT == 1)
-        if (p.tt == 4)
-            return launch_tiles_t<BITS, NT, 4, false, TO>(a, p, s);
-    return p.tt == 2 ? launch_tiles_t<BITS, NT, 2, false, TO>(a, p, s) : launch_tiles_t<BITS, NT, 1, false, TO>(a, p, s);
-}
-
-template <int BITS, typename TO>
-hipError_t launch(const LinearArgs& a, hipStream_t s)
-{
-    if (use_fold(a.S, a.K, a.out_type))
-        return launch_fold<BITS, TO>(a, s);
-    if (use_tiles(a.S, a.K))
-        return launch_tiles<BITS, TO>(a, s);
-    return launch_rows<BITS, TO>(a, s);
 }
 
 template <int BITS>
-hipError_t launch_type(const LinearArgs& a, hipStream_t s)
+hipError_t launch(const LinearArgs& a, hipStream_t s)
 {
-    return a.out_type == COLI_F32 ? launch<BITS, float>(a, s) : launch<BITS, bf16>(a, s);
+    const bool f32 = a.out_type == COLI_F32;
+    if (use_rows(a.S, a.K))
+        return f32 ? launch_rows<BITS, float>(a, s) : launch_rows<BITS, bf16>(a, s);
+    if (use_tiles(a.S, a.N, a.K, a.group, a.out_type))
+        return launch_tiles<BITS>(a, s);
+    return f32 ? launch_fold<BITS, float>(a, s) : launch_fold<BITS, bf16>(a, s);
 }
 
 } // namespace
 
 size_t linear_workspace_bytes(int32_t S, int32_t N, int32_t K, int32_t qtype, int32_t group, int32_t out_type)
 {
-    return use_fold(S, K, out_type) ? fold_plan(S, N, K).total
-           : use_tiles(S, K)        ? tile_plan(S, N, K, group, out_type).total : 256;
+    if (use_rows(S, K))
+        return 256;
+    return use_tiles(S, N, K, group, out_type) ? tile_plan(S, N, K).total : fold_plan(S, N, K, group).total;
 }
 
 hipError_t launch_linear_q(const LinearArgs& a, hipStream_t s)
 {
-    return a.qtype == COLI_Q8   ? launch_type<8>(a, s)
-           : a.qtype == COLI_Q4 ? launch_type<4>(a, s)
-                                : launch_type<2>(a, s);
+    return a.qtype == COLI_Q8 ? launch<8>(a, s) : a.qtype == COLI_Q4 ? launch<4>(a, s) : launch<2>(a, s);
 }
 
 } // namespace coli

@@ -158,6 +158,20 @@ def test_linear(qre, S, N, K, bits, group, dtype):
         within(got, y, ref.linear_tol(y, A, K, dtype), f"{a}")
 
 
+@pytest.mark.parametrize("S,N,K,bits,group", [
+    (7700, 2100, 224, 4, 0), (7690, 2179, 160, 2, 0), (7681, 2177, 416, 8, 0), (2100, 2050, 288, 4, 0),
+    (2060, 2113, 160, 2, 32), (2049, 2050, 416, 8, 0), (2049, 2177, 640, 4, 128)])
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
+def test_linear_many_tokens(qre, S, N, K, bits, group, dtype):
+    """Tiles for every compute unit, with ragged edges, a last step of half its length and an epilogue."""
+    say(f"linear {S} x {N} x {K} int{bits} group {group} {dtype}")
+    w, sc, q, d, bank, g = make_linear(qre, S, N, K, bits, group)
+    bias, res = torch.randn(N, generator=g), torch.randn(S, N, generator=g).to(dtype)
+    y, A = ref.linear(w, sc, bits, group, q, d, bias, "silu", res)
+    got = qre.linear_q(bank, q.cuda(), d.cuda(), bias=bias.cuda(), activation="silu", residual=res.cuda())
+    within(got, y, ref.linear_tol(y, A, K, dtype), "many")
+
+
 @pytest.mark.parametrize("S", [1, 40])
 def test_linear_in_place_and_guard(qre, S):
     """out as its own residual; nothing is written behind the result; equal calls give equal bits."""
