@@ -315,6 +315,16 @@ __device__ __forceinline__ void to_lds(const void* src, void* dst)
                  : "memory");
 }
 
+/* Four bytes per lane, at dst + 4 lane. */
+__device__ __forceinline__ void word_to_lds(const void* src, void* dst)
+{
+    const uint32_t at = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) void*)dst;
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off" ::"s"(
+                     __builtin_amdgcn_readfirstlane(at)),
+                 "v"(src)
+                 : "memory");
+}
+
 /* Waits until at most LEFT of this wave's loads are outstanding, then for the
  * workgroup: past it every wave's earlier loads have arrived, and every wave
  * has left the buffer that is loaded next. */
@@ -431,40 +441,6 @@ __device__ __forceinline__ void store_rows(const LinearArgs& a, int tok, int n, 
                 store1(out + j, v[j] + (res ? to_f32(res[j]) : 0.0f));
     }
 }
-
-/* A scale group's row scales for one wave: lane l loads its rows' (row n0 + l)
- * when the group opens, in one instruction; when it closes they go through the
- * wave's own LDS words to the lanes that hold those rows' sums. */
-template <int RR>
-struct GroupScales {
-    float mine;
-    __device__ __forceinline__ void open(const LinearArgs& a, int n0, int gpr, int g)
-    {
-        const int lane = threadIdx.x & 63;
-        mine = a.w_scale[(int64_t)min(n0 + lane % (32 * RR), a.N - 1) * gpr + min(g, gpr - 1)];
-    }
-    template <int TT, typename P, typename A>
-    __device__ __forceinline__ void close(float* words, int h, P& part, A& acc)
-    {
-        words[threadIdx.x & 63] = mine;
-        __builtin_amdgcn_wave_barrier();
-#pragma unroll
-        for (int r = 0; r < RR; ++r)
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const float4 v = *(const float4*)(words + r * 32 + 8 * q + 4 * h);
-                const float s[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-#pragma unroll
-                    for (int t = 0; t < TT; ++t) {
-                        acc[r][t][4 * q + j] = __builtin_fmaf(part[r][t][4 * q + j], s[j], acc[r][t][4 * q + j]);
-                        part[r][t][4 * q + j] = 0.0f;
-                    }
-            }
-        __builtin_amdgcn_wave_barrier();
-    }
-};
 
 /* What the tile kernels take of a launch. */
 struct TileArgs {
@@ -695,29 +671,31 @@ struct FoldShape {
     static constexpr int kRows = 32 * RR * WN, kTok = 32 * TT * (4 / WN);
 };
 
-/* LDS of a stage: codes, weights, scales; and the stages in flight, as many as
+/* LDS of a stage: codes, weights, the tokens' scales, the groups'; and the stages in flight, as many as
  * leave room for two workgroups in a CU's 160 KB. */
-template <int BITS, int RR, int TT, int WN>
+template <int BITS, int RR, int TT, int WN, int GROUPED>
 struct FoldLds {
     using F = FoldShape<RR, TT, WN>;
     static constexpr int kX = F::kTok * kStageK, kW = F::kRows * kStageK * BITS / 8;
     static constexpr int kRunsD = (F::kTok * kChunk + 1023) / 1024;
-    static constexpr int kStage = kX + kW + kRunsD * 1024;
+    /* row scales of each block's group (GROUPED 1), or of the stage's (2) */
+    static constexpr int kScales = GROUPED == 0 ? 0 : GROUPED == 1 ? 4 : 1, kS = kScales * WN * 256;
+    static constexpr int kStage = kX + kW + kRunsD * 1024 + kS;
     static constexpr int kFit = 79 * 1024 / kStage;
     static constexpr int kStages = kFit < 2 ? 2 : kFit > 4 ? 4 : kFit;
     /* loads of a wave and stage; where there are fewer runs than waves, waves
      * load the same one, so that every wave counts alike */
-    static constexpr int kLoads = kX / 4096 + (kW + 4095) / 4096 + 1;
+    static constexpr int kLoads = kX / 4096 + (kW + 4095) / 4096 + 1 + kScales;
 };
 
-template <int BITS, int RR, int TT, int WN, bool GROUPED, typename TO>
+template <int BITS, int RR, int TT, int WN, int GROUPED, typename TO>
 __global__ __launch_bounds__(256, 2) void linear_fold(LinearArgs a, TileArgs ta)
 {
     constexpr int XC = kStageK / kChunk;       /* chunks of a token's stage */
     constexpr int WC = kStageK * BITS / 128;   /* chunks of a row's stage: 8, 4, 2 */
     using F = FoldShape<RR, TT, WN>;
-    using L = FoldLds<BITS, RR, TT, WN>;
-    constexpr int XB = L::kX, WB = L::kW, STAGES = L::kStages;
+    using L = FoldLds<BITS, RR, TT, WN, GROUPED>;
+    constexpr int XB = L::kX, WB = L::kW, SB = L::kStage - L::kS, STAGES = L::kStages;
     extern __shared__ __align__(1024) uint8_t lds[];
     const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6, h = lane >> 5, col = lane & 31;
 
@@ -729,7 +707,7 @@ __global__ __launch_bounds__(256, 2) void linear_fold(LinearArgs a, TileArgs ta)
     const TileAt at = {wg.n0 + wv % WN * 32 * RR, wg.tok0 + wv / WN * 32 * TT};
     const int share = (ta.stages + ta.splits - 1) / ta.splits;
     const int s0 = split * share, s1 = min(s0 + share, ta.stages);
-    const int nb = a.K / 32;
+    const int nb = a.K / 32, gpr = GROUPED ? a.K / a.group : 1, gb = GROUPED ? a.group / 32 : 1;
     const int64_t row_bytes = (int64_t)a.K * BITS / 8;
 
     /* Slot s of a token's or row's chunks holds chunk s ^ f, so that 16 of them
@@ -757,6 +735,13 @@ __global__ __launch_bounds__(256, 2) void linear_fold(LinearArgs a, TileArgs ta)
         const int run = wv % L::kRunsD;
         to_lds(a.xd + (int64_t)min(wg.tok0 + run * 64 + lane, a.S - 1) * nb + min(stage * 4, nb - 4),
                buf + XB + WB + run * 1024);
+        if constexpr (GROUPED) {
+#pragma unroll
+            for (int b = 0; b < L::kScales; ++b)
+                word_to_lds(a.w_scale + (int64_t)min(at.n0 + lane % (32 * RR), a.N - 1) * gpr +
+                                min(stage * 4 + b, nb - 1) / gb,
+                            buf + SB + (b * WN + wv % WN) * 256);
+        }
     };
 
     float acc[RR][TT][16], part[GROUPED ? RR : 1][GROUPED ? TT : 1][16];
@@ -770,12 +755,6 @@ __global__ __launch_bounds__(256, 2) void linear_fold(LinearArgs a, TileArgs ta)
                 if constexpr (GROUPED)
                     part[r][t][i] = 0.0f;
             }
-    const int gpr = GROUPED ? a.K / a.group : 1, gb = GROUPED ? a.group / 32 : 1;
-    __shared__ float scale_words[GROUPED ? 4 : 1][64];
-    GroupScales<RR> scales;
-    int g = s0 * 4 / gb;
-    if constexpr (GROUPED)
-        scales.open(a, at.n0, gpr, g);
 #pragma unroll
     for (int i = 0; i < STAGES - 1; ++i)
         fetch(s0 + i);
@@ -828,6 +807,31 @@ __global__ __launch_bounds__(256, 2) void linear_fold(LinearArgs a, TileArgs ta)
             for (int i = 0; i < 16; ++i)
                 o[i] = __builtin_fmaf((float)z[m & 1][i], d[t][b2], o[i]);
         };
+        /* after block b: where its group ends (or the range does, which is no
+         * harm inside a group) the group's sums take their rows' scales */
+        auto close = [&](int b) {
+            if (GROUPED == 2 && b < 3)
+                return;
+            const int blk = stage * 4 + b;
+            if ((blk + 1) % gb && (b < 3 || stage + 1 < s1))
+                return;
+            const float* words = (const float*)(buf + SB + (b % (GROUPED == 1 ? 4 : 1) * WN + wv % WN) * 256);
+#pragma unroll
+            for (int r = 0; r < RR; ++r)
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const float4 v = *(const float4*)(words + r * 32 + 8 * q + 4 * h);
+                    const float e[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+#pragma unroll
+                        for (int t = 0; t < TT; ++t) {
+                            float& p = part[GROUPED ? r : 0][GROUPED ? t : 0][4 * q + j];
+                            acc[r][t][4 * q + j] = __builtin_fmaf(p, e[j], acc[r][t][4 * q + j]);
+                            p = 0.0f;
+                        }
+                }
+        };
         v4i wf[RR];
 #pragma unroll
         for (int m = 0; m < 4 * RR * TT; ++m) {
@@ -839,23 +843,14 @@ __global__ __launch_bounds__(256, 2) void linear_fold(LinearArgs a, TileArgs ta)
             __builtin_amdgcn_sched_barrier(0);
             if (m)
                 fold(m - 1);
-            if constexpr (GROUPED) {
-                /* every fold of the blocks before this one is done */
-                if (m % (RR * TT) == 0) {
-                    const int now = min(stage * 4 + b, nb - 1) / gb;
-                    if (now > g) {
-                        scales.template close<TT>(scale_words[wv], h, part, acc);
-                        g = now;
-                        scales.open(a, at.n0, gpr, g);
-                    }
-                }
-            }
+            if constexpr (GROUPED)
+                if (m && m % (RR * TT) == 0)
+                    close(b - 1);
         }
         fold(4 * RR * TT - 1);
+        if constexpr (GROUPED)
+            close(3);
     }
-    if constexpr (GROUPED)
-        scales.template close<TT>(scale_words[wv], h, part, acc);
-
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); /* no load outlives the workgroup's LDS */
     constexpr float unit_w = 1.0f / (float)(1 << (8 - BITS));
     if (ta.splits == 1) {
@@ -1013,7 +1008,7 @@ FoldPlan fold_plan(int32_t S, int32_t N, int32_t K, int32_t group)
     return p;
 }
 
-template <int BITS, int RR, int TT, int WN, bool GROUPED, typename TO>
+template <int BITS, int RR, int TT, int WN, int GROUPED, typename TO>
 hipError_t launch_fold_g(const LinearArgs& a, const FoldPlan& p, hipStream_t s)
 {
     TileArgs ta = {};
@@ -1022,7 +1017,7 @@ hipError_t launch_fold_g(const LinearArgs& a, const FoldPlan& p, hipStream_t s)
     ta.t_tiles = p.t_tiles;
     ta.stages = p.stages;
     ta.splits = p.splits;
-    constexpr int bytes = FoldLds<BITS, RR, TT, WN>::kStage * FoldLds<BITS, RR, TT, WN>::kStages;
+    constexpr int bytes = FoldLds<BITS, RR, TT, WN, GROUPED>::kStage * FoldLds<BITS, RR, TT, WN, GROUPED>::kStages;
     if (bytes > 64 * 1024) {
         const hipError_t e = hipFuncSetAttribute((const void*)linear_fold<BITS, RR, TT, WN, GROUPED, TO>,
                                                  hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
@@ -1041,8 +1036,9 @@ hipError_t launch_fold_g(const LinearArgs& a, const FoldPlan& p, hipStream_t s)
 template <int BITS, int RR, int TT, int WN, typename TO>
 hipError_t launch_fold_shape(const LinearArgs& a, const FoldPlan& p, hipStream_t s)
 {
-    return a.group ? launch_fold_g<BITS, RR, TT, WN, true, TO>(a, p, s)
-                   : launch_fold_g<BITS, RR, TT, WN, false, TO>(a, p, s);
+    return a.group == 0             ? launch_fold_g<BITS, RR, TT, WN, 0, TO>(a, p, s)
+           : a.group % kStageK == 0 ? launch_fold_g<BITS, RR, TT, WN, 2, TO>(a, p, s)
+                                    : launch_fold_g<BITS, RR, TT, WN, 1, TO>(a, p, s);
 }
 
 template <int BITS, typename TO>
@@ -1051,8 +1047,9 @@ hipError_t launch_fold(const LinearArgs& a, hipStream_t s)
     const FoldPlan p = fold_plan(a.S, a.N, a.K, a.group);
     switch (p.shape) {
     case 0:
-        return a.group ? launch_fold_g<BITS, 2, 1, 2, true, TO>(a, p, s)
-                       : launch_fold_g<BITS, 2, 2, 2, false, TO>(a, p, s);
+        return a.group == 0               ? launch_fold_g<BITS, 2, 2, 2, 0, TO>(a, p, s)
+               : a.group % kStageK == 0 ? launch_fold_g<BITS, 2, 1, 2, 2, TO>(a, p, s)
+                                        : launch_fold_g<BITS, 2, 1, 2, 1, TO>(a, p, s);
     case 1: return launch_fold_shape<BITS, 1, 1, 2, TO>(a, p, s);
     default: return launch_fold_shape<BITS, 1, 1, 4, TO>(a, p, s);
     }
