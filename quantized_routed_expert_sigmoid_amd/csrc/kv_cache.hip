@@ -1,13 +1,21 @@
 /*
  * kv_cache.hip -- append to and read-back from the paged int8 cache.
  *
- * Append: one workgroup per (sequence, touched block, head) takes the block's
- * new scale from the old one and the new values' largest magnitude, then
- * requantises what the block held (only where the scale grew) and writes the
- * new codes.  It reads each new value once from memory (the second pass over
- * them hits the caches) and touches 64 tokens of one head at most.
+ * A workgroup takes the keys or the values of one (block, head).  Its units are
+ * the 16-byte pieces in which the codes lie in the page: for keys 16 dims of
+ * one token, for values 16 tokens of one dim (value_byte); neighbouring lanes
+ * have neighbouring pieces, so a page is read and written in whole lines, and
+ * packed rows in runs of 32 bytes or more.
+ *
+ * Append: a = the new values' largest magnitude, s' = max(s, a / 127); held
+ * codes become rnd(c s / s') where the scale grew, new ones rnd(v / s').  The
+ * values stay in registers between the two, so each is read once; pieces that
+ * neither hold a new token nor change are not touched.  Bound by the bytes of
+ * the rows and codes, for a decode step by latency.
  */
 #include "block_device.h"
+
+#include <type_traits>
 
 namespace coli {
 
@@ -15,101 +23,237 @@ namespace {
 
 constexpr int kThreads = 256;
 
-template <typename T>
-__device__ void append_one(const T* x, int64_t stride, int D, int H, int h, int64_t row0, int t0, int t1,
-                           bool held, int8_t* page, float* scale, bool key, float* part)
-{
-    /* new tokens t0 .. t1 - 1 of the block from packed row row0 on */
-    const int n4 = D / 4, n = (t1 - t0) * n4;
-    float a = 0.0f;
-    for (int i = threadIdx.x; i < n; i += kThreads) {
-        const float4 v = load4(x + (row0 + i / n4) * stride + (int64_t)h * D + 4 * (i % n4));
-        a = fmaxf(a, fmaxf(fmaxf(fabsf(v.x), fabsf(v.y)), fmaxf(fabsf(v.z), fabsf(v.w))));
+/* Token (of the block) and dim of byte b of piece u. */
+template <int D, bool KEY>
+struct Piece {
+    int token0, dim0;
+    __device__ __forceinline__ explicit Piece(int u)
+    {
+        if (KEY) { /* half-block, 16 dims, token */
+            token0 = u / (2 * D) * 32 + u % 32;
+            dim0 = u / 32 % (D / 16) * 16;
+        } else { /* half-block, dim, bit 2 of the token */
+            token0 = u / (2 * D) * 32 + (u & 1) * 4;
+            dim0 = u / 2 % D;
+        }
     }
+    __device__ __forceinline__ int token(int b) const { return KEY ? token0 : token0 + b / 4 * 8 + b % 4; }
+};
+
+/* The sixteen values of a piece from the packed rows; x is the row that token 0
+ * of the block has or would have, only tokens t0 .. t1 - 1 have rows.  Loads are
+ * unconditional, from the nearest row: one under a branch would be waited for
+ * by itself. */
+template <typename T, int D, bool KEY>
+__device__ __forceinline__ void load_piece(const T* x, int64_t stride, const Piece<D, KEY>& p, int t0, int t1,
+                                           float (&v)[16])
+{
+    if constexpr (KEY) {
+        const T* r = x + min(max(p.token0, t0), t1 - 1) * stride + p.dim0;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const float4 e = load4(r + 4 * j);
+            v[4 * j] = e.x;
+            v[4 * j + 1] = e.y;
+            v[4 * j + 2] = e.z;
+            v[4 * j + 3] = e.w;
+        }
+    } else {
+#pragma unroll
+        for (int b = 0; b < 16; ++b)
+            v[b] = to_f32(x[min(max(p.token(b), t0), t1 - 1) * stride + p.dim0]);
+    }
+}
+
+/* The code of v as q8_code gives it, plus 128. */
+__device__ __forceinline__ float code_up(float v, float inv)
+{
+    const float r = v * inv, t = __builtin_truncf(r);
+    const float e = __builtin_fabsf(r - t) >= 0.5f ? t + __builtin_copysignf(1.0f, r) : t;
+    return __builtin_amdgcn_fmed3f(e, -127.0f, 127.0f) + 128.0f;
+}
+
+/* Sixteen codes, each converted into its byte. */
+__device__ __forceinline__ uint4 encode16(const float (&v)[16], float inv)
+{
+    uint32_t w[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        uint32_t u = 0;
+        u = __builtin_amdgcn_cvt_pk_u8_f32(code_up(v[4 * j], inv), 0, u);
+        u = __builtin_amdgcn_cvt_pk_u8_f32(code_up(v[4 * j + 1], inv), 1, u);
+        u = __builtin_amdgcn_cvt_pk_u8_f32(code_up(v[4 * j + 2], inv), 2, u);
+        u = __builtin_amdgcn_cvt_pk_u8_f32(code_up(v[4 * j + 3], inv), 3, u);
+        w[j] = u ^ 0x80808080u;
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+template <typename T, int D, bool KEY>
+__device__ void append_block(const T* x, int64_t stride, int t0, int t1, int8_t* page, float* scale)
+{
+    constexpr int N = D / 64; /* pieces of a thread: 4 D in a block */
+    __shared__ float part[kThreads / kWave];
+    float v[N][16], a = 0.0f;
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+        load_piece<T, D, KEY>(x, stride, Piece<D, KEY>(threadIdx.x + kThreads * n), t0, t1, v[n]);
+#pragma unroll
+        for (int b = 0; b < 16; ++b)
+            a = fmaxf(a, fabsf(v[n][b])); /* rows outside are copies of ones inside */
+    }
+    const float old = t0 > 0 ? *scale : 0.0f;
     for (int m = 32; m >= 1; m >>= 1)
         a = fmaxf(a, shfl_xor(a, m));
-    __syncthreads();
     if ((threadIdx.x & 63) == 0)
         part[threadIdx.x >> 6] = a;
     __syncthreads();
     a = fmaxf(fmaxf(part[0], part[1]), fmaxf(part[2], part[3]));
-    const float old = held ? *scale : 0.0f;
     const float now = fmaxf(old, a / 127.0f);
-    const float inv = now == 0.0f ? 0.0f : 1.0f / now;
-    if (held && now != old) {
-        const float f = old * inv;
-        for (int i = threadIdx.x; i < t0 * D; i += kThreads) {
-            const int t = i / D, c = i % D;
-            int8_t* p = page + (key ? key_byte(t, c, D) : value_byte(t, c, D));
-            *p = (int8_t)q8_code((float)*p, f);
+    const float inv = now == 0.0f ? 0.0f : 1.0f / now, f = old * inv;
+    const bool grew = t0 > 0 && now != old;
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+        const int u = threadIdx.x + kThreads * n;
+        const Piece<D, KEY> p(u);
+        const int first = p.token(0), last = p.token(15);
+        const bool whole = first >= t0 && last < t1; /* all new */
+        bool any = whole;
+        if (!KEY) {
+#pragma unroll
+            for (int b = 0; b < 16; b += 4)
+                any |= p.token(b) < t1 && p.token(b) + 3 >= t0;
         }
+        if (!any && !(grew && first < t0))
+            continue;
+        uint4* at = (uint4*)page + u;
+        if (whole) {
+            *at = encode16(v[n], inv);
+            continue;
+        }
+        /* some held, or behind the last token: these keep their bytes */
+        const uint4 o = *at;
+        uint32_t w[4] = {o.x, o.y, o.z, o.w};
+#pragma unroll
+        for (int b = 0; b < 16; ++b) {
+            const int t = p.token(b), sh = 8 * (b & 3);
+            int32_t c = (int8_t)(w[b / 4] >> sh);
+            if (t >= t0 && t < t1)
+                c = q8_code(v[n][b], inv);
+            else if (t < t0 && grew)
+                c = q8_code((float)c, f);
+            w[b / 4] = (w[b / 4] & ~(0xFFu << sh)) | ((uint32_t)(c & 0xFF) << sh);
+        }
+        *at = make_uint4(w[0], w[1], w[2], w[3]);
     }
-    for (int i = threadIdx.x; i < n; i += kThreads) {
-        const int t = t0 + i / n4, c = 4 * (i % n4);
-        const float4 v = load4(x + (row0 + i / n4) * stride + (int64_t)h * D + c);
-        const float e[4] = {v.x, v.y, v.z, v.w};
-        for (int j = 0; j < 4; ++j)
-            page[key ? key_byte(t, c + j, D) : value_byte(t, c + j, D)] = (int8_t)q8_code(e[j], inv);
-    }
-    __syncthreads(); /* every thread has read the old scale */
+    __syncthreads(); /* every wave has the old scale, and has left `part` */
     if (threadIdx.x == 0)
         *scale = now;
 }
 
-template <typename T>
+template <typename T, int D>
 __global__ __launch_bounds__(kThreads) void kv_append_kernel(coli_kv_cache c, coli_kv_batch b, const T* k,
                                                              const T* v, int64_t k_stride, int64_t v_stride)
 {
-    __shared__ float part[kThreads / kWave];
-    const int h = blockIdx.y, s = blockIdx.z, D = c.head_dim;
+    const int h = blockIdx.y >> 1, s = blockIdx.z;
+    const bool key = !(blockIdx.y & 1);
     const SeqBounds q = seq_bounds(b, s);
     const int from = max(q.first, 0);
     if (q.kv_len <= from)
         return;
-    const int blk0 = from / COLI_KV_BLOCK, blk1 = (q.kv_len - 1) / COLI_KV_BLOCK;
-    for (int blk = blk0 + blockIdx.x; blk <= blk1; blk += gridDim.x) {
+    const int blk1 = (q.kv_len - 1) / COLI_KV_BLOCK;
+    for (int blk = from / COLI_KV_BLOCK + blockIdx.x; blk <= blk1; blk += gridDim.x) {
         const int page = page_of(b, c.n_pages, s, blk);
         if (page < 0)
             continue;
         const int base = blk * COLI_KV_BLOCK;
         const int t0 = max(from - base, 0), t1 = min(q.kv_len - base, COLI_KV_BLOCK);
-        const int64_t row0 = (int64_t)q.row0 + (base + t0 - q.first);
-        const int64_t at = (int64_t)page * c.n_heads + h, bytes = (int64_t)COLI_KV_BLOCK * D;
-        append_one(k, k_stride, D, c.n_heads, h, row0, t0, t1, t0 > 0, c.k + at * bytes, c.k_scale + at, true,
-                   part);
-        append_one(v, v_stride, D, c.n_heads, h, row0, t0, t1, t0 > 0, c.v + at * bytes, c.v_scale + at, false,
-                   part);
+        const int64_t row0 = (int64_t)q.row0 + (base - q.first); /* the row that token 0 would have */
+        const int64_t at = (int64_t)page * c.n_heads + h;
+        if (key)
+            append_block<T, D, true>(k + row0 * k_stride + (int64_t)h * D, k_stride, t0, t1,
+                                     c.k + at * (COLI_KV_BLOCK * D), c.k_scale + at);
+        else
+            append_block<T, D, false>(v + row0 * v_stride + (int64_t)h * D, v_stride, t0, t1,
+                                      c.v + at * (COLI_KV_BLOCK * D), c.v_scale + at);
     }
 }
 
-template <typename T>
+/* The rows' values of one block and head; a missing page (null) gives zeros. */
+template <typename T, int D, bool KEY>
+__device__ __forceinline__ void read_block(const int8_t* page, float scale, int t0, int t1, T* x, int64_t stride)
+{
+#pragma unroll
+    for (int n = 0; n < D / 64; ++n) {
+        const int u = threadIdx.x + kThreads * n;
+        const Piece<D, KEY> p(u);
+        const uint4 o = page ? ((const uint4*)page)[u] : make_uint4(0, 0, 0, 0);
+        const uint32_t w[4] = {o.x, o.y, o.z, o.w};
+        float v[16];
+#pragma unroll
+        for (int b = 0; b < 16; ++b)
+            v[b] = (float)(int8_t)(w[b / 4] >> (8 * (b & 3))) * scale;
+        if constexpr (KEY) {
+            if (p.token0 >= t0 && p.token0 < t1)
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    store4(x + p.token0 * stride + p.dim0 + 4 * j,
+                           make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]));
+        } else {
+#pragma unroll
+            for (int b = 0; b < 16; ++b) {
+                const int t = p.token(b);
+                if (t >= t0 && t < t1)
+                    store1(x + t * stride + p.dim0, v[b]);
+            }
+        }
+    }
+}
+
+template <typename T, int D>
 __global__ __launch_bounds__(kThreads) void kv_read_kernel(coli_kv_cache c, coli_kv_batch b, T* k, T* v)
 {
-    const int s = blockIdx.z, D = c.head_dim, H = c.n_heads, n4 = H * D / 4;
+    const int h = blockIdx.y >> 1, s = blockIdx.z;
+    const bool key = !(blockIdx.y & 1);
+    if (!(key ? k : v))
+        return;
     const SeqBounds q = seq_bounds(b, s);
-    for (int i = blockIdx.x; i < q.q_len; i += gridDim.x) {
-        const int tok = q.first + i;
-        const int page = tok < 0 ? -1 : page_of(b, c.n_pages, s, tok / COLI_KV_BLOCK);
-        const int t = tok & (COLI_KV_BLOCK - 1);
-        const int64_t o = (int64_t)(q.row0 + i) * H * D;
-        for (int e = threadIdx.x; e < n4; e += kThreads) {
-            const int h = 4 * e / D, d = 4 * e % D;
-            float4 kk = make_float4(0.f, 0.f, 0.f, 0.f), vv = kk;
-            if (page >= 0) {
-                const int64_t at = (int64_t)page * H + h;
-                const float sk = c.k_scale[at], sv = c.v_scale[at];
-                const int8_t* pk = c.k + at * COLI_KV_BLOCK * D;
-                const int8_t* pv = c.v + at * COLI_KV_BLOCK * D;
-                kk = make_float4(sk * pk[key_byte(t, d, D)], sk * pk[key_byte(t, d + 1, D)],
-                                 sk * pk[key_byte(t, d + 2, D)], sk * pk[key_byte(t, d + 3, D)]);
-                vv = make_float4(sv * pv[value_byte(t, d, D)], sv * pv[value_byte(t, d + 1, D)],
-                                 sv * pv[value_byte(t, d + 2, D)], sv * pv[value_byte(t, d + 3, D)]);
-            }
-            if (k)
-                store4(k + o + 4 * e, kk);
-            if (v)
-                store4(v + o + 4 * e, vv);
-        }
+    const int64_t stride = (int64_t)c.n_heads * D;
+    /* rows before the first token (the rows outnumber the tokens) are in blocks
+     * below 0, which have no page */
+    const int blk0 = q.first >> 6, blk1 = (q.kv_len - 1) >> 6;
+    for (int64_t blk = (int64_t)blk0 + blockIdx.x; q.q_len && blk <= blk1; blk += gridDim.x) {
+        const int64_t base = blk * COLI_KV_BLOCK;
+        const int page = blk < 0 ? -1 : page_of(b, c.n_pages, s, (int)blk);
+        const int t0 = (int)max((int64_t)q.first - base, (int64_t)0);
+        const int t1 = (int)min((int64_t)q.kv_len - base, (int64_t)COLI_KV_BLOCK);
+        const int64_t row0 = (int64_t)q.row0 + (base - q.first), at = (int64_t)max(page, 0) * c.n_heads + h;
+        if (key)
+            read_block<T, D, true>(page < 0 ? nullptr : c.k + at * (COLI_KV_BLOCK * D), page < 0 ? 0.0f : c.k_scale[at],
+                                   t0, t1, k + row0 * stride + (int64_t)h * D, stride);
+        else
+            read_block<T, D, false>(page < 0 ? nullptr : c.v + at * (COLI_KV_BLOCK * D), page < 0 ? 0.0f : c.v_scale[at],
+                                    t0, t1, v + row0 * stride + (int64_t)h * D, stride);
+    }
+}
+
+/* Workgroups of a sequence: a block each of the longest expected run of rows,
+ * and one where the run straddles; longer runs take several turns. */
+dim3 grid_of(const coli_kv_cache& c, const coli_kv_batch& b)
+{
+    const int rows = max(1, min(b.max_q, b.n_tokens));
+    const int blocks = rows == 1 ? 1 : (rows - 2) / COLI_KV_BLOCK + 2;
+    return dim3((uint32_t)min(blocks, 1024), (uint32_t)c.n_heads * 2, (uint32_t)b.n_seq);
+}
+
+template <typename F>
+void by_dim(int32_t head_dim, F f)
+{
+    switch (head_dim) {
+    case 64: f(std::integral_constant<int, 64>()); break;
+    case 128: f(std::integral_constant<int, 128>()); break;
+    case 192: f(std::integral_constant<int, 192>()); break;
+    default: f(std::integral_constant<int, 256>()); break;
     }
 }
 
@@ -118,24 +262,28 @@ __global__ __launch_bounds__(kThreads) void kv_read_kernel(coli_kv_cache c, coli
 hipError_t launch_kv_append(const coli_kv_cache& c, const coli_kv_batch& b, const void* k, const void* v,
                             int32_t type, int64_t k_stride, int64_t v_stride, hipStream_t s)
 {
-    const dim3 grid((uint32_t)min(b.max_q / COLI_KV_BLOCK + 2, 1024), (uint32_t)c.n_heads, (uint32_t)b.n_seq);
-    if (type == COLI_F32)
-        hipLaunchKernelGGL(kv_append_kernel<float>, grid, dim3(kThreads), 0, s, c, b, (const float*)k,
-                           (const float*)v, k_stride, v_stride);
-    else
-        hipLaunchKernelGGL(kv_append_kernel<bf16>, grid, dim3(kThreads), 0, s, c, b, (const bf16*)k,
-                           (const bf16*)v, k_stride, v_stride);
+    by_dim(c.head_dim, [&](auto d) {
+        if (type == COLI_F32)
+            hipLaunchKernelGGL((kv_append_kernel<float, d.value>), grid_of(c, b), dim3(kThreads), 0, s, c, b,
+                               (const float*)k, (const float*)v, k_stride, v_stride);
+        else
+            hipLaunchKernelGGL((kv_append_kernel<bf16, d.value>), grid_of(c, b), dim3(kThreads), 0, s, c, b,
+                               (const bf16*)k, (const bf16*)v, k_stride, v_stride);
+    });
     return hipGetLastError();
 }
 
 hipError_t launch_kv_read(const coli_kv_cache& c, const coli_kv_batch& b, void* k, void* v, int32_t type,
                           hipStream_t s)
 {
-    const dim3 grid((uint32_t)max(1, min(b.max_q, 4096)), 1, (uint32_t)b.n_seq);
-    if (type == COLI_F32)
-        hipLaunchKernelGGL(kv_read_kernel<float>, grid, dim3(kThreads), 0, s, c, b, (float*)k, (float*)v);
-    else
-        hipLaunchKernelGGL(kv_read_kernel<bf16>, grid, dim3(kThreads), 0, s, c, b, (bf16*)k, (bf16*)v);
+    by_dim(c.head_dim, [&](auto d) {
+        if (type == COLI_F32)
+            hipLaunchKernelGGL((kv_read_kernel<float, d.value>), grid_of(c, b), dim3(kThreads), 0, s, c, b, (float*)k,
+                               (float*)v);
+        else
+            hipLaunchKernelGGL((kv_read_kernel<bf16, d.value>), grid_of(c, b), dim3(kThreads), 0, s, c, b, (bf16*)k,
+                               (bf16*)v);
+    });
     return hipGetLastError();
 }
 
