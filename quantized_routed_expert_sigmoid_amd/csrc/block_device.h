@@ -97,6 +97,47 @@ __device__ __forceinline__ void store4_any(bf16* p, float4 v)
     __builtin_memcpy(p, &u, 8);
 }
 
+/* Sixteen bytes per lane from memory into LDS at dst + 16 lane (dst uniform).
+ * Written out because the compiler, which cannot tell the buffers apart, would
+ * wait for every such load before the next LDS read; whoever uses it waits
+ * himself (arrive_all).  M0 holds the LDS address; no other instruction of
+ * these kernels takes M0. */
+__device__ __forceinline__ void to_lds(const void* src, void* dst)
+{
+    const uint32_t at = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) void*)dst;
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(
+                     __builtin_amdgcn_readfirstlane(at)),
+                 "v"(src)
+                 : "memory");
+}
+
+/* Four bytes per lane, at dst + 4 lane. */
+__device__ __forceinline__ void word_to_lds(const void* src, void* dst)
+{
+    const uint32_t at = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) void*)dst;
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off" ::"s"(
+                     __builtin_amdgcn_readfirstlane(at)),
+                 "v"(src)
+                 : "memory");
+}
+
+/* Waits until at most LEFT of this wave's loads are outstanding and its LDS
+ * accesses are done, then for the workgroup: past it every wave's earlier loads
+ * have arrived, and every wave has left the buffer that is written next. */
+template <int LEFT>
+__device__ __forceinline__ void arrive_all()
+{
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(LEFT) : "memory");
+}
+
+/* Workgroups go to the eight XCDs in turn; each XCD takes a contiguous run of
+ * units (the grid is a multiple of eight), so that what it works on at a time
+ * shares its L2. */
+__device__ __forceinline__ int64_t xcd_unit()
+{
+    return (int64_t)(blockIdx.x & 7) * (gridDim.x >> 3) + (blockIdx.x >> 3);
+}
+
 /* Byte of (token t, dim c) inside a page's keys and values of one head. */
 __device__ __forceinline__ int key_byte(int t, int c, int D)
 {

@@ -186,10 +186,11 @@ __device__ __forceinline__ float row_sum(float v)
 }
 
 /* A query row in int8 digits, most significant first, as operands of the key
- * product; returns the value of one unit (NaN if the row holds a NaN or an
- * infinity). */
+ * product, negated for a negative softmax scale; returns the value of one unit
+ * (not negative, NaN if the row holds a NaN or an infinity). */
 template <typename T, int R, int D, int ND>
-__device__ __forceinline__ float load_query(const T* row, bool live, int g, v4i (&dig)[ND][D / Tile<R>::kDims])
+__device__ __forceinline__ float load_query(const T* row, bool live, bool negate, int g,
+                                            v4i (&dig)[ND][D / Tile<R>::kDims])
 {
     constexpr int KS = D / Tile<R>::kDims;
     float x[KS * 16];
@@ -213,7 +214,7 @@ __device__ __forceinline__ float load_query(const T* row, bool live, int g, v4i 
     const float lift = amax < 0x1p-60f ? 0x1p64f : 1.0f;
     constexpr float top = ND == 2 ? 127.0f * 256 : 127.0f * 65536;
     const float up = amax * lift;
-    const float f = up == 0.0f ? 0.0f : top / up;
+    const float f = up == 0.0f ? 0.0f : negate ? -top / up : top / up;
 #pragma unroll
     for (int s = 0; s < KS; ++s)
 #pragma unroll
@@ -317,6 +318,46 @@ __device__ __forceinline__ Span row_span(const coli_kv_attn& a, const SeqBounds&
     return s;
 }
 
+/* Scores of the tokens that the lane's row does not see, in NU halves of a block
+ * from token `base` on. */
+template <int R, int NU>
+__device__ __forceinline__ void mask_tile(float* t, int base, int end, int begin, int lg)
+{
+#pragma unroll
+    for (int i = 0; i < NU * (R / 2); ++i) {
+        const int j = base + i / (R / 2) * 32 + Tile<R>::token(i % (R / 2), lg);
+        t[i] = j < end && j >= begin ? t[i] : -__builtin_inff();
+    }
+}
+
+/* Scores t in units of c (c >= 0, one per row) become 2^(t c - m) with m raised
+ * to the largest; l, the lane's sum, takes them up; returns the factor of what
+ * was summed before.  The scale goes into the exponent's fma: the largest of t
+ * is the largest of t c. */
+template <int R, int N>
+__device__ __forceinline__ float softmax_tile(float* t, float c, float& m, float& l)
+{
+    float mx = t[0];
+#pragma unroll
+    for (int i = 1; i < N; ++i)
+        mx = fmaxf(mx, t[i]);
+    mx = row_max<R>(mx);
+    /* a row that has seen nothing keeps -inf (0 * -inf is no number) */
+    const float mn = mx == -__builtin_inff() ? m : fmaxf(m, mx * c);
+    const float mb = mn == -__builtin_inff() ? 0.0f : mn;
+    const float cc = c == 0.0f ? 0x1p-126f : c; /* hidden tokens stay at -inf, the others at 0 */
+    const float f = __builtin_amdgcn_exp2f(m - mb);
+    float sum = 0.0f;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        t[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(t[i], cc, -mb));
+        sum += t[i];
+    }
+    l = __builtin_fmaf(l, f, sum);
+    m = mn;
+    return f;
+}
+
 /*
  * Few query rows: a workgroup takes one tile of R rows of one (sequence, cache
  * head) and one of nsplit ranges of its blocks, its four waves the pieces of
@@ -326,15 +367,14 @@ __device__ __forceinline__ Span row_span(const coli_kv_attn& a, const SeqBounds&
  * Keys and values go straight from memory to the matrix cores' registers (a
  * wave reads whole lines of a page).  The next piece's keys are in flight
  * under this piece's softmax and value product, its values under the next
- * scores.  A piece is a block, or half a block where head_dim exceeds 128 and
- * the registers hold no more.
+ * scores.  A piece is a block, or half a block where the registers hold no more.
  */
 template <typename T, int R, int D>
-__global__ __launch_bounds__(256, 2) void kv_attention_split(AttnArgs g)
+__global__ __launch_bounds__(256, R == 32 && D > 128 ? 1 : 2) void kv_attention_split(AttnArgs g)
 {
     using TL = Tile<R>;
     constexpr int ND = sizeof(T) == 4 ? 3 : 2, NP = sizeof(T) == 4 ? 3 : 1;
-    constexpr int NU = D <= 128 ? 2 : 1; /* halves of a block in a piece */
+    constexpr int NU = D <= (R == 16 ? 128 : 64) ? 2 : 1; /* halves of a block in a piece */
     constexpr int HS = R / 2;            /* scores of a half in a lane */
     constexpr int KN = D / 32, VN = D / R, DT = D / R, NA = TL::kAcc;
     __shared__ float so[2][DT * NA][64];
@@ -358,8 +398,9 @@ __global__ __launch_bounds__(256, 2) void kv_attention_split(AttnArgs g)
             const int64_t tok = (int64_t)q.row0 + qi;
             v4i dig[ND][D / TL::kDims];
             const float unit_q =
-                load_query<T, R, D, ND>((const T*)g.a.q + tok * g.a.q_stride + (int64_t)head * D, live, lg, dig) *
-                (g.a.scale * kLog2e);
+                load_query<T, R, D, ND>((const T*)g.a.q + tok * g.a.q_stride + (int64_t)head * D, live,
+                                        g.a.scale < 0.0f, lg, dig) *
+                (fabsf(g.a.scale) * kLog2e);
             const Span sp = row_span(g.a, q, qi, (int)(r0 / G), (int)((r0 + live_rows - 1) / G));
             /* pieces of 32 NU tokens */
             constexpr int PT = 32 * NU;
@@ -413,33 +454,9 @@ __global__ __launch_bounds__(256, 2) void kv_attention_split(AttnArgs g)
                     const float c = unit_q * ks;
                     const int base = p * PT;
                     const bool missing = page < 0;
-                    if (missing || base + PT > sp.all_end || base < sp.all_begin) {
-                        const int e0 = missing ? 0 : sp.end;
-#pragma unroll
-                        for (int i = 0; i < NU * HS; ++i) {
-                            const int j = base + i / HS * 32 + TL::token(i % HS, lg);
-                            t[i] = j < e0 && j >= sp.begin ? t[i] * c : -__builtin_inff();
-                        }
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < NU * HS; ++i)
-                            t[i] *= c;
-                    }
-                    float mx = t[0];
-#pragma unroll
-                    for (int i = 1; i < NU * HS; ++i)
-                        mx = fmaxf(mx, t[i]);
-                    const float mn = fmaxf(m, row_max<R>(mx));
-                    const float mb = mn == -__builtin_inff() ? 0.0f : mn;
-                    const float f = __builtin_amdgcn_exp2f(m - mb);
-                    float sum = 0.0f;
-#pragma unroll
-                    for (int i = 0; i < NU * HS; ++i) {
-                        t[i] = __builtin_amdgcn_exp2f(t[i] - mb);
-                        sum += t[i];
-                    }
-                    l = __builtin_fmaf(l, f, sum);
-                    m = mn;
+                    if (missing || base + PT > sp.all_end || base < sp.all_begin)
+                        mask_tile<R, NU>(t, base, missing ? 0 : sp.end, sp.begin, lg);
+                    const float f = softmax_tile<R, NU * HS>(t, c, m, l);
                     if (__any(f != 1.0f)) {
 #pragma unroll
                         for (int d = 0; d < DT; ++d)
@@ -535,6 +552,174 @@ __global__ __launch_bounds__(256, 2) void kv_attention_split(AttnArgs g)
     }
 }
 
+/*
+ * Many query rows: a workgroup takes 128 rows of one (sequence, cache head), 32
+ * to a wave, and a range of its blocks.  A block's codes travel to LDS under
+ * the block before it; its values are turned into bf16 once there for the four
+ * waves, which read both as they lie (a wave's operand is one run of 1 KB).
+ * Bound by the VALU: about 11 instructions per score and row, the exponential
+ * four times the others, beside 33 + 32 cycles of the matrix cores for 64
+ * scores.
+ */
+constexpr int kTileRows = 128;
+
+template <typename T, int D>
+__global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void kv_attention_tile(AttnArgs g)
+{
+    using TL = Tile<32>;
+    constexpr int ND = sizeof(T) == 4 ? 3 : 2, NP = sizeof(T) == 4 ? 3 : 1;
+    constexpr int KS = D / 32, DT = D / 32, PB = kBlk * D; /* bytes of a block's keys, or values */
+    extern __shared__ __align__(1024) uint8_t lds[];       /* two blocks' codes, one block's values in bf16 */
+    uint8_t* const vb = lds + 4 * PB;
+    const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6, lg = lane >> 5, col = lane & 31;
+    const int H = g.c.n_heads, G = g.group;
+    for (int64_t unit = xcd_unit(); unit < g.units; unit += gridDim.x) {
+        /* heads outermost (an XCD's share has every sequence), then sequences, the
+         * longest row tiles first */
+        const int split = (int)(unit % g.nsplit);
+        int64_t r = unit / g.nsplit;
+        const int rt0 = g.row_tiles - 1 - (int)(r % g.row_tiles);
+        r /= g.row_tiles;
+        const int s = (int)(r % g.b.n_seq), hk = (int)(r / g.b.n_seq);
+        const SeqBounds q = seq_bounds(g.b, s);
+        const int64_t n_rows = (int64_t)q.q_len * G;
+        for (int64_t r0 = (int64_t)rt0 * kTileRows; r0 < n_rows; r0 += (int64_t)g.row_tiles * kTileRows) {
+            const int live_rows = (int)min(n_rows - r0, (int64_t)kTileRows);
+            const int mine = wv * 32 + col;
+            const int64_t row = r0 + min(mine, live_rows - 1);
+            const int qi = (int)(row / G), head = hk * G + (int)(row % G);
+            const bool live = mine < live_rows;
+            const int64_t tok = (int64_t)q.row0 + qi;
+            v4i dig[ND][KS];
+            const float unit_q = load_query<T, 32, D, ND>((const T*)g.a.q + tok * g.a.q_stride + (int64_t)head * D, live,
+                                                          g.a.scale < 0.0f, lg, dig) *
+                                 (fabsf(g.a.scale) * kLog2e);
+            /* the workgroup's blocks, and what this wave's rows see of them */
+            const Span wg = row_span(g.a, q, qi, (int)(r0 / G), (int)((r0 + live_rows - 1) / G));
+            const int64_t w0 = r0 + min(wv * 32, live_rows - 1), w1 = r0 + min(wv * 32 + 31, live_rows - 1);
+            const Span sp = row_span(g.a, q, qi, (int)(w0 / G), (int)(w1 / G));
+            const int p_lo = wg.any_begin / kBlk, p_hi = (wg.any_end + kBlk - 1) / kBlk;
+            const int per = (max(p_hi - p_lo, 0) + g.nsplit - 1) / g.nsplit;
+            const int p0 = min(p_lo + split * per, p_hi), p1 = min(p0 + per, p_hi);
+
+            float m = -__builtin_inff(), l = 0.0f;
+            v16f acc[DT];
+#pragma unroll
+            for (int d = 0; d < DT; ++d)
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    acc[d][i] = 0.0f;
+
+            auto page_at = [&](int p) {
+                return __builtin_amdgcn_readfirstlane(page_of(g.b, g.c.n_pages, s, min(p, p1 - 1)));
+            };
+            auto at = [&](int page) { return (int64_t)max(page, 0) * H + hk; };
+            auto fetch = [&](int page, int p) {
+                uint8_t* buf = lds + ((p - p0) & 1) * (2 * PB);
+                const int8_t *k = g.c.k + at(page) * PB, *v = g.c.v + at(page) * PB;
+#pragma unroll
+                for (int i = 0; i < PB / 4096; ++i) {
+                    const int o = (i * 4 + wv) * 1024;
+                    to_lds(k + o + lane * 16, buf + o);
+                    to_lds(v + o + lane * 16, buf + PB + o);
+                }
+            };
+            if (p0 < p1) {
+                int page = page_at(p0), next = page_at(p0 + 1);
+                fetch(page, p0);
+                float ks = g.c.k_scale[at(page)], vs = g.c.v_scale[at(page)];
+                for (int p = p0; p < p1; ++p) {
+                    const int after = page_at(p + 2);
+                    const float ks_next = g.c.k_scale[at(next)], vs_next = g.c.v_scale[at(next)];
+                    /* this block has arrived; every wave has left the other buffer and vb */
+                    arrive_all<0>();
+                    if (p + 1 < p1)
+                        fetch(next, p + 1);
+                    const uint8_t* buf = lds + ((p - p0) & 1) * (2 * PB);
+                    /* values to bf16: sixteen tokens of a dim are two operands of it */
+#pragma unroll
+                    for (int i = 0; i < PB / 4096; ++i) {
+                        const int u = i * 256 + threadIdx.x, half = u / (2 * D), c = u / 2 % D, hh = u & 1;
+                        const v4i w = *(const v4i*)(buf + PB + u * 16);
+                        uint8_t* o = vb + (half * 2 * DT + c / 32) * 1024 + hh * 512 + c % 32 * 16;
+                        *(v8b*)o = codes_bf16(w[0], w[1]);
+                        *(v8b*)(o + DT * 1024) = codes_bf16(w[2], w[3]);
+                    }
+                    const int base = p * kBlk;
+                    const bool missing = page < 0;
+                    const bool active = !missing && base < sp.any_end && base + kBlk > sp.any_begin;
+                    float t[32], f = 1.0f;
+                    if (active) {
+#pragma unroll
+                        for (int u = 0; u < 2; ++u) {
+                            v4i k[KS];
+#pragma unroll
+                            for (int x = 0; x < KS; ++x)
+                                k[x] = *(const v4i*)(buf + (u * KS + x) * 1024 + lane * 16);
+                            score_half<32, D, ND>(k, dig, t + 16 * u);
+                        }
+                        if (base + kBlk > sp.all_end || base < sp.all_begin)
+                            mask_tile<32, 2>(t, base, sp.end, sp.begin, lg);
+                        f = softmax_tile<32, 32>(t, unit_q * ks, m, l);
+                        if (__any(f != 1.0f)) {
+#pragma unroll
+                            for (int d = 0; d < DT; ++d)
+#pragma unroll
+                                for (int i = 0; i < 16; ++i)
+                                    acc[d][i] *= f;
+                        }
+                    }
+                    /* every wave's values are in vb (the next block's loads stay in flight) */
+                    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+                    if (active) {
+#pragma unroll
+                        for (int x = 0; x < 4; ++x) {
+                            v8b term[NP];
+                            split_bf16<NP>(t + 8 * x, vs, term);
+#pragma unroll
+                            for (int d = 0; d < DT; ++d) {
+                                const v8b a = *(const v8b*)(vb + (x * DT + d) * 1024 + lane * 16);
+#pragma unroll
+                                for (int e = 0; e < NP; ++e)
+                                    acc[d] = TL::mfma(a, term[e], acc[d]);
+                            }
+                        }
+                    }
+                    page = next;
+                    next = after;
+                    ks = ks_next;
+                    vs = vs_next;
+                }
+                __syncthreads(); /* the buffers are free for the next tile of rows */
+            }
+            l = row_sum<32>(l);
+            if (live) {
+                const bool whole = g.nsplit == 1;
+                const float inv = !whole ? 1.0f : l == 0.0f ? 0.0f : 1.0f / l;
+                const int64_t o_at = ((int64_t)split * g.b.n_tokens + tok) * g.a.n_heads + head;
+#pragma unroll
+                for (int d = 0; d < DT; ++d)
+#pragma unroll
+                    for (int i = 0; i < 16; i += 4) {
+                        const int dim = d * 32 + TL::dim(i, lg);
+                        const float4 v =
+                            make_float4(acc[d][i] * inv, acc[d][i + 1] * inv, acc[d][i + 2] * inv, acc[d][i + 3] * inv);
+                        if (whole)
+                            store4((T*)g.a.out + tok * g.a.out_stride + (int64_t)head * D + dim, v);
+                        else
+                            store4(g.part_o + o_at * D + dim, v);
+                    }
+                if (lg == 0) {
+                    if (!whole)
+                        *(float2*)(g.part_ml + 2 * o_at) = make_float2(m, l);
+                    else if (g.a.lse)
+                        g.a.lse[tok * g.a.n_heads + head] = l == 0.0f ? -__builtin_inff() : m * kLn2 + logf(l);
+                }
+            }
+        }
+    }
+}
+
 /* Joins the ranges' partial sums, W waves per (token, head): wave w takes the
  * ranges w, w + W, ... in order, four rows of partial sums in flight, and the
  * waves' sums are added in wave order. */
@@ -603,8 +788,8 @@ __global__ __launch_bounds__(256) void kv_attention_join(AttnArgs g)
 constexpr size_t kPartAlign = 256;
 
 /* How a call is cut: rows of a tile, tiles by the longest expected query run,
- * ranges so that about kTargetUnits workgroups run, each wave with a block at
- * least. */
+ * ranges so that about kTargetUnits workgroups run, each wave (kv_attention_tile:
+ * each workgroup) with a few blocks at least. */
 struct Plan {
     int rows, row_tiles, nsplit;
     int64_t units;
@@ -620,12 +805,14 @@ Plan plan_attention(const coli_kv_cache& c, const coli_kv_batch& b, const coli_k
     Plan p;
     const int G = a.n_heads / c.n_heads;
     const int64_t rows = (int64_t)max(1, min(b.max_q, b.n_tokens)) * G;
-    p.rows = rows <= 16 || a.type == COLI_F32 ? 16 : 32;
+    p.rows = rows > 32 ? kTileRows : rows <= 16 || a.type == COLI_F32 ? 16 : 32;
     p.row_tiles = (int)min((rows + p.rows - 1) / p.rows, (int64_t)1 << 20);
     const int64_t units = (int64_t)max(b.n_seq, 1) * p.row_tiles * c.n_heads;
     const int64_t seen = a.window > 0 ? min((int64_t)a.max_kv, (int64_t)a.window + b.max_q) : a.max_kv;
-    const int64_t blocks = (seen + kBlk - 1) / kBlk;
-    p.nsplit = (int)max((int64_t)1, min(min((kTargetUnits + units - 1) / units, (blocks + 3) / 4), (int64_t)kMaxSplit));
+    const int64_t blocks = (seen + kBlk - 1) / kBlk, target = p.rows == kTileRows ? 512 : kTargetUnits;
+    p.nsplit = (int)max((int64_t)1, min(min((target + units - 1) / units, (blocks + 3) / 4), (int64_t)kMaxSplit));
+    if (p.rows == kTileRows && units >= 256)
+        p.nsplit = 1;
     if ((int64_t)b.n_tokens * a.n_heads > kMaxSplitRows)
         p.nsplit = 1;
     p.units = units * p.nsplit;
@@ -638,11 +825,22 @@ Plan plan_attention(const coli_kv_cache& c, const coli_kv_batch& b, const coli_k
 template <typename T, int D>
 hipError_t launch(const AttnArgs& g, int rows, hipStream_t s)
 {
-    const uint32_t grid = (uint32_t)min(g.units, (int64_t)1 << 20);
-    if (rows == 16)
-        hipLaunchKernelGGL((kv_attention_split<T, 16, D>), dim3(grid), dim3(256), 0, s, g);
-    else
-        hipLaunchKernelGGL((kv_attention_split<bf16, 32, D>), dim3(grid), dim3(256), 0, s, g);
+    if (rows == kTileRows) {
+        constexpr int bytes = 4 * kBlk * D + 2 * kBlk * D;
+        if (bytes > 64 * 1024) {
+            const hipError_t e = hipFuncSetAttribute((const void*)kv_attention_tile<T, D>,
+                                                     hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+            if (e != hipSuccess)
+                return e;
+        }
+        hipLaunchKernelGGL((kv_attention_tile<T, D>), dim3((uint32_t)min((g.units + 7) / 8 * 8, (int64_t)1 << 20)), dim3(256), bytes, s, g);
+    } else {
+        const uint32_t grid = (uint32_t)min(g.units, (int64_t)1 << 20);
+        if (rows == 16)
+            hipLaunchKernelGGL((kv_attention_split<T, 16, D>), dim3(grid), dim3(256), 0, s, g);
+        else
+            hipLaunchKernelGGL((kv_attention_split<bf16, 32, D>), dim3(grid), dim3(256), 0, s, g);
+    }
     if (g.nsplit > 1) {
         const int64_t n = (int64_t)g.b.n_tokens * g.a.n_heads;
         if (g.nsplit <= 8)

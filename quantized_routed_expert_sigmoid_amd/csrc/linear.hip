@@ -301,39 +301,6 @@ __global__ __launch_bounds__(256) void linear_expand(LinearArgs a, uint8_t* xh, 
     }
 }
 
-/* Sixteen bytes per lane from memory into LDS at dst + 16 lane (dst uniform).
- * Written out because the compiler, which cannot tell the buffers apart, would
- * wait for every such load before the next LDS read; whoever uses it waits
- * himself (arrive_all).  M0 holds the LDS address; no other instruction of
- * these kernels takes M0. */
-__device__ __forceinline__ void to_lds(const void* src, void* dst)
-{
-    const uint32_t at = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) void*)dst;
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(
-                     __builtin_amdgcn_readfirstlane(at)),
-                 "v"(src)
-                 : "memory");
-}
-
-/* Four bytes per lane, at dst + 4 lane. */
-__device__ __forceinline__ void word_to_lds(const void* src, void* dst)
-{
-    const uint32_t at = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) void*)dst;
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off" ::"s"(
-                     __builtin_amdgcn_readfirstlane(at)),
-                 "v"(src)
-                 : "memory");
-}
-
-/* Waits until at most LEFT of this wave's loads are outstanding, then for the
- * workgroup: past it every wave's earlier loads have arrived, and every wave
- * has left the buffer that is loaded next. */
-template <int LEFT>
-__device__ __forceinline__ void arrive_all()
-{
-    asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"(LEFT) : "memory");
-}
-
 __device__ __forceinline__ v2h as_h2(uint32_t u)
 {
     v2h r;
@@ -393,13 +360,6 @@ __device__ __forceinline__ TileAt tile_at(int id, int n_tiles, int t_tiles)
     constexpr int GT = 8;
     const int band = id / (GT * n_tiles), in = id % (GT * n_tiles), wide = min(GT, t_tiles - band * GT);
     return TileAt{in / wide * ROWS, (band * GT + in % wide) * TOKS};
-}
-
-/* Workgroups go to the eight XCDs in turn; each XCD takes a contiguous run of
- * units, so that what it works on at a time shares its L2. */
-__device__ __forceinline__ int xcd_unit()
-{
-    return (int)(blockIdx.x & 7) * ((int)gridDim.x >> 3) + (int)(blockIdx.x >> 3);
 }
 
 /* One uniform branch on the activation for N values. */
@@ -475,7 +435,7 @@ __global__ __launch_bounds__(256, 2) void linear_tiles(LinearArgs a, TileArgs ta
     extern __shared__ __align__(1024) uint8_t lds[];
     const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6, h = lane >> 5, col = lane & 31;
     const int wn = wv & 1, wt = wv >> 1;
-    const int unit = xcd_unit();
+    const int unit = (int)xcd_unit();
     if (unit >= ta.n_tiles * ta.t_tiles)
         return;
     const TileAt wg = tile_at<kTileN, 64 * TT>(unit, ta.n_tiles, ta.t_tiles);
@@ -699,7 +659,7 @@ __global__ __launch_bounds__(256, 2) void linear_fold(LinearArgs a, TileArgs ta)
     extern __shared__ __align__(1024) uint8_t lds[];
     const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6, h = lane >> 5, col = lane & 31;
 
-    const int unit = xcd_unit(), total = ta.n_tiles * ta.t_tiles;
+    const int unit = (int)xcd_unit(), total = ta.n_tiles * ta.t_tiles;
     if (unit >= total * ta.splits)
         return;
     const int id = unit / ta.splits, split = unit % ta.splits;
