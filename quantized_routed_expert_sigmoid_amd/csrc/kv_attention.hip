@@ -255,14 +255,14 @@ __device__ __forceinline__ v8b codes_bf16(int w0, int w1)
     return v;
 }
 
-/* Eight weights times w as NP bf16 terms. */
+/* Eight weights as NP bf16 terms. */
 template <int NP>
-__device__ __forceinline__ void split_bf16(const float* p, float w, v8b (&term)[NP])
+__device__ __forceinline__ void split_bf16(const float* p, v8b (&term)[NP])
 {
     float x[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-        x[i] = p[i] * w;
+        x[i] = p[i];
 #pragma unroll
     for (int e = 0; e < NP; ++e) {
         uint32_t r[4];
@@ -330,12 +330,14 @@ __device__ __forceinline__ void mask_tile(float* t, int base, int end, int begin
     }
 }
 
-/* Scores t in units of c (c >= 0, one per row) become 2^(t c - m) with m raised
- * to the largest; l, the lane's sum, takes them up; returns the factor of what
- * was summed before.  The scale goes into the exponent's fma: the largest of t
- * is the largest of t c. */
+/* Scores t in units of c (c >= 0, one per row) become w 2^(t c - m), w being the
+ * block's value scale, with m raised to the largest; l, the lane's sum, takes
+ * them up without w; returns the factor of what was summed before.  Both scales
+ * go into the exponent's fma: the largest of t is the largest of t c, and w is
+ * 2^log2(w), whose rounding (2^-21) weighs a block's sums and its share of l
+ * alike.  A w that is not positive is multiplied in afterwards. */
 template <int R, int N>
-__device__ __forceinline__ float softmax_tile(float* t, float c, float& m, float& l)
+__device__ __forceinline__ float softmax_tile(float* t, float c, float w, float& m, float& l)
 {
     float mx = t[0];
 #pragma unroll
@@ -347,14 +349,21 @@ __device__ __forceinline__ float softmax_tile(float* t, float c, float& m, float
     const float mb = mn == -__builtin_inff() ? 0.0f : mn;
     const float cc = c == 0.0f ? 0x1p-126f : c; /* hidden tokens stay at -inf, the others at 0 */
     const float f = __builtin_amdgcn_exp2f(m - mb);
+    const bool plus = w >= 0x1p-100f; /* uniform */
+    const float off = (plus ? __builtin_amdgcn_logf(w) : 0.0f) - mb, back = plus ? 1.0f / w : 1.0f;
     float sum = 0.0f;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-        t[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(t[i], cc, -mb));
+        t[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(t[i], cc, off));
         sum += t[i];
     }
-    l = __builtin_fmaf(l, f, sum);
+    l = __builtin_fmaf(l, f, sum * back);
     m = mn;
+    if (!plus) {
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            t[i] *= w;
+    }
     return f;
 }
 
@@ -456,7 +465,7 @@ __global__ __launch_bounds__(256, R == 32 && D > 128 ? 1 : 2) void kv_attention_
                     const bool missing = page < 0;
                     if (missing || base + PT > sp.all_end || base < sp.all_begin)
                         mask_tile<R, NU>(t, base, missing ? 0 : sp.end, sp.begin, lg);
-                    const float f = softmax_tile<R, NU * HS>(t, c, m, l);
+                    const float f = softmax_tile<R, NU * HS>(t, c, missing ? 0.0f : vs, m, l);
                     if (__any(f != 1.0f)) {
 #pragma unroll
                         for (int d = 0; d < DT; ++d)
@@ -464,12 +473,11 @@ __global__ __launch_bounds__(256, R == 32 && D > 128 ? 1 : 2) void kv_attention_
                             for (int i = 0; i < NA; ++i)
                                 acc[d][i] *= f;
                     }
-                    const float w = missing ? 0.0f : vs;
 #pragma unroll
                     for (int x = 0; x < NU * HS / 8; ++x) {
                         constexpr int per_half = HS / 8; /* value operands of a half */
                         v8b term[NP];
-                        split_bf16<NP>(t + 8 * x, w, term);
+                        split_bf16<NP>(t + 8 * x, term);
 #pragma unroll
                         for (int d = 0; d < DT; ++d) {
                             const auto& vv = vreg[x / per_half][d];
@@ -555,8 +563,9 @@ __global__ __launch_bounds__(256, R == 32 && D > 128 ? 1 : 2) void kv_attention_
 /*
  * Many query rows: a workgroup takes 128 rows of one (sequence, cache head), 32
  * to a wave, and a range of its blocks.  A block's codes travel to LDS under
- * the block before it; its values are turned into bf16 once there for the four
- * waves, which read both as they lie (a wave's operand is one run of 1 KB).
+ * the blocks before it, and its values are turned into bf16 there once for the
+ * four waves, one block ahead; the waves read both as they lie (an operand is
+ * one run of 1 KB).
  * Bound by the VALU: about 11 instructions per score and row, the exponential
  * four times the others, beside 33 + 32 cycles of the matrix cores for 64
  * scores.
@@ -569,8 +578,7 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void kv_attention_tile(AttnA
     using TL = Tile<32>;
     constexpr int ND = sizeof(T) == 4 ? 3 : 2, NP = sizeof(T) == 4 ? 3 : 1;
     constexpr int KS = D / 32, DT = D / 32, PB = kBlk * D; /* bytes of a block's keys, or values */
-    extern __shared__ __align__(1024) uint8_t lds[];       /* two blocks' codes, one block's values in bf16 */
-    uint8_t* const vb = lds + 4 * PB;
+    extern __shared__ __align__(1024) uint8_t lds[];       /* of two blocks each: keys, values, values in bf16 */
     const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6, lg = lane >> 5, col = lane & 31;
     const int H = g.c.n_heads, G = g.group;
     for (int64_t unit = xcd_unit(); unit < g.units; unit += gridDim.x) {
@@ -614,42 +622,50 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void kv_attention_tile(AttnA
                 return __builtin_amdgcn_readfirstlane(page_of(g.b, g.c.n_pages, s, min(p, p1 - 1)));
             };
             auto at = [&](int page) { return (int64_t)max(page, 0) * H + hk; };
-            auto fetch = [&](int page, int p) {
-                uint8_t* buf = lds + ((p - p0) & 1) * (2 * PB);
-                const int8_t *k = g.c.k + at(page) * PB, *v = g.c.v + at(page) * PB;
+            auto fetch = [&](const int8_t* from, uint8_t* to) {
 #pragma unroll
                 for (int i = 0; i < PB / 4096; ++i) {
                     const int o = (i * 4 + wv) * 1024;
-                    to_lds(k + o + lane * 16, buf + o);
-                    to_lds(v + o + lane * 16, buf + PB + o);
+                    to_lds(from + o + lane * 16, to + o);
+                }
+            };
+            auto fetch_k = [&](int page, int p) { fetch(g.c.k + at(page) * PB, lds + (p & 1) * PB); };
+            auto fetch_v = [&](int page, int p) { fetch(g.c.v + at(page) * PB, lds + (2 + (p & 1)) * PB); };
+            /* values to bf16: sixteen tokens of a dim are two operands of it */
+            auto convert = [&](int p) {
+                const uint8_t* raw = lds + (2 + (p & 1)) * PB;
+                uint8_t* vb = lds + (4 + 2 * (p & 1)) * PB;
+#pragma unroll
+                for (int i = 0; i < PB / 4096; ++i) {
+                    const int u = i * 256 + threadIdx.x, half = u / (2 * D), c = u / 2 % D, hh = u & 1;
+                    const v4i w = *(const v4i*)(raw + u * 16);
+                    uint8_t* o = vb + (half * 2 * DT + c / 32) * 1024 + hh * 512 + c % 32 * 16;
+                    *(v8b*)o = codes_bf16(w[0], w[1]);
+                    *(v8b*)(o + DT * 1024) = codes_bf16(w[2], w[3]);
                 }
             };
             if (p0 < p1) {
-                int page = page_at(p0), next = page_at(p0 + 1);
-                fetch(page, p0);
+                int page = page_at(p0), page1 = page_at(p0 + 1), page2 = page_at(p0 + 2);
+                fetch_k(page, p0);
+                fetch_v(page, p0);
                 float ks = g.c.k_scale[at(page)], vs = g.c.v_scale[at(page)];
+                arrive_all<0>();
+                fetch_v(page1, p0 + 1);
+                convert(p0);
                 for (int p = p0; p < p1; ++p) {
-                    const int after = page_at(p + 2);
-                    const float ks_next = g.c.k_scale[at(next)], vs_next = g.c.v_scale[at(next)];
-                    /* this block has arrived; every wave has left the other buffer and vb */
+                    const int page3 = page_at(p + 3);
+                    const float ks_next = g.c.k_scale[at(page1)], vs_next = g.c.v_scale[at(page1)];
+                    /* this block's keys and the next one's values have arrived, this one's
+                     * are converted; what is written next was left before this point */
                     arrive_all<0>();
-                    if (p + 1 < p1)
-                        fetch(next, p + 1);
-                    const uint8_t* buf = lds + ((p - p0) & 1) * (2 * PB);
-                    /* values to bf16: sixteen tokens of a dim are two operands of it */
-#pragma unroll
-                    for (int i = 0; i < PB / 4096; ++i) {
-                        const int u = i * 256 + threadIdx.x, half = u / (2 * D), c = u / 2 % D, hh = u & 1;
-                        const v4i w = *(const v4i*)(buf + PB + u * 16);
-                        uint8_t* o = vb + (half * 2 * DT + c / 32) * 1024 + hh * 512 + c % 32 * 16;
-                        *(v8b*)o = codes_bf16(w[0], w[1]);
-                        *(v8b*)(o + DT * 1024) = codes_bf16(w[2], w[3]);
-                    }
+                    fetch_k(page1, p + 1);
+                    fetch_v(page2, p + 2);
+                    convert(p + 1);
+                    const uint8_t* buf = lds + (p & 1) * PB;
+                    const uint8_t* vb = lds + (4 + 2 * (p & 1)) * PB;
                     const int base = p * kBlk;
-                    const bool missing = page < 0;
-                    const bool active = !missing && base < sp.any_end && base + kBlk > sp.any_begin;
-                    float t[32], f = 1.0f;
-                    if (active) {
+                    if (page >= 0 && base < sp.any_end && base + kBlk > sp.any_begin) {
+                        float t[32];
 #pragma unroll
                         for (int u = 0; u < 2; ++u) {
                             v4i k[KS];
@@ -660,7 +676,7 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void kv_attention_tile(AttnA
                         }
                         if (base + kBlk > sp.all_end || base < sp.all_begin)
                             mask_tile<32, 2>(t, base, sp.end, sp.begin, lg);
-                        f = softmax_tile<32, 32>(t, unit_q * ks, m, l);
+                        const float f = softmax_tile<32, 32>(t, unit_q * ks, vs, m, l);
                         if (__any(f != 1.0f)) {
 #pragma unroll
                             for (int d = 0; d < DT; ++d)
@@ -668,14 +684,10 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void kv_attention_tile(AttnA
                                 for (int i = 0; i < 16; ++i)
                                     acc[d][i] *= f;
                         }
-                    }
-                    /* every wave's values are in vb (the next block's loads stay in flight) */
-                    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
-                    if (active) {
 #pragma unroll
                         for (int x = 0; x < 4; ++x) {
                             v8b term[NP];
-                            split_bf16<NP>(t + 8 * x, vs, term);
+                            split_bf16<NP>(t + 8 * x, term);
 #pragma unroll
                             for (int d = 0; d < DT; ++d) {
                                 const v8b a = *(const v8b*)(vb + (x * DT + d) * 1024 + lane * 16);
@@ -685,12 +697,13 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void kv_attention_tile(AttnA
                             }
                         }
                     }
-                    page = next;
-                    next = after;
+                    page = page1;
+                    page1 = page2;
+                    page2 = page3;
                     ks = ks_next;
                     vs = vs_next;
                 }
-                __syncthreads(); /* the buffers are free for the next tile of rows */
+                arrive_all<0>(); /* the buffers are free for the next tile of rows */
             }
             l = row_sum<32>(l);
             if (live) {
@@ -826,7 +839,7 @@ template <typename T, int D>
 hipError_t launch(const AttnArgs& g, int rows, hipStream_t s)
 {
     if (rows == kTileRows) {
-        constexpr int bytes = 4 * kBlk * D + 2 * kBlk * D;
+        constexpr int bytes = 8 * kBlk * D;
         if (bytes > 64 * 1024) {
             const hipError_t e = hipFuncSetAttribute((const void*)kv_attention_tile<T, D>,
                                                      hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
