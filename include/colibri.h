@@ -565,9 +565,10 @@ int colibri_add_rms_norm(const coli_norm* n, coli_stream_t stream);
  * out itself; out [S][rows] of out_type, rounded once.  Sums are held in
  * fp32; their order depends on the shape, not on the data, so equal calls give
  * equal bits, but a token's result may differ in the last bits between batch
- * sizes.  fp32 outputs take the activations exactly (to 2^-22 of their value);
- * for bf16 outputs of many tokens the activations enter the matrix cores
- * rounded to fp16 (2^-12 of their value), an eighth of the output's own rounding.
+ * sizes.  Products inside a 32-element block are exact integers; only for bf16
+ * outputs of very many tokens (one scale per row) the activations enter the
+ * matrix cores rounded to fp16 instead, 2^-12 of their value, an eighth of the
+ * output's own rounding.
  * 1 <= rows <= COLI_MAX_LINEAR_ROWS, K <= COLI_MAX_LINEAR_K, K % 32 == 0;
  * xq and W->data 16-byte, out and residual 4-byte aligned.  ws as sized by
  * colibri_linear_workspace_bytes (0: invalid arguments).  S == 0 is a no-op.
@@ -605,8 +606,9 @@ typedef struct coli_kv_cache {
  * [n_seq + 1], kv_len int32 [n_seq] and page_table int32 [n_seq][max_pages]
  * are device memory.  An entry of page_table outside [0, n_pages) is a missing
  * page: its tokens are not written, read as zeros, and are seen by no query.
- * kv_len is taken as at most max_pages * 64 and at least 0, cu_q entries as at
- * most n_tokens; rows from cu_q[n_seq] on are left as they are.  max_q is the
+ * cu_q does not decrease.  kv_len is taken as at most max_pages * 64 and at least
+ * 0, cu_q entries as at most n_tokens; rows before cu_q[0] and from cu_q[n_seq]
+ * on are left as they are.  max_q is the
  * expected longest q_len: it sizes the launch, longer ones are slower and
  * equally right.
  */
@@ -653,7 +655,7 @@ int colibri_kv_read(const coli_kv_cache* cache, const coli_kv_batch* batch, void
  * cache head h / (n_heads / cache heads).  lse: fp32 [n_tokens][n_heads] or
  * null.  max_kv is the expected longest kv_len, used like max_q.  q and out
  * 16-byte aligned, strides multiples of 8, at least n_heads * head_dim; out
- * overlaps nothing.  A query with a NaN or an infinity gets NaN in its own
+ * overlaps nothing.  scale is finite, of either sign.  A query with a NaN or an infinity gets NaN in its own
  * out and lse.  Scores, softmax statistics and sums are fp32; for bf16 the
  * weights p enter the value product rounded to bf16, for fp32 as three bf16
  * terms.  ws as sized by colibri_kv_attention_workspace_bytes for the same

@@ -9,7 +9,6 @@ refused call raises before anything is enqueued.
 
 from __future__ import annotations
 
-import contextlib
 import ctypes
 from typing import NamedTuple, Optional, Tuple
 
@@ -48,13 +47,18 @@ class KVAttnDesc(ctypes.Structure):
                 ("n_heads", _i32), ("causal", _i32), ("window", _i32), ("max_kv", _i32), ("scale", _f32)]
 
 
-_fns = None
+# the current stream's handle and the current device's number, without the
+# objects that torch.cuda builds around them (a few microseconds a call)
+_raw_stream = torch._C._cuda_getCurrentRawStream
+_current_device = torch._C._cuda_getDevice
+
+_fns = None  # (the library, its entry points)
 
 
 def _f():
     """The library's entry points with their argument types."""
     global _fns
-    L = _qre.lib()
+    L = _qre._lib or _qre.lib()
     if _fns is None or _fns[0] is not L:
         sz, ci = ctypes.c_size_t, ctypes.c_int
         for name, res, args in [
@@ -78,11 +82,6 @@ def _type(dtype: torch.dtype) -> int:
     return t
 
 
-def _need(ok, what: str):
-    if not ok:
-        raise ValueError(what)
-
-
 def _on(dev: torch.device, *tensors: Optional[torch.Tensor]):
     for t in tensors:
         if t is not None and t.device != dev:
@@ -95,28 +94,32 @@ def _dev(t: torch.Tensor) -> torch.device:
     return t.device
 
 
-def _here(dev: torch.device):
-    """The launch belongs to the tensors' device, which may not be the current one."""
-    return contextlib.nullcontext() if dev.index == torch.cuda.current_device() else torch.cuda.device(dev)
-
-
 def _at(t: Optional[torch.Tensor]):
     return None if t is None else t.data_ptr()
 
 
-def _flat(t: Optional[torch.Tensor], dtype: torch.dtype, shape, what: str):
+def _flat(t: Optional[torch.Tensor], dtype: torch.dtype, shape: tuple, what: str):
     """t is contiguous, of this type and shape (or None)."""
-    if t is not None:
-        if t.dtype != dtype:
-            raise TypeError(f"{what}: {dtype} expected, got {t.dtype}")
-        _need(tuple(t.shape) == tuple(shape), f"{what}: shape {tuple(shape)} expected, got {tuple(t.shape)}")
-        _need(t.is_contiguous(), f"{what}: contiguous tensor expected")
+    if t is None or (t.dtype == dtype and t.shape == shape and t.is_contiguous()):
+        return
+    if t.dtype != dtype:
+        raise TypeError(f"{what}: {dtype} expected, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{what}: shape {tuple(shape)} expected, got {tuple(t.shape)}")
+    raise ValueError(f"{what}: contiguous tensor expected")
 
 
 def _call(dev: torch.device, name: str, *args):
-    fn = getattr(_f(), name)
-    with _here(dev):
-        _qre._check(fn(*args, torch.cuda.current_stream(dev).cuda_stream), name)
+    """Enqueues on the current stream of the tensors' device, which may not be the current one."""
+    fn, index = getattr(_f(), name), dev.index
+    stream = _raw_stream(index)
+    if index == _current_device():
+        st = fn(*args, stream)
+    else:
+        with torch.cuda.device(dev):
+            st = fn(*args, stream)
+    if st:
+        raise _qre.ColibriError(st, name)
 
 
 # ---------------------------------------------------------------------------
@@ -141,17 +144,22 @@ def add_rms_norm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6, *,
     returned in y_dtype if that is given (the layer takes fp32), the Q8_0 codes
     and scales (what linear_q takes) unless q8 is False."""
     dev = _dev(x)
-    _need(x.dim() == 2, "x: [rows][K] expected")
+    if not (x.dim() == 2):
+        raise ValueError("x: [rows][K] expected")
     rows, K = x.shape
     xt = _type(x.dtype)
     _on(dev, weight, residual, sum_out)
     _flat(weight, torch.float32, (K,), "weight")
-    _need(rows <= 1 or x.stride(0) >= K, "x: rows that do not overlap expected")
-    _need(K == 0 or x.stride(1) == 1, "x: contiguous rows expected")
+    if not (rows <= 1 or x.stride(0) >= K):
+        raise ValueError("x: rows that do not overlap expected")
+    if not (K == 0 or x.stride(1) == 1):
+        raise ValueError("x: contiguous rows expected")
     rt, rs = xt, K
     if residual is not None:
-        _need(residual.shape == x.shape, "residual: the shape of x expected")
-        _need(residual.stride(1) == 1, "residual: contiguous rows expected")
+        if not (residual.shape == x.shape):
+            raise ValueError("residual: the shape of x expected")
+        if not (residual.stride(1) == 1):
+            raise ValueError("residual: contiguous rows expected")
         rt, rs = _type(residual.dtype), residual.stride(0) if rows > 1 else K
         if sum_out is None:
             sum_out = torch.empty(rows, K, dtype=residual.dtype, device=dev)
@@ -172,11 +180,14 @@ def add_rms_norm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6, *,
 
 def linear_workspace(bank, S: int, dtype: torch.dtype = torch.float32) -> torch.Tensor:
     """Workspace of linear_q for up to S tokens; calls that may overlap need one each."""
-    w = bank.desc()
-    n = _f().colibri_linear_workspace_bytes(ctypes.byref(w), S, _type(dtype))
+    return _linear_ws(bank.desc(), S, _type(dtype), bank.data.device)
+
+
+def _linear_ws(w, S: int, t: int, dev: torch.device) -> torch.Tensor:
+    n = _f().colibri_linear_workspace_bytes(ctypes.byref(w), S, t)
     if n == 0:
         raise _qre.ColibriError(_qre.COLI_E_INVAL, "colibri_linear_workspace_bytes")
-    return torch.empty(n, dtype=torch.uint8, device=bank.data.device)
+    return torch.empty(n, dtype=torch.uint8, device=dev)
 
 
 def linear_q(bank, xq: torch.Tensor, xd: torch.Tensor, *, bias: Optional[torch.Tensor] = None,
@@ -193,7 +204,8 @@ def linear_q(bank, xq: torch.Tensor, xd: torch.Tensor, *, bias: Optional[torch.T
     if activation not in _ACTS:
         raise ValueError(f"activation: one of {[a for a in _ACTS if a]} expected, got {activation!r}")
     w = bank.desc()
-    _need(xq.dim() == 2 and xq.shape[1] == w.K, f"xq: [S][{w.K}] expected, got {tuple(xq.shape)}")
+    if not (xq.dim() == 2 and xq.shape[1] == w.K):
+        raise ValueError(f"xq: [S][{w.K}] expected, got {tuple(xq.shape)}")
     S = xq.shape[0]
     given = out if out is not None else residual
     dtype = dtype or (given.dtype if given is not None else torch.float32)
@@ -204,12 +216,13 @@ def linear_q(bank, xq: torch.Tensor, xd: torch.Tensor, *, bias: Optional[torch.T
     _flat(bias, torch.float32, (w.rows,), "bias")
     _flat(residual, dtype, (S, w.rows), "residual")
     _flat(out, dtype, (S, w.rows), "out")
-    _need(bank.scale.dtype == torch.float32 and bank.scale.numel() == w.n_mat * w.rows *
-          (w.K // w.group if w.group else 1), "bank: one fp32 scale per row, or per group, expected")
+    if bank.scale.dtype != torch.float32 or (
+            bank.scale.numel() != w.n_mat * w.rows * (w.K // w.group if w.group else 1)):
+        raise ValueError("bank: one fp32 scale per row, or per group, expected")
     if out is None:
         out = torch.empty(S, w.rows, dtype=dtype, device=dev)
     if ws is None:
-        ws = linear_workspace(bank, S, dtype)
+        ws = _linear_ws(w, S, t, dev)
     _call(dev, "colibri_linear_q", ctypes.byref(w), xq.data_ptr(), xd.data_ptr(), S, _at(bias), _ACTS[activation],
           _at(residual), out.data_ptr(), t, ws.data_ptr(), ws.numel() * ws.element_size())
     return out
@@ -232,8 +245,8 @@ class KVCache:
                  head_dim: int):
         dev = _dev(k)
         _on(dev, v, k_scale, v_scale)
-        _need(k.dim() == 3 and k.shape[2] == KV_BLOCK * head_dim,
-              f"k: [n_pages][n_heads][{KV_BLOCK * head_dim}] expected, got {tuple(k.shape)}")
+        if not (k.dim() == 3 and k.shape[2] == KV_BLOCK * head_dim):
+            raise ValueError(f"k: [n_pages][n_heads][{KV_BLOCK * head_dim}] expected, got {tuple(k.shape)}")
         _flat(k, torch.int8, k.shape, "k")
         _flat(v, torch.int8, k.shape, "v")
         _flat(k_scale, torch.float32, k.shape[:2], "k_scale")
@@ -255,7 +268,8 @@ class KVCache:
 def _batch(cache: KVCache, page_table, cu_q, kv_len, n_tokens: int, max_q: Optional[int]) -> KVBatchDesc:
     dev = cache.k.device
     _on(dev, page_table, cu_q, kv_len)
-    _need(page_table.dim() == 2, "page_table: [n_seq][max_pages] expected")
+    if not (page_table.dim() == 2):
+        raise ValueError("page_table: [n_seq][max_pages] expected")
     n, mp = page_table.shape
     _flat(page_table, torch.int32, (n, mp), "page_table")
     _flat(cu_q, torch.int32, (n + 1,), "cu_q")
@@ -266,9 +280,10 @@ def _batch(cache: KVCache, page_table, cu_q, kv_len, n_tokens: int, max_q: Optio
 
 def _rows(t: torch.Tensor, n_heads: int, D: int, what: str) -> int:
     """Stride between the tokens of t [n_tokens][n_heads][D], whose heads lie together."""
-    _need(t.dim() == 3 and t.shape[1] == n_heads and t.shape[2] == D,
-          f"{what}: [n_tokens][{n_heads}][{D}] expected, got {tuple(t.shape)}")
-    _need(t.stride(2) == 1 and (n_heads == 1 or t.stride(1) == D), f"{what}: contiguous heads expected")
+    if not (t.dim() == 3 and t.shape[1] == n_heads and t.shape[2] == D):
+        raise ValueError(f"{what}: [n_tokens][{n_heads}][{D}] expected, got {tuple(t.shape)}")
+    if not (t.stride(2) == 1 and (n_heads == 1 or t.stride(1) == D)):
+        raise ValueError(f"{what}: contiguous heads expected")
     return t.stride(0) if t.shape[0] > 1 else n_heads * D
 
 
@@ -282,7 +297,8 @@ def kv_append(cache: KVCache, page_table: torch.Tensor, cu_q: torch.Tensor, kv_l
     H, D = cache.n_heads, cache.head_dim
     _on(cache.k.device, k, v)
     ks, vs = _rows(k, H, D, "k"), _rows(v, H, D, "v")
-    _need(k.shape[0] == v.shape[0] and k.dtype == v.dtype, "k and v: one length and type expected")
+    if not (k.shape[0] == v.shape[0] and k.dtype == v.dtype):
+        raise ValueError("k and v: one length and type expected")
     b = _batch(cache, page_table, cu_q, kv_len, k.shape[0], max_q)
     _call(cache.k.device, "colibri_kv_append", ctypes.byref(cache.desc), ctypes.byref(b), k.data_ptr(),
           v.data_ptr(), _type(k.dtype), ks, vs)
@@ -331,13 +347,15 @@ def kv_attention(cache: KVCache, page_table: torch.Tensor, cu_q: torch.Tensor, k
     row's sum.  max_q and max_kv are the expected longest lengths (they shape
     the launch, not the result).  ws: see kv_attention_workspace."""
     dev, D = cache.k.device, cache.head_dim
-    _need(q.dim() == 3, "q: [n_tokens][n_heads][head_dim] expected")
+    if not (q.dim() == 3):
+        raise ValueError("q: [n_tokens][n_heads][head_dim] expected")
     T, H = q.shape[0], q.shape[1]
     qs = _rows(q, H, D, "q")
     _on(dev, q, out, lse, ws)
     if out is None:
         out = torch.empty(T, H, D, dtype=q.dtype, device=dev)
-    _need(out.shape == q.shape and out.dtype == q.dtype, "out: the shape and type of q expected")
+    if not (out.shape == q.shape and out.dtype == q.dtype):
+        raise ValueError("out: the shape and type of q expected")
     os = _rows(out, H, D, "out")
     _flat(lse, torch.float32, (T, H), "lse")
     b = _batch(cache, page_table, cu_q, kv_len, T, max_q)

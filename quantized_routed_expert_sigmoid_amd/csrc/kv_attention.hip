@@ -415,7 +415,8 @@ __global__ __launch_bounds__(256, R == 32 && D > 128 ? 1 : 2) void kv_attention_
             constexpr int PT = 32 * NU;
             const int p_lo = sp.any_begin / PT, p_hi = (sp.any_end + PT - 1) / PT;
             const int per = (max(p_hi - p_lo, 0) + g.nsplit - 1) / g.nsplit;
-            const int p0 = min(p_lo + split * per, p_hi), p1 = min(p0 + per, p_hi);
+            const int p0 = __builtin_amdgcn_readfirstlane(min(p_lo + split * per, p_hi));
+            const int p1 = __builtin_amdgcn_readfirstlane(min(p0 + per, p_hi));
 
             float m = -__builtin_inff(), l = 0.0f;
             typename TL::Acc acc[DT];
@@ -446,7 +447,7 @@ __global__ __launch_bounds__(256, R == 32 && D > 128 ? 1 : 2) void kv_attention_
                 for (int u = 0; u < NU; ++u)
                     TL::template load_v<D>(b + u * 32 * D, col, lg, vreg[u]);
             };
-            int p = p0 + wv;
+            int p = __builtin_amdgcn_readfirstlane(p0 + wv);
             if (p < p1) {
                 int page = page_at(p), next = page_at(p + 4);
                 load_k(page, p);
@@ -608,7 +609,8 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void kv_attention_tile(AttnA
             const Span sp = row_span(g.a, q, qi, (int)(w0 / G), (int)(w1 / G));
             const int p_lo = wg.any_begin / kBlk, p_hi = (wg.any_end + kBlk - 1) / kBlk;
             const int per = (max(p_hi - p_lo, 0) + g.nsplit - 1) / g.nsplit;
-            const int p0 = min(p_lo + split * per, p_hi), p1 = min(p0 + per, p_hi);
+            const int p0 = __builtin_amdgcn_readfirstlane(min(p_lo + split * per, p_hi));
+            const int p1 = __builtin_amdgcn_readfirstlane(min(p0 + per, p_hi));
 
             float m = -__builtin_inff(), l = 0.0f;
             v16f acc[DT];

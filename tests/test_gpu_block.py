@@ -389,6 +389,47 @@ def test_attention_bad_query_stays_alone(qre, q_len, dtype):
     assert torch.equal(out[:, Hq:][~bad], clean[~bad]) and bool((out[:, :Hq] == 0).all())
 
 
+@pytest.mark.parametrize("q_len", [1, 4, 40])
+@pytest.mark.parametrize("scale", [-0.2, 0.0])
+def test_attention_scale_of_any_sign(qre, q_len, scale):
+    g, codes, scales, seqs, cache = make_cache(qre, [(q_len, 150), (q_len, q_len)], 1, 64, "sign")
+    kval, vval = (ref.page_values(c, s, at) for c, s, at in zip(codes, scales, ref.page_bytes(64)))
+    for dtype in (F32, BF16):
+        q = torch.randn(seqs.rows, 8, 64, generator=g).to(dtype)
+        want, lse, sb, vb = ref.attention(kval, vval, seqs, q, scale)
+        got_lse = torch.zeros(seqs.rows, 8, device="cuda")
+        got = qre.kv_attention(cache, *dev(seqs), q.cuda(), scale=scale, lse=got_lse)
+        within(got, want, ref.attention_tol(want, sb, vb, dtype), "out")
+        within(got_lse, lse, ref.lse_tol(sb, lse, dtype), "lse")
+
+
+@pytest.mark.parametrize("q_len", [2, 50])
+def test_lengths_beyond_their_bounds(qre, q_len):
+    """kv_len above the table's capacity counts as the capacity, below zero as zero; cu_q above the rows is cut;
+    rows before the first sequence stay as they were."""
+    D, H, Hq = 64, 1, 8
+    g, codes, scales, seqs, cache = make_cache(qre, [(q_len, 192), (q_len, 100)], H, D, "bounds", extra_pages=0)
+    kval, vval = (ref.page_values(c, s, at) for c, s, at in zip(codes, scales, ref.page_bytes(D)))
+    rows = 2 * q_len
+    q = torch.randn(rows + 1, Hq, D, generator=g)
+    table = seqs.table.cuda()
+    cu = torch.tensor([1, q_len + 1, 10 ** 6], dtype=torch.int32).cuda()
+    kv = torch.tensor([10 ** 9, -7], dtype=torch.int32).cuda()
+    out = torch.full((rows + 1, Hq, D), 5.0, device="cuda")
+    for max_kv in (192, 1, None):
+        qre.kv_attention(cache, table, cu, kv, q.cuda(), out=out, max_kv=max_kv)
+        s2 = ref.Seqs([(q_len, 192), (q_len, 0)], seqs.table)
+        want, _, sb, vb = ref.attention(kval, vval, s2, q[1:], D ** -0.5)
+        within(out[1:], want, ref.attention_tol(want, sb, vb, F32), "cut")
+        assert bool((out[0] == 5.0).all())
+    k, v = qre.kv_read(cache, table, cu, kv, rows + 1)
+    assert bool((k[q_len + 1:] == 0).all())
+    before = cache.k.clone()
+    qre.kv_append(cache, table, torch.tensor([0, 0, q_len], dtype=torch.int32).cuda(), kv,
+                  torch.randn(rows + 1, H, D).cuda(), torch.randn(rows + 1, H, D).cuda())
+    assert torch.equal(cache.k, before)  # no token number that is not negative
+
+
 def test_attention_long_offsets(qre):
     """A page beyond 2^31 bytes of the pool: offsets in 64 bits."""
     D, H = 256, 8
