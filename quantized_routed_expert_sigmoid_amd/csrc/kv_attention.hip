@@ -811,7 +811,7 @@ struct Plan {
     size_t o_bytes, total;
 };
 
-constexpr int64_t kTargetUnits = 1024;
+constexpr int64_t kTargetUnits = 512;
 constexpr int kMaxSplit = 256;
 constexpr int64_t kMaxSplitRows = 1 << 22; /* bounds the workspace and the join's grid */
 
@@ -824,7 +824,7 @@ Plan plan_attention(const coli_kv_cache& c, const coli_kv_batch& b, const coli_k
     p.row_tiles = (int)min((rows + p.rows - 1) / p.rows, (int64_t)1 << 20);
     const int64_t units = (int64_t)max(b.n_seq, 1) * p.row_tiles * c.n_heads;
     const int64_t seen = a.window > 0 ? min((int64_t)a.max_kv, (int64_t)a.window + b.max_q) : a.max_kv;
-    const int64_t blocks = (seen + kBlk - 1) / kBlk, target = p.rows == kTileRows ? 512 : kTargetUnits;
+    const int64_t blocks = (seen + kBlk - 1) / kBlk, target = kTargetUnits;
     p.nsplit = (int)max((int64_t)1, min(min((target + units - 1) / units, (blocks + 3) / 4), (int64_t)kMaxSplit));
     if (p.rows == kTileRows && units >= 256)
         p.nsplit = 1;

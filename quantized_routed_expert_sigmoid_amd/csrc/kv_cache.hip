@@ -179,34 +179,51 @@ __global__ __launch_bounds__(kThreads) void kv_append_kernel(coli_kv_cache c, co
     }
 }
 
-/* The rows' values of one block and head; a missing page (null) gives zeros. */
+/* The rows' values of one block and head; a missing page (null) gives zeros.
+ * The page goes through LDS, where the codes of a token's eight dims are picked
+ * up by the lane that writes them: a row is written in whole lines.  Keys lie
+ * there by tokens, values as in the page with the dims four bytes further
+ * apart, so that neighbouring lanes' bytes lie in different banks. */
 template <typename T, int D, bool KEY>
 __device__ __forceinline__ void read_block(const int8_t* page, float scale, int t0, int t1, T* x, int64_t stride)
 {
+    constexpr int KT = D + 16, VC = 36;
+    __shared__ __align__(16) uint8_t codes[KEY ? COLI_KV_BLOCK * KT : 2 * D * VC];
+    __syncthreads(); /* the block before is written */
+    if (page) {
 #pragma unroll
-    for (int n = 0; n < D / 64; ++n) {
-        const int u = threadIdx.x + kThreads * n;
-        const Piece<D, KEY> p(u);
-        const uint4 o = page ? ((const uint4*)page)[u] : make_uint4(0, 0, 0, 0);
-        const uint32_t w[4] = {o.x, o.y, o.z, o.w};
-        float v[16];
-#pragma unroll
-        for (int b = 0; b < 16; ++b)
-            v[b] = (float)(int8_t)(w[b / 4] >> (8 * (b & 3))) * scale;
-        if constexpr (KEY) {
-            if (p.token0 >= t0 && p.token0 < t1)
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    store4(x + p.token0 * stride + p.dim0 + 4 * j,
-                           make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]));
-        } else {
-#pragma unroll
-            for (int b = 0; b < 16; ++b) {
-                const int t = p.token(b);
-                if (t >= t0 && t < t1)
-                    store1(x + t * stride + p.dim0, v[b]);
+        for (int n = 0; n < D / 64; ++n) {
+            const int u = threadIdx.x + kThreads * n;
+            const Piece<D, KEY> p(u);
+            const uint4 o = ((const uint4*)page)[u];
+            if (KEY) {
+                *(uint4*)(codes + p.token0 * KT + p.dim0) = o;
+            } else {
+                uint32_t* w = (uint32_t*)(codes + u / 2 * VC + (u & 1) * 16);
+                w[0] = o.x;
+                w[1] = o.y;
+                w[2] = o.z;
+                w[3] = o.w;
             }
         }
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < (t1 - t0) * (D / 8); i += kThreads) {
+        const int t = t0 + i / (D / 8), c = i % (D / 8) * 8;
+        float v[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            v[j] = (float)(int8_t)(KEY ? codes[t * KT + c + j]
+                                       : codes[(t / 32 * D + c + j) * VC + (t >> 2 & 1) * 16 + t % 32 / 8 * 4 + t % 4]) *
+                   scale;
+        if (!page) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                v[j] = 0.0f;
+        }
+        T* o = x + t * stride + c;
+        store4(o, make_float4(v[0], v[1], v[2], v[3]));
+        store4(o + 4, make_float4(v[4], v[5], v[6], v[7]));
     }
 }
 
