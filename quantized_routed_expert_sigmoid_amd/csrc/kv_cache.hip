@@ -4,8 +4,10 @@
  * A workgroup takes the keys or the values of one (block, head).  Its units are
  * the 16-byte pieces in which the codes lie in the page: for keys 16 dims of
  * one token, for values 16 tokens of one dim (value_byte); neighbouring lanes
- * have neighbouring pieces, so a page is read and written in whole lines, and
- * packed rows in runs of 32 bytes or more.
+ * have neighbouring pieces, so a page is read and written in whole lines.  Rows
+ * are read and written by eight dims of a token, whole lines too; LDS lies
+ * between the two orders (read-back 17.5 -> 8.8 us, 8 k tokens of 8 heads of 128
+ * dims as bf16, against single values written where their piece has them).
  *
  * Append: a = the new values' largest magnitude, s' = max(s, a / 127); held
  * codes become rnd(c s / s') where the scale grew, new ones rnd(v / s').  The
@@ -40,31 +42,6 @@ struct Piece {
     __device__ __forceinline__ int token(int b) const { return KEY ? token0 : token0 + b / 4 * 8 + b % 4; }
 };
 
-/* The sixteen values of a piece from the packed rows; x is the row that token 0
- * of the block has or would have, only tokens t0 .. t1 - 1 have rows.  Loads are
- * unconditional, from the nearest row: one under a branch would be waited for
- * by itself. */
-template <typename T, int D, bool KEY>
-__device__ __forceinline__ void load_piece(const T* x, int64_t stride, const Piece<D, KEY>& p, int t0, int t1,
-                                           float (&v)[16])
-{
-    if constexpr (KEY) {
-        const T* r = x + min(max(p.token0, t0), t1 - 1) * stride + p.dim0;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const float4 e = load4(r + 4 * j);
-            v[4 * j] = e.x;
-            v[4 * j + 1] = e.y;
-            v[4 * j + 2] = e.z;
-            v[4 * j + 3] = e.w;
-        }
-    } else {
-#pragma unroll
-        for (int b = 0; b < 16; ++b)
-            v[b] = to_f32(x[min(max(p.token(b), t0), t1 - 1) * stride + p.dim0]);
-    }
-}
-
 /* The code of v as q8_code gives it, plus 128. */
 __device__ __forceinline__ float code_up(float v, float inv)
 {
@@ -73,82 +50,119 @@ __device__ __forceinline__ float code_up(float v, float inv)
     return __builtin_amdgcn_fmed3f(e, -127.0f, 127.0f) + 128.0f;
 }
 
-/* Sixteen codes, each converted into its byte. */
-__device__ __forceinline__ uint4 encode16(const float (&v)[16], float inv)
+/* Four codes, each converted into its byte. */
+__device__ __forceinline__ uint32_t encode4(const float* v, float inv)
 {
-    uint32_t w[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        uint32_t u = 0;
-        u = __builtin_amdgcn_cvt_pk_u8_f32(code_up(v[4 * j], inv), 0, u);
-        u = __builtin_amdgcn_cvt_pk_u8_f32(code_up(v[4 * j + 1], inv), 1, u);
-        u = __builtin_amdgcn_cvt_pk_u8_f32(code_up(v[4 * j + 2], inv), 2, u);
-        u = __builtin_amdgcn_cvt_pk_u8_f32(code_up(v[4 * j + 3], inv), 3, u);
-        w[j] = u ^ 0x80808080u;
-    }
-    return make_uint4(w[0], w[1], w[2], w[3]);
+    uint32_t u = 0;
+    u = __builtin_amdgcn_cvt_pk_u8_f32(code_up(v[0], inv), 0, u);
+    u = __builtin_amdgcn_cvt_pk_u8_f32(code_up(v[1], inv), 1, u);
+    u = __builtin_amdgcn_cvt_pk_u8_f32(code_up(v[2], inv), 2, u);
+    u = __builtin_amdgcn_cvt_pk_u8_f32(code_up(v[3], inv), 3, u);
+    return u ^ 0x80808080u;
 }
 
+/* Values' codes in LDS: the dims of a page four bytes further apart, so that
+ * the bytes of neighbouring dims lie in different banks. */
+constexpr int kDimBytes = 36;
+
+__device__ __forceinline__ int value_at(int t, int c, int D)
+{
+    return (t / 32 * D + c) * kDimBytes + (t >> 2 & 1) * 16 + t % 32 / 8 * 4 + t % 4;
+}
+
+/* x is the row that token 0 of the block has or would have; only tokens t0 ..
+ * t1 - 1 have rows.  A thread takes eight dims of a token at a time (loads are
+ * unconditional, from the nearest row: one under a branch would be waited for by
+ * itself); the codes go through LDS to the threads that own their pieces. */
 template <typename T, int D, bool KEY>
 __device__ void append_block(const T* x, int64_t stride, int t0, int t1, int8_t* page, float* scale)
 {
-    constexpr int N = D / 64; /* pieces of a thread: 4 D in a block */
+    constexpr int N = D / 32, KT = D + 16; /* groups of eight values of a thread; bytes of a key row in LDS */
     __shared__ float part[kThreads / kWave];
-    float v[N][16], a = 0.0f;
+    __shared__ __align__(16) uint8_t codes[KEY ? COLI_KV_BLOCK * KT : 2 * D * kDimBytes];
+    float v[N][8], a = 0.0f;
 #pragma unroll
     for (int n = 0; n < N; ++n) {
-        load_piece<T, D, KEY>(x, stride, Piece<D, KEY>(threadIdx.x + kThreads * n), t0, t1, v[n]);
+        const int i = threadIdx.x + kThreads * n, t = min(max(i / (D / 8), t0), t1 - 1), c = i % (D / 8) * 8;
+        const float4 lo = load4(x + t * stride + c), hi = load4(x + t * stride + c + 4);
+        v[n][0] = lo.x;
+        v[n][1] = lo.y;
+        v[n][2] = lo.z;
+        v[n][3] = lo.w;
+        v[n][4] = hi.x;
+        v[n][5] = hi.y;
+        v[n][6] = hi.z;
+        v[n][7] = hi.w;
 #pragma unroll
-        for (int b = 0; b < 16; ++b)
-            a = fmaxf(a, fabsf(v[n][b])); /* rows outside are copies of ones inside */
+        for (int j = 0; j < 8; ++j)
+            a = fmaxf(a, fabsf(v[n][j]));
     }
     const float old = t0 > 0 ? *scale : 0.0f;
     for (int m = 32; m >= 1; m >>= 1)
         a = fmaxf(a, shfl_xor(a, m));
     if ((threadIdx.x & 63) == 0)
         part[threadIdx.x >> 6] = a;
-    __syncthreads();
+    __syncthreads(); /* and the block before has left `codes` */
     a = fmaxf(fmaxf(part[0], part[1]), fmaxf(part[2], part[3]));
     const float now = fmaxf(old, a / 127.0f);
     const float inv = now == 0.0f ? 0.0f : 1.0f / now, f = old * inv;
     const bool grew = t0 > 0 && now != old;
 #pragma unroll
     for (int n = 0; n < N; ++n) {
+        const int i = threadIdx.x + kThreads * n, t = i / (D / 8), c = i % (D / 8) * 8;
+        if (t < t0 || t >= t1)
+            continue;
+        const uint32_t w[2] = {encode4(v[n], inv), encode4(v[n] + 4, inv)};
+        if (KEY) {
+            *(uint2*)(codes + t * KT + c) = make_uint2(w[0], w[1]);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                codes[value_at(t, c + j, D)] = (uint8_t)(w[j / 4] >> (8 * (j & 3)));
+        }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int n = 0; n < D / 64; ++n) {
         const int u = threadIdx.x + kThreads * n;
         const Piece<D, KEY> p(u);
-        const int first = p.token(0), last = p.token(15);
-        const bool whole = first >= t0 && last < t1; /* all new */
-        bool any = whole;
-        if (!KEY) {
+        bool any = false, whole = true, held = false;
 #pragma unroll
-            for (int b = 0; b < 16; b += 4)
-                any |= p.token(b) < t1 && p.token(b) + 3 >= t0;
+        for (int b = 0; b < (KEY ? 1 : 16); ++b) {
+            const int t = p.token(b);
+            const bool fresh = t >= t0 && t < t1;
+            any |= fresh;
+            whole &= fresh;
+            held |= t < t0;
         }
-        if (!any && !(grew && first < t0))
+        if (!any && !(grew && held))
             continue;
+        uint32_t w[4];
+        const uint32_t* from = (const uint32_t*)(KEY ? codes + p.token0 * KT + p.dim0
+                                                     : codes + u / 2 * kDimBytes + (u & 1) * 16);
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            w[j] = from[j];
         uint4* at = (uint4*)page + u;
-        if (whole) {
-            *at = encode16(v[n], inv);
-            continue;
-        }
-        /* some held, or behind the last token: these keep their bytes */
-        const uint4 o = *at;
-        uint32_t w[4] = {o.x, o.y, o.z, o.w};
+        if (!whole) {
+            /* some held, or behind the last token: these keep their bytes */
+            const uint4 o = *at;
+            const uint32_t was[4] = {o.x, o.y, o.z, o.w};
 #pragma unroll
-        for (int b = 0; b < 16; ++b) {
-            const int t = p.token(b), sh = 8 * (b & 3);
-            int32_t c = (int8_t)(w[b / 4] >> sh);
-            if (t >= t0 && t < t1)
-                c = q8_code(v[n][b], inv);
-            else if (t < t0 && grew)
-                c = q8_code((float)c, f);
-            w[b / 4] = (w[b / 4] & ~(0xFFu << sh)) | ((uint32_t)(c & 0xFF) << sh);
+            for (int b = 0; b < 16; ++b) {
+                const int t = p.token(b), sh = 8 * (b & 3);
+                if (t >= t0 && t < t1)
+                    continue;
+                int32_t c = (int8_t)(was[b / 4] >> sh);
+                if (t < t0 && grew)
+                    c = q8_code((float)c, f);
+                w[b / 4] = (w[b / 4] & ~(0xFFu << sh)) | ((uint32_t)(c & 0xFF) << sh);
+            }
         }
         *at = make_uint4(w[0], w[1], w[2], w[3]);
     }
-    __syncthreads(); /* every wave has the old scale, and has left `part` */
     if (threadIdx.x == 0)
-        *scale = now;
+        *scale = now; /* every wave has read the old one */
 }
 
 template <typename T, int D>
@@ -181,14 +195,12 @@ __global__ __launch_bounds__(kThreads) void kv_append_kernel(coli_kv_cache c, co
 
 /* The rows' values of one block and head; a missing page (null) gives zeros.
  * The page goes through LDS, where the codes of a token's eight dims are picked
- * up by the lane that writes them: a row is written in whole lines.  Keys lie
- * there by tokens, values as in the page with the dims four bytes further
- * apart, so that neighbouring lanes' bytes lie in different banks. */
+ * up by the lane that writes them: a row is written in whole lines. */
 template <typename T, int D, bool KEY>
 __device__ __forceinline__ void read_block(const int8_t* page, float scale, int t0, int t1, T* x, int64_t stride)
 {
-    constexpr int KT = D + 16, VC = 36;
-    __shared__ __align__(16) uint8_t codes[KEY ? COLI_KV_BLOCK * KT : 2 * D * VC];
+    constexpr int KT = D + 16;
+    __shared__ __align__(16) uint8_t codes[KEY ? COLI_KV_BLOCK * KT : 2 * D * kDimBytes];
     __syncthreads(); /* the block before is written */
     if (page) {
 #pragma unroll
@@ -199,7 +211,7 @@ __device__ __forceinline__ void read_block(const int8_t* page, float scale, int 
             if (KEY) {
                 *(uint4*)(codes + p.token0 * KT + p.dim0) = o;
             } else {
-                uint32_t* w = (uint32_t*)(codes + u / 2 * VC + (u & 1) * 16);
+                uint32_t* w = (uint32_t*)(codes + u / 2 * kDimBytes + (u & 1) * 16);
                 w[0] = o.x;
                 w[1] = o.y;
                 w[2] = o.z;
@@ -213,9 +225,7 @@ __device__ __forceinline__ void read_block(const int8_t* page, float scale, int 
         float v[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j)
-            v[j] = (float)(int8_t)(KEY ? codes[t * KT + c + j]
-                                       : codes[(t / 32 * D + c + j) * VC + (t >> 2 & 1) * 16 + t % 32 / 8 * 4 + t % 4]) *
-                   scale;
+            v[j] = (float)(int8_t)codes[KEY ? t * KT + c + j : value_at(t, c + j, D)] * scale;
         if (!page) {
 #pragma unroll
             for (int j = 0; j < 8; ++j)
