@@ -1,4 +1,4 @@
-"""Python binding of the operators around the layer (include/colibri.h): the
+"""Python binding of the operators around the layer (include/colibri_block.h): the
 residual addition with root-mean-square norm and Q8_0, the quantised matrix
 product with its epilogue, and attention over a paged int8 cache.
 
@@ -239,7 +239,7 @@ def kv_page_shape(n_pages: int, n_heads: int, head_dim: int) -> Tuple[int, int, 
 class KVCache:
     """A paged int8 cache of keys and values: k, v int8 [n_pages][n_heads][64 * head_dim]
     (the codes of one block of 64 tokens and head in the order given in
-    include/colibri.h), k_scale, v_scale fp32 [n_pages][n_heads]."""
+    include/colibri_block.h), k_scale, v_scale fp32 [n_pages][n_heads]."""
 
     def __init__(self, k: torch.Tensor, v: torch.Tensor, k_scale: torch.Tensor, v_scale: torch.Tensor,
                  head_dim: int):

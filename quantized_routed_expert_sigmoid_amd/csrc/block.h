@@ -8,7 +8,7 @@
 #ifndef COLI_BLOCK_H
 #define COLI_BLOCK_H
 
-#include "../../include/colibri.h"
+#include "../../include/colibri_block.h"
 
 #include <hip/hip_runtime.h>
 #include <stddef.h>

@@ -1,6 +1,6 @@
 /*
  * block_api.hip -- the C ABI of the operators around the layer (declared in
- * include/colibri.h): argument validation on the host, then one launcher.
+ * include/colibri_block.h): argument validation on the host, then one launcher.
  * Nothing here synchronises or allocates.
  */
 #include "block.h"

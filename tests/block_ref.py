@@ -1,6 +1,6 @@
 """Plain 64-bit forms of the operators around the layer, for their tests, and
 the bounds that the tests hold the kernels to.  Written from the definitions
-in include/colibri.h; CPU tensors in, CPU float64 tensors out."""
+in include/colibri_block.h; CPU tensors in, CPU float64 tensors out."""
 
 import math
 

@@ -170,3 +170,15 @@ def test_binding_refuses():
         qre.KVCache.empty(2, 1, 64, device="cpu")
     with pytest.raises(TypeError):
         block._type(torch.float16)
+
+
+def test_library_exports_every_declared_symbol(L):
+    import os
+    import re
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    with open(os.path.join(root, "include", "colibri_block.h")) as f:
+        text = re.sub(r"/\*.*?\*/", "", f.read(), flags=re.S)
+    names = set(re.findall(r"\b(colibri_\w+)\s*\(", text))
+    assert len(names) == 7
+    for name in names:
+        assert hasattr(L, name), name
