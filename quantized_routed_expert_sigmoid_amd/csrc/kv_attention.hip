@@ -38,6 +38,7 @@ typedef __bf16 v8b __attribute__((ext_vector_type(8)));
 constexpr int kBlk = COLI_KV_BLOCK;
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kLn2 = 0.69314718055994530942f;
+constexpr float kSlack = 8.0f;
 
 struct AttnArgs {
     coli_kv_cache c;
@@ -331,7 +332,7 @@ __device__ __forceinline__ void mask_tile(float* t, int base, int end, int begin
 }
 
 /* Scores t in units of c (c >= 0, one per row) become w 2^(t c - m), w being the
- * block's value scale, with m raised to the largest; l, the lane's sum, takes
+ * block's value scale, with m raised towards the largest; l, the lane's sum, takes
  * them up without w; returns the factor of what was summed before.  Both scales
  * go into the exponent's fma: the largest of t is the largest of t c, and w is
  * 2^log2(w), whose rounding (2^-21) weighs a block's sums and its share of l
@@ -344,8 +345,10 @@ __device__ __forceinline__ float softmax_tile(float* t, float c, float w, float&
     for (int i = 1; i < N; ++i)
         mx = fmaxf(mx, t[i]);
     mx = row_max<R>(mx);
-    /* a row that has seen nothing keeps -inf (0 * -inf is no number) */
-    const float mn = mx == -__builtin_inff() ? m : fmaxf(m, mx * c);
+    /* m follows the largest only when that is 2^kSlack above it: until then the
+     * powers stay below 2^kSlack and the sums need no factor.  A row that has
+     * seen nothing keeps -inf (0 * -inf is no number). */
+    const float mn = mx != -__builtin_inff() && mx * c > m + kSlack ? mx * c : m;
     const float mb = mn == -__builtin_inff() ? 0.0f : mn;
     const float cc = c == 0.0f ? 0x1p-126f : c; /* hidden tokens stay at -inf, the others at 0 */
     const float f = __builtin_amdgcn_exp2f(m - mb);
