@@ -67,7 +67,9 @@ constexpr int kMaxRowsWg = 256; /* weight rows of a workgroup, most */
  * row; unit 64 j + lane), and streams its rows past them, one row's loads
  * ahead of the products.  A unit lies inside one 32-element block, so its
  * exact integer dot product takes one pair of scales.  Rows longer than 64 NU
- * units go in several rounds, their sums kept in LDS.
+ * units go in several rounds, their sums kept in LDS.  Bound by the weights'
+ * bytes: 1 x 10240 x 6144 int4 6.7 us (4.7 TB/s), 4 x 6144 x 8192 int8 with groups of
+ * 128 11.5 us (4.4 TB/s).
  */
 template <int BITS, int T, int NU, bool GROUPED, typename TO>
 __global__ __launch_bounds__(256) void linear_rows_kernel(LinearArgs a, int rows_wg)
@@ -419,6 +421,9 @@ struct TileArgs {
  * products, 36 KB of an int4 step, so that two workgroups share a CU.  Weights
  * stay packed in LDS and are unpacked by the waves that multiply them.  Lane
  * (l % 32, h = l / 32) of instruction i of a step takes k = 16 i + 8 h .. + 7.
+ * Measured: 4096 x 10240 x 6144 int4 488 us and 24 us of linear_expand, 1.0 PFLOP/s
+ * (a bf16 library product of that size: 1.45); without the unpacking 65 us less,
+ * without the loads 100 us less, the matrix cores busy half of the time.
  */
 constexpr int kTileTT = 4;
 
@@ -576,7 +581,9 @@ __global__ __launch_bounds__(256, 2) void linear_tiles(LinearArgs a, TileArgs ta
  * waves WN x 4 / WN of these, in stages of four blocks; weights and codes
  * travel packed from memory to LDS one stage ahead.  Codes of fewer bits are
  * unpacked to the top of their bytes, 2^(8 - bits) times their value, which
- * the row's scale takes out again.
+ * the row's scale takes out again.  Measured: 2048 x 4096 x 4096 int4, fp32 out,
+ * 89 us (771 TFLOP/s; the VALU's limit is 1.26 P), with groups of 128 143 us; 16 x
+ * 10240 x 6144 int4 16 us, bound by the latency of its stages.
  */
 constexpr int kStageK = 128;
 
