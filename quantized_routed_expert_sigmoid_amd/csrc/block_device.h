@@ -97,28 +97,34 @@ __device__ __forceinline__ void store4_any(bf16* p, float4 v)
     __builtin_memcpy(p, &u, 8);
 }
 
-/* Sixteen bytes per lane from memory into LDS at dst + 16 lane (dst uniform).
- * Written out because the compiler, which cannot tell the buffers apart, would
- * wait for every such load before the next LDS read; whoever uses it waits
- * himself (arrive_all).  M0 holds the LDS address; no other instruction of
- * these kernels takes M0. */
-__device__ __forceinline__ void to_lds(const void* src, void* dst)
+/* LDS address of a byte of shared memory. */
+__device__ __forceinline__ uint32_t lds_address(const void* p)
 {
-    const uint32_t at = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) void*)dst;
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(
-                     __builtin_amdgcn_readfirstlane(at)),
-                 "v"(src)
+    return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const void*)p;
+}
+
+/* Sixteen (four) bytes per lane from base + off into LDS at `to` + 16 (4) lane;
+ * base and `to` are uniform, so a loop that moves only these spends no vector
+ * instructions on addresses.  Written out because the compiler, which cannot
+ * tell the buffers apart, would wait for every such load before the next LDS
+ * read; whoever uses it waits himself (arrive_all).  M0 holds the LDS address;
+ * no other instruction of these kernels takes M0. */
+__device__ __forceinline__ void to_lds(const void* base, uint32_t off, uint32_t to)
+{
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(to), "v"(off), "s"(base)
                  : "memory");
 }
 
-/* Four bytes per lane, at dst + 4 lane. */
-__device__ __forceinline__ void word_to_lds(const void* src, void* dst)
+__device__ __forceinline__ void word_to_lds(const void* base, uint32_t off, uint32_t to)
 {
-    const uint32_t at = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) void*)dst;
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off" ::"s"(
-                     __builtin_amdgcn_readfirstlane(at)),
-                 "v"(src)
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, %2" ::"s"(to), "v"(off), "s"(base)
                  : "memory");
+}
+
+/* The wave of the workgroup, as a uniform value. */
+__device__ __forceinline__ int wave_of()
+{
+    return __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
 }
 
 /* Waits until at most LEFT of this wave's loads are outstanding and its LDS

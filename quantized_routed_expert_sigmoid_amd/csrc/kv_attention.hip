@@ -589,7 +589,8 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void kv_attention_tile(AttnA
     constexpr int ND = sizeof(T) == 4 ? 3 : 2, NP = sizeof(T) == 4 ? 3 : 1;
     constexpr int KS = D / 32, DT = D / 32, PB = kBlk * D; /* bytes of a block's keys, or values */
     extern __shared__ __align__(1024) uint8_t lds[];       /* of two blocks each: keys, values, values in bf16 */
-    const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6, lg = lane >> 5, col = lane & 31;
+    const int lane = threadIdx.x & 63, wv = wave_of(), lg = lane >> 5, col = lane & 31;
+    const uint32_t lds0 = lds_address(lds);
     const int H = g.c.n_heads, G = g.group;
     for (int64_t unit = xcd_unit(); unit < g.units; unit += gridDim.x) {
         /* heads outermost (an XCD's share has every sequence), then sequences, the
@@ -633,15 +634,15 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void kv_attention_tile(AttnA
                 return __builtin_amdgcn_readfirstlane(page_of(g.b, g.c.n_pages, s, min(p, p1 - 1)));
             };
             auto at = [&](int page) { return (int64_t)max(page, 0) * H + hk; };
-            auto fetch = [&](const int8_t* from, uint8_t* to) {
+            auto fetch = [&](const int8_t* from, uint32_t to) {
 #pragma unroll
                 for (int i = 0; i < PB / 4096; ++i) {
                     const int o = (i * 4 + wv) * 1024;
-                    to_lds(from + o + lane * 16, to + o);
+                    to_lds(from + o, lane * 16, lds0 + to + o);
                 }
             };
-            auto fetch_k = [&](int page, int p) { fetch(g.c.k + at(page) * PB, lds + (p & 1) * PB); };
-            auto fetch_v = [&](int page, int p) { fetch(g.c.v + at(page) * PB, lds + (2 + (p & 1)) * PB); };
+            auto fetch_k = [&](int page, int p) { fetch(g.c.k + at(page) * PB, (p & 1) * PB); };
+            auto fetch_v = [&](int page, int p) { fetch(g.c.v + at(page) * PB, (2 + (p & 1)) * PB); };
             /* values to bf16: sixteen tokens of a dim are two operands of it */
             auto convert = [&](int p) {
                 const uint8_t* raw = lds + (2 + (p & 1)) * PB;

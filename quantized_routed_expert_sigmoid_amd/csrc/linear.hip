@@ -440,7 +440,7 @@ __global__ __launch_bounds__(256, 2) void linear_tiles(LinearArgs a, TileArgs ta
     constexpr int TT = kTileTT, XB = L::kX, LPR = BITS / 2; /* 16-byte chunks of a row's step */
     constexpr int kWRuns = L::kW / 1024;
     extern __shared__ __align__(1024) uint8_t lds[];
-    const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6, h = lane >> 5, col = lane & 31;
+    const int lane = threadIdx.x & 63, wv = wave_of(), h = lane >> 5, col = lane & 31;
     const int wn = wv & 1, wt = wv >> 1;
     const int unit = (int)xcd_unit();
     if (unit >= ta.n_tiles * ta.t_tiles)
@@ -454,23 +454,29 @@ __global__ __launch_bounds__(256, 2) void linear_tiles(LinearArgs a, TileArgs ta
     constexpr int RPB = LPR >= 16 ? 1 : 16 / LPR;
     auto swz = [](int n) { return n / RPB % LPR; };
 
+    /* where the weights are fewer runs than waves, waves load the same one */
+    constexpr int kWMine = (kWRuns + 3) / 4;
+    const uint32_t lds0 = lds_address(lds);
+    const uint8_t* w0 = w + wg.n0 * row_bytes;
+    uint32_t woff[kWMine];
+#pragma unroll
+    for (int i = 0; i < kWMine; ++i) {
+        const int slot = (i * 4 + wv) % kWRuns * 64 + lane, n = slot / LPR, c = slot % LPR ^ swz(n);
+        woff[i] = (uint32_t)(min(n, a.N - 1 - wg.n0) * (int)row_bytes + c * kChunk);
+    }
     auto fetch = [&](int step) {
-        uint8_t* buf = lds + (step & 1) * L::kStage;
+        const uint32_t buf = lds0 + (step & 1) * L::kStage;
         step = min(step, ta.stages - 1); /* past the end: loaded and not used */
         const uint8_t* x = ta.xh + ((int64_t)step * ta.tiles + wg.tok0 / kTileTok) * (8 * kTileTok * kChunk);
 #pragma unroll
         for (int i = 0; i < XB / 4096; ++i) {
             const int o = (i * 4 + wv) * 1024;
-            to_lds(x + o + lane * 16, buf + o);
+            to_lds(x + o, lane * 16, buf + o);
         }
         const int64_t kb = (int64_t)min(step * kKB, a.K - kKB) * BITS / 8;
-        /* where the weights are fewer runs than waves, waves load the same one */
 #pragma unroll
-        for (int i = 0; i < (kWRuns + 3) / 4; ++i) {
-            const int run = (i * 4 + wv) % kWRuns;
-            const int slot = run * 64 + lane, n = slot / LPR, c = slot % LPR ^ swz(n);
-            to_lds(w + min(wg.n0 + n, a.N - 1) * row_bytes + kb + c * kChunk, buf + XB + run * 1024);
-        }
+        for (int i = 0; i < kWMine; ++i)
+            to_lds(w0 + kb, woff[i], buf + XB + (i * 4 + wv) % kWRuns * 1024);
     };
 
     v16f acc[2][TT];
@@ -666,7 +672,7 @@ __global__ __launch_bounds__(256, 2) void linear_fold(LinearArgs a, TileArgs ta)
     using L = FoldLds<BITS, RR, TT, WN, GROUPED>;
     constexpr int XB = L::kX, WB = L::kW, SB = L::kStage - L::kS, STAGES = L::kStages;
     extern __shared__ __align__(1024) uint8_t lds[];
-    const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6, h = lane >> 5, col = lane & 31;
+    const int lane = threadIdx.x & 63, wv = wave_of(), h = lane >> 5, col = lane & 31;
 
     const int unit = (int)xcd_unit(), total = ta.n_tiles * ta.t_tiles;
     if (unit >= total * ta.splits)
@@ -684,32 +690,46 @@ __global__ __launch_bounds__(256, 2) void linear_fold(LinearArgs a, TileArgs ta)
      * are its last one: their blocks' scales are taken as 0. */
     auto xswz = [](int t) { return t / 2 % 8; };
     auto wswz = [](int n) { return n / (16 / WC) % WC; };
+    constexpr int kXMine = XB / 4096, kWMine = (WB + 4095) / 4096;
+    const uint32_t lds0 = lds_address(lds);
+    const uint8_t* w0 = (const uint8_t*)a.w + wg.n0 * row_bytes;
+    const int8_t* x0 = a.xq + (int64_t)wg.tok0 * a.K;
+    const float* d0 = a.xd + (int64_t)wg.tok0 * nb;
+    const float* s_0 = a.w_scale + (int64_t)wg.n0 * gpr;
+    /* this lane's row and chunk of each of its runs */
+    int xrow[kXMine], xchunk[kXMine], wrow[kWMine], wchunk[kWMine];
+#pragma unroll
+    for (int i = 0; i < kXMine; ++i) {
+        const int slot = (i * 4 + wv) * 64 + lane, t = slot / XC;
+        xrow[i] = min(t, a.S - 1 - wg.tok0) * a.K;
+        xchunk[i] = (slot % XC ^ xswz(t)) * kChunk;
+    }
+#pragma unroll
+    for (int i = 0; i < kWMine; ++i) {
+        const int slot = (i * 4 + wv) % (WB / 1024) * 64 + lane, n = slot / WC;
+        wrow[i] = min(n, a.N - 1 - wg.n0) * (int)row_bytes;
+        wchunk[i] = (slot % WC ^ wswz(n)) * kChunk;
+    }
+    const int drun = wv % L::kRunsD;
+    const uint32_t doff = (uint32_t)min(drun * 64 + lane, a.S - 1 - wg.tok0) * nb * 4;
+    const uint32_t soff = (uint32_t)(min(at.n0 + lane % (32 * RR), a.N - 1) - wg.n0) * gpr * 4;
     auto fetch = [&](int stage) {
-        uint8_t* buf = lds + (stage - s0) % STAGES * L::kStage;
+        const uint32_t buf = lds0 + (stage - s0) % STAGES * L::kStage;
         stage = min(stage, ta.stages - 1); /* past the end: loaded and not used */
+        const int xk = stage * kStageK, xb = min(xk, a.K - kChunk);
 #pragma unroll
-        for (int i = 0; i < XB / 4096; ++i) {
-            const int slot = (i * 4 + wv) * 64 + lane, t = slot / XC, c = slot % XC ^ xswz(t);
-            const int k = min(stage * kStageK + c * kChunk, a.K - kChunk);
-            to_lds(a.xq + (int64_t)min(wg.tok0 + t, a.S - 1) * a.K + k, buf + (i * 4 + wv) * 1024);
-        }
+        for (int i = 0; i < kXMine; ++i)
+            to_lds(x0 + xb, xrow[i] + min(xk + xchunk[i], a.K - kChunk) - xb, buf + (i * 4 + wv) * 1024);
+        const int wk = stage * WC * kChunk, wlast = (int)row_bytes - kChunk, wb = min(wk, wlast);
 #pragma unroll
-        for (int i = 0; i < (WB + 4095) / 4096; ++i) {
-            const int run = (i * 4 + wv) % (WB / 1024);
-            const int slot = run * 64 + lane, n = slot / WC, c = slot % WC ^ wswz(n);
-            const int64_t o = min((int64_t)(stage * WC + c) * kChunk, row_bytes - kChunk);
-            to_lds((const uint8_t*)a.w + min(wg.n0 + n, a.N - 1) * row_bytes + o, buf + XB + run * 1024);
-        }
+        for (int i = 0; i < kWMine; ++i)
+            to_lds(w0 + wb, wrow[i] + min(wk + wchunk[i], wlast) - wb, buf + XB + (i * 4 + wv) % (WB / 1024) * 1024);
         /* the four scales of each token's stage, at a row's end its last four */
-        const int run = wv % L::kRunsD;
-        to_lds(a.xd + (int64_t)min(wg.tok0 + run * 64 + lane, a.S - 1) * nb + min(stage * 4, nb - 4),
-               buf + XB + WB + run * 1024);
+        to_lds(d0 + min(stage * 4, nb - 4), doff, buf + XB + WB + drun * 1024);
         if constexpr (GROUPED) {
 #pragma unroll
             for (int b = 0; b < L::kScales; ++b)
-                word_to_lds(a.w_scale + (int64_t)min(at.n0 + lane % (32 * RR), a.N - 1) * gpr +
-                                min(stage * 4 + b, nb - 1) / gb,
-                            buf + SB + (b * WN + wv % WN) * 256);
+                word_to_lds(s_0 + min(stage * 4 + b, nb - 1) / gb, soff, buf + SB + (b * WN + wv % WN) * 256);
         }
     };
 
