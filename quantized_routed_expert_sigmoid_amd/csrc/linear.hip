@@ -657,7 +657,7 @@ struct FoldLds {
     static constexpr int kScales = GROUPED == 0 ? 0 : GROUPED == 1 ? 4 : 1, kS = kScales * WN * 256;
     static constexpr int kStage = kX + kW + kRunsD * 1024 + kS;
     static constexpr int kFit = 79 * 1024 / kStage;
-    static constexpr int kStages = kFit < 2 ? 2 : kFit > 4 ? 4 : kFit;
+    static constexpr int kStages = kFit < 2 ? 2 : kFit > 3 ? 3 : kFit;
     /* loads of a wave and stage; where there are fewer runs than waves, waves
      * load the same one, so that every wave counts alike */
     static constexpr int kLoads = kX / 4096 + (kW + 4095) / 4096 + 1 + kScales;
