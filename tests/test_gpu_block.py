@@ -584,6 +584,49 @@ def test_block_captured_and_replayed(qre):
         assert torch.equal(out[0], eager[i][0]) and torch.equal(out[1], eager[i][1]), f"replay {i}"
 
 
+def test_prompt_kernels_captured_and_replayed(qre):
+    """The forms for many tokens (LDS of more than 64 KB among them) inside one graph, replayed with other inputs."""
+    D, H, Hq = 128, 2, 8
+    g, codes, scales, seqs, cache = make_cache(qre, [(90, 300), (40, 700)], H, D, "graph")
+    args = dev(seqs)
+    w, sc, xq, xd, bank, _ = make_linear(qre, 130, 2100, 384, 4, 128, "graph")
+    _, _, xq2, xd2, bank2, _ = make_linear(qre, 7700, 2100, 128, 2, 0, "graph")
+    ins = [(torch.randn(130, Hq, D, generator=g).to(BF16).cuda(), torch.randn(130, H, D, generator=g).to(BF16).cuda(),
+            torch.roll(xq.cuda(), i, 0), torch.roll(xd.cuda(), i, 0), torch.roll(xq2.cuda(), i, 0),
+            torch.roll(xd2.cuda(), i, 0)) for i in range(4)]
+    start = [t.clone() for t in (cache.k, cache.v, cache.k_scale, cache.v_scale)]
+
+    def step(q, k, a, b, c, d):
+        qre.kv_append(cache, *args, k, k, max_q=90)
+        return (qre.kv_attention(cache, *args, q), qre.linear_q(bank, a, b, dtype=F32),
+                qre.linear_q(bank2, c, d, dtype=BF16, activation="gelu"), *qre.kv_read(cache, *args, 130))
+
+    def reset():
+        for t, c in zip((cache.k, cache.v, cache.k_scale, cache.v_scale), start):
+            t.copy_(c)
+    eager = []
+    for x in ins:
+        reset()
+        eager.append([t.clone() for t in step(*x)])
+    buf = [t.clone() for t in ins[0]]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step(*buf)
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = step(*buf)
+    for i in (1, 3, 0, 2, 1):
+        reset()
+        for b, x in zip(buf, ins[i]):
+            b.copy_(x)
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(out, eager[i]):
+            assert torch.equal(a, b), f"inputs {i}"
+
+
 def test_two_streams_at_once(qre):
     """Calls that overlap on two streams, each with its own workspace and outputs."""
     g, codes, scales, seqs, cache = make_cache(qre, [(1, 2000), (1, 900)], 2, 128, "streams")
@@ -592,11 +635,19 @@ def test_two_streams_at_once(qre):
     xq, xd, args = xq.cuda(), xd.cuda(), dev(seqs)
     want, lin = qre.kv_attention(cache, *args, q), qre.linear_q(bank, xq, xd)
     torch.cuda.synchronize()
+    _, _, _, long_seqs, long_cache = make_cache(qre, [(60, 500), (200, 900)], 2, 128, "streams")
+    long_q, long_args = torch.randn(260, 8, 128, generator=g).cuda(), dev(long_seqs)
+    _, _, xq2, xd2, bank2, _ = make_linear(qre, 300, 500, 1024, 8, 0)
+    xq2, xd2 = xq2.cuda(), xd2.cuda()
+    want2, lin2 = qre.kv_attention(long_cache, *long_args, long_q), qre.linear_q(bank2, xq2, xd2)
+    torch.cuda.synchronize()
     streams = [torch.cuda.Stream() for _ in range(2)]
     outs = []
     for i in range(6):
         with torch.cuda.stream(streams[i % 2]):
-            outs.append((qre.kv_attention(cache, *args, q), qre.linear_q(bank, xq, xd)))
+            outs.append((qre.kv_attention(cache, *args, q), qre.linear_q(bank, xq, xd),
+                         qre.kv_attention(long_cache, *long_args, long_q), qre.linear_q(bank2, xq2, xd2)))
     torch.cuda.synchronize()
-    for a, b in outs:
-        assert torch.equal(a, want) and torch.equal(b, lin)
+    for got in outs:
+        for a, b in zip(got, (want, lin, want2, lin2)):
+            assert torch.equal(a, b)
