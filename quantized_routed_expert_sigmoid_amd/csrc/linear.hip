@@ -421,9 +421,9 @@ struct TileArgs {
  * products, 36 KB of an int4 step, so that two workgroups share a CU.  Weights
  * stay packed in LDS and are unpacked by the waves that multiply them.  Lane
  * (l % 32, h = l / 32) of instruction i of a step takes k = 16 i + 8 h .. + 7.
- * Measured: 4096 x 10240 x 6144 int4 488 us and 24 us of linear_expand, 1.0 PFLOP/s
- * (a bf16 library product of that size: 1.45); without the unpacking 65 us less,
- * without the loads 100 us less, the matrix cores busy half of the time.
+ * Measured: 4096 x 10240 x 6144 int4 466 us and 24 us of linear_expand, 1.05
+ * PFLOP/s (a bf16 library product of 8192^3: 1.45); without the unpacking 65 us
+ * less; the matrix cores are busy half of the time, at 1.9 GHz.
  */
 constexpr int kTileTT = 4;
 
@@ -588,7 +588,7 @@ __global__ __launch_bounds__(256, 2) void linear_tiles(LinearArgs a, TileArgs ta
  * travel packed from memory to LDS one stage ahead.  Codes of fewer bits are
  * unpacked to the top of their bytes, 2^(8 - bits) times their value, which
  * the row's scale takes out again.  Measured: 2048 x 4096 x 4096 int4, fp32 out,
- * 89 us (771 TFLOP/s; the VALU's limit is 1.26 P), with groups of 128 143 us; 16 x
+ * 88 us (780 TFLOP/s; the VALU's limit is 1.26 P), with groups of 128 111 us; 16 x
  * 10240 x 6144 int4 16 us, bound by the latency of its stages.
  */
 constexpr int kStageK = 128;
@@ -911,16 +911,16 @@ int64_t n_tiles_of(int32_t S, int32_t N, int rows, int toks)
 }
 
 /* linear_rows_kernel's weight reads are the whole cost up to four tokens (S = 4,
- * N = 10240, K = 6144, int4: 11.3 us against 15.9 on the matrix cores; S = 8:
- * 17.4 against 15.9); shorter rows than a stage of the fold stay with it. */
+ * N = 10240, K = 6144, int4: 11.1 us against 15.7 on the matrix cores; S = 8:
+ * 17.4 against 15.7); shorter rows than a stage of the fold stay with it. */
 bool use_rows(int32_t S, int32_t K)
 {
     return S <= 4 || K < kStageK;
 }
 
 /* linear_tiles pays for the expansion where every CU has two of its tiles or
- * more (int4, bf16: 4096 x 10240 x 6144 523 us against 602 on the int8 cores;
- * 2048 x 4096 x 4096, one tile a CU, 94 against 90). */
+ * more (int4, bf16: 4096 x 10240 x 6144 490 us against 586 on the int8 cores;
+ * 2048 x 4096 x 4096, one tile a CU, 94 against 86 to 93). */
 bool use_tiles(int32_t S, int32_t N, int32_t K, int32_t group, int32_t out_type)
 {
     return !use_rows(S, K) && out_type == COLI_BF16 && !group && n_tiles_of(S, N, kTileN, 64 * kTileTT) >= 512;
@@ -969,11 +969,11 @@ hipError_t launch_tiles(const LinearArgs& a, hipStream_t s)
 }
 
 /* Shapes of the fold kernel, rows and tokens of a workgroup: 128 x 128 where
- * every CU gets one, else 64 x 64 (S = 512, N = K = 4096: 34.8 us, 46.7 with 128 x
- * 64), for up to 32 tokens 128 x 32.  A scale group's own sums take as many
+ * every CU gets one, else 64 x 64 (S = 512, N = K = 4096, int4: 33.4 us, 39.2 with
+ * 128 x 128), for up to 32 tokens 128 x 32.  A scale group's own sums take as many
  * registers again, so 128 x 128 is 128 x 64 with groups.  With fewer tiles than 512 the
  * stages are shared out as well, two at least each, and linear_join adds the
- * parts (S = 64, N = 10240, K = 6144, int8: 23.4 us against 33.4 with one
+ * parts (S = 64, N = 10240, K = 6144, int8: 21.4 us against 30.6 with one
  * workgroup per CU). */
 struct FoldPlan {
     int shape, rows, toks, n_tiles, t_tiles, stages, splits;
