@@ -274,8 +274,9 @@ def _batch(cache: KVCache, page_table, cu_q, kv_len, n_tokens: int, max_q: Optio
     _flat(page_table, torch.int32, (n, mp), "page_table")
     _flat(cu_q, torch.int32, (n + 1,), "cu_q")
     _flat(kv_len, torch.int32, (n,), "kv_len")
-    return KVBatchDesc(page_table.data_ptr(), cu_q.data_ptr(), kv_len.data_ptr(), n, mp, n_tokens,
-                       n_tokens if max_q is None else max_q)
+    if max_q is None:  # decode and verify steps have equal runs; of prompts nothing is known
+        max_q = -(-n_tokens // n) if 0 < n_tokens <= 16 * n else n_tokens
+    return KVBatchDesc(page_table.data_ptr(), cu_q.data_ptr(), kv_len.data_ptr(), n, mp, n_tokens, max_q)
 
 
 def _rows(t: torch.Tensor, n_heads: int, D: int, what: str) -> int:
@@ -344,8 +345,10 @@ def kv_attention(cache: KVCache, page_table: torch.Tensor, cu_q: torch.Tensor, k
     scale defaults to head_dim ** -0.5; causal: row i of sequence s sees the
     tokens up to its own, kv_len[s] - q_len + i, with window > 0 the last
     `window` of them.  lse fp32 [n_tokens][n_heads] receives the log of each
-    row's sum.  max_q and max_kv are the expected longest lengths (they shape
-    the launch, not the result).  ws: see kv_attention_workspace."""
+    row's sum.  max_q and max_kv are the expected longest lengths: they shape
+    the launch, not the result (by default the rows shared out evenly, or all
+    of them if that is more than 16 a sequence, and the table's capacity; a
+    max_kv far above the lengths costs time).  ws: see kv_attention_workspace."""
     dev, D = cache.k.device, cache.head_dim
     if not (q.dim() == 3):
         raise ValueError("q: [n_tokens][n_heads][head_dim] expected")
