@@ -161,8 +161,9 @@ int colibri_kv_read(const coli_kv_cache* cache, const coli_kv_batch* batch, void
  * cache head h / (n_heads / cache heads).  lse: fp32 [n_tokens][n_heads] or
  * null.  max_kv is the expected longest kv_len, used like max_q.  q and out
  * 16-byte aligned, strides multiples of 8, at least n_heads * head_dim; out
- * overlaps nothing.  scale is finite, of either sign.  A query with a NaN or an infinity gets NaN in its own
- * out and lse.  Scores, softmax statistics and sums are fp32; for bf16 the
+ * overlaps nothing.  scale is finite, of either sign; n_tokens * (n_heads /
+ * cache heads) is under 2^31.  A query with a NaN or an infinity gets NaN in its
+ * own out and lse.  Scores, softmax statistics and sums are fp32; for bf16 the
  * weights p enter the value product rounded to bf16, for fp32 as three bf16
  * terms.  ws as sized by colibri_kv_attention_workspace_bytes for the same
  * batch sizes (0: invalid arguments).

@@ -73,12 +73,13 @@ int check_batch(const coli_kv_batch* b)
     return COLI_OK;
 }
 
-int check_attn_sizes(const coli_kv_cache* c, const coli_kv_attn* a)
+int check_attn_sizes(const coli_kv_cache* c, const coli_kv_batch* b, const coli_kv_attn* a)
 {
     if (!a || a->n_heads < 1 || a->n_heads % c->n_heads || a->max_kv < 0 || a->window < 0 ||
         (a->window > 0 && !a->causal) || !isfinite(a->scale))
         return COLI_E_INVAL;
-    if (!is_type(a->type) || a->n_heads > 8 * COLI_MAX_KV_HEADS)
+    if (!is_type(a->type) || a->n_heads > 8 * COLI_MAX_KV_HEADS ||
+        (int64_t)b->n_tokens * (a->n_heads / c->n_heads) >= (int64_t)1 << 31)
         return COLI_E_UNSUPPORTED;
     return COLI_OK;
 }
@@ -190,7 +191,7 @@ int colibri_kv_read(const coli_kv_cache* cache, const coli_kv_batch* batch, void
 size_t colibri_kv_attention_workspace_bytes(const coli_kv_cache* cache, const coli_kv_batch* batch,
                                             const coli_kv_attn* attn)
 {
-    if (check_cache(cache) || check_batch_sizes(batch) || check_attn_sizes(cache, attn))
+    if (check_cache(cache) || check_batch_sizes(batch) || check_attn_sizes(cache, batch, attn))
         return 0;
     return kv_attention_workspace_bytes(*cache, *batch, *attn);
 }
@@ -199,7 +200,7 @@ int colibri_kv_attention(const coli_kv_cache* cache, const coli_kv_batch* batch,
                          void* ws, size_t ws_bytes, coli_stream_t stream)
 {
     int st = check_cache(cache);
-    if (st || (st = check_batch(batch)) || (st = check_attn_sizes(cache, attn)))
+    if (st || (st = check_batch(batch)) || (st = check_attn_sizes(cache, batch, attn)))
         return st;
     if (batch->n_seq == 0 || batch->n_tokens == 0)
         return COLI_OK;

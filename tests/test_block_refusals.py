@@ -158,6 +158,8 @@ def test_attention_workspace(L):
     assert L.colibri_kv_attention(r(cache()), r(batch()), r(attn()), P, 0, None) == WS
     assert L.colibri_kv_attention(r(cache()), r(batch()), None, P, 1 << 50, None) == INVAL
     assert L.colibri_kv_attention_workspace_bytes(r(cache()), r(batch()), r(attn(n_heads=5))) == 0
+    many = batch(n_tokens=1 << 30)
+    assert L.colibri_kv_attention(r(cache()), r(many), r(attn()), P, 1 << 62, None) == UNSUP
 
 
 def test_binding_refuses():
