@@ -457,10 +457,10 @@ int colibri_tier_prefetch(coli_tier* t, const float* x, int32_t S, coli_stream_t
  * 如何在我的低配置电脑上运行 GLM-5.2", section 已实现的功能, the native MTP
  * item) pass through tiers[0 .. n_layers - 1] in order, each layer's
  * forward being colibri_tier_forward's.
- *   x    device fp32 [n_layers][S][hidden]: layer l's input.  The attention
- *        and norms between the layers are not part of this library, so the
- *        caller supplies every layer's input (recorded or synthetic
- *        activations).
+ *   x    device fp32 [n_layers][S][hidden]: layer l's input.  The call
+ *        runs no attention or norm between the layers (colibri_block.h has
+ *        them), so the caller supplies every layer's input (recorded or
+ *        synthetic activations).
  *   out  device fp32 [n_layers][S][hidden]: layer l's output, bit-identical
  *        to colibri_tier_forward's and the resident forward's on x_l.
  *   lookahead  nonzero: the router look-ahead of the same section (the
