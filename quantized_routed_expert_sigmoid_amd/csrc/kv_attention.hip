@@ -436,8 +436,9 @@ __global__ __launch_bounds__(256, R == 32 && D > 128 ? 1 : 2) void kv_attention_
                 for (int i = 0; i < NA; ++i)
                     acc[d][i] = 0.0f;
 
-            /* a missing page reads page 0 and is masked as a whole; pieces past
-             * the range read its last one (loads are unconditional) */
+            /* a missing page reads page 0, whose scales may be anything: it is masked
+             * as a whole and both its scales are taken as 0; pieces past the range
+             * read its last one (loads are unconditional) */
             auto page_at = [&](int p) {
                 return __builtin_amdgcn_readfirstlane(page_of(g.b, g.c.n_pages, s, min(p, p1 - 1) * PT / kBlk));
             };
@@ -471,9 +472,9 @@ __global__ __launch_bounds__(256, R == 32 && D > 128 ? 1 : 2) void kv_attention_
                     const int after = page_at(p + 8);
                     load_k(next, p + 4);
                     const float ks_next = g.c.k_scale[at(next)], vs_next = g.c.v_scale[at(next)];
-                    const float c = unit_q * ks;
-                    const int base = p * PT;
                     const bool missing = page < 0;
+                    const float c = unit_q * (missing ? 0.0f : ks);
+                    const int base = p * PT;
                     if (missing || base + PT > sp.all_end || base < sp.all_begin)
                         mask_tile<R, NU>(t, base, missing ? 0 : sp.end, sp.begin, lg);
                     const float f = softmax_tile<R, NU * HS>(t, c, missing ? 0.0f : vs, m, l);

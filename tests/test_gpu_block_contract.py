@@ -1,0 +1,42 @@
+"""What the contract of the operators around the layer promises at its edges, on
+the GPU."""
+
+import pytest
+import torch
+
+from tests import block_ref as ref
+from tests.test_gpu_block import BF16, F32, dev, make_cache, qre, within  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+
+# ---- missing pages --------------------------------------------------------
+
+
+@pytest.mark.parametrize("bad", [float("nan"), -1.0, float("inf"), float("-inf")])
+@pytest.mark.parametrize("q_len", [1, 6, 80])
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
+def test_missing_page_takes_no_part(qre, dtype, q_len, bad):
+    """A missing page is seen by no query, whatever stands in the pool's first page (which need not be written)."""
+    D, H, Hq = 64, 2, 8
+    lens = [(q_len, 400), (q_len, 120), (q_len, 100)]
+    g, codes, scales, seqs, cache = make_cache(qre, lens, H, D, "first page")
+    used = set(seqs.table[seqs.table >= 0].tolist())
+    free = next(p for p in range(1, cache.n_pages) if p not in used)
+    seqs.table[seqs.table == 0] = free
+    seqs.table[0, 0] = -1
+    seqs.table[0, 4] = cache.n_pages
+    seqs.table[1, :] = -7
+    q = torch.randn(seqs.rows, Hq, D, generator=g).to(dtype)
+    results = []
+    for value in (1.0, bad):
+        cache.k_scale[0] = value
+        cache.v_scale[0] = value
+        lse = torch.full((seqs.rows, Hq), 3.0, device="cuda")
+        results.append((qre.kv_attention(cache, *dev(seqs), q.cuda(), max_q=q_len, max_kv=400, lse=lse), lse))
+    kval, vval = (ref.page_values(c, s, at) for c, s, at in zip(codes, scales, ref.page_bytes(D)))
+    want, lse64, sb, vb = ref.attention(kval, vval, seqs, q, D ** -0.5)
+    for out, lse in results:
+        within(out, want, ref.attention_tol(want, sb, vb, dtype), "out")
+        within(lse, lse64, ref.lse_tol(sb, lse64, dtype), "lse")
+    assert torch.equal(results[0][0], results[1][0]) and torch.equal(results[0][1], results[1][1])
