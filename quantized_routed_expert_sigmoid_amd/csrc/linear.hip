@@ -32,8 +32,8 @@ typedef int v16i __attribute__((ext_vector_type(16)));
 
 __device__ __forceinline__ float activate(float v, int act)
 {
-    if (act == COLI_ACT_RELU)
-        return fmaxf(v, 0.0f);
+    if (act == COLI_ACT_RELU) /* a NaN stays one */
+        return v <= 0.0f ? 0.0f : v;
     if (act == COLI_ACT_SILU) /* 2^-21: one rounding each of the product, the power and the reciprocal */
         return v * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(v * -1.44269504088896340736f));
     if (act == COLI_ACT_GELU)

@@ -5,7 +5,7 @@ import pytest
 import torch
 
 from tests import block_ref as ref
-from tests.test_gpu_block import BF16, F32, dev, make_cache, qre, within  # noqa: F401
+from tests.test_gpu_block import BF16, F32, dev, make_cache, make_linear, qre, within  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -40,3 +40,25 @@ def test_missing_page_takes_no_part(qre, dtype, q_len, bad):
         within(out, want, ref.attention_tol(want, sb, vb, dtype), "out")
         within(lse, lse64, ref.lse_tol(sb, lse64, dtype), "lse")
     assert torch.equal(results[0][0], results[1][0]) and torch.equal(results[0][1], results[1][1])
+
+
+# ---- NaN through the activations ------------------------------------------
+
+
+@pytest.mark.parametrize("S,N,K,dtype", [(1, 70, 256, F32), (4, 70, 256, BF16), (9, 70, 512, F32), (70, 70, 256, BF16),
+                                         (2049, 2050, 128, F32), (7700, 2100, 128, BF16)])
+@pytest.mark.parametrize("act", ["relu", "silu", "gelu"])
+def test_linear_keeps_nan(qre, S, N, K, dtype, act):
+    """A NaN in a bias, a row's scale or a token's scale comes out as NaN, and nowhere else."""
+    w, sc, q, d, bank, g = make_linear(qre, S, N, K, 8, 0, "nan")
+    bias = torch.randn(N, generator=g)
+    clean = qre.linear_q(bank, q.cuda(), d.cuda(), bias=bias.cuda(), activation=act, dtype=dtype)
+    bias[3] = float("nan")
+    bank.scale[0, 5] = float("nan")
+    d[S // 2, 1] = float("nan")
+    got = qre.linear_q(bank, q.cuda(), d.cuda(), bias=bias.cuda(), activation=act, dtype=dtype)
+    bad = torch.zeros(S, N, dtype=torch.bool, device="cuda")
+    bad[:, 3] = bad[:, 5] = True
+    bad[S // 2] = True
+    assert bool(torch.isnan(got[bad]).all())
+    assert torch.equal(got[~bad], clean[~bad])
