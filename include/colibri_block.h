@@ -77,7 +77,8 @@ int colibri_add_rms_norm(const coli_norm* n, coli_stream_t stream);
  * output's own rounding.
  * 1 <= rows <= COLI_MAX_LINEAR_ROWS, K <= COLI_MAX_LINEAR_K, K % 32 == 0;
  * xq and W->data 16-byte, out and residual 4-byte aligned.  ws as sized by
- * colibri_linear_workspace_bytes (0: invalid arguments).  S == 0 is a no-op.
+ * colibri_linear_workspace_bytes for this bank and type and for S or more
+ * tokens (0: invalid arguments).  S == 0 is a no-op.
  */
 size_t colibri_linear_workspace_bytes(const coli_qbank* W, int32_t S, int32_t out_type);
 int colibri_linear_q(const coli_qbank* W, const int8_t* xq, const float* xd, int32_t S, const float* bias,

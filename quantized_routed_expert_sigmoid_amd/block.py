@@ -179,7 +179,8 @@ def add_rms_norm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6, *,
 
 
 def linear_workspace(bank, S: int, dtype: torch.dtype = torch.float32) -> torch.Tensor:
-    """Workspace of linear_q for up to S tokens; calls that may overlap need one each."""
+    """Workspace of linear_q for any number of tokens up to S and outputs of this type; calls that may overlap need
+    one each."""
     return _linear_ws(bank.desc(), S, _type(dtype), bank.data.device)
 
 

@@ -30,7 +30,9 @@ struct LinearArgs {
     int32_t S, N, K, qtype, group, act, out_type;
 };
 
-size_t linear_workspace_bytes(int32_t S, int32_t N, int32_t K, int32_t qtype, int32_t group, int32_t out_type);
+/* What one call of S tokens needs; the most that one of 1 .. S tokens does. */
+size_t linear_workspace_need(int32_t S, int32_t N, int32_t K, int32_t group, int32_t out_type);
+size_t linear_workspace_bytes(int32_t S, int32_t N, int32_t K, int32_t group, int32_t out_type);
 hipError_t launch_linear_q(const LinearArgs& a, hipStream_t s);
 
 hipError_t launch_kv_append(const coli_kv_cache& c, const coli_kv_batch& b, const void* k, const void* v,

@@ -111,7 +111,7 @@ size_t colibri_linear_workspace_bytes(const coli_qbank* W, int32_t S, int32_t ou
 {
     if (check_linear(W, S, out_type))
         return 0;
-    return linear_workspace_bytes(S, W->rows, W->K, W->qtype, W->group, out_type);
+    return linear_workspace_bytes(S, W->rows, W->K, W->group, out_type);
 }
 
 int colibri_linear_q(const coli_qbank* W, const int8_t* xq, const float* xd, int32_t S, const float* bias,
@@ -130,7 +130,7 @@ int colibri_linear_q(const coli_qbank* W, const int8_t* xq, const float* xd, int
     if (!aligned(xq, 16) || !aligned(xd, 4) || !aligned(bias, 4) || !aligned(residual, 4) || !aligned(out, 4) ||
         !aligned(ws, kAlign))
         return COLI_E_UNSUPPORTED;
-    if (ws_bytes < linear_workspace_bytes(S, W->rows, W->K, W->qtype, W->group, out_type))
+    if (ws_bytes < linear_workspace_need(S, W->rows, W->K, W->group, out_type))
         return COLI_E_WORKSPACE;
     LinearArgs a;
     a.w = W->data;

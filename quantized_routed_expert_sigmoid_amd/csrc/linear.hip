@@ -1057,11 +1057,25 @@ hipError_t launch(const LinearArgs& a, hipStream_t s)
 
 } // namespace
 
-size_t linear_workspace_bytes(int32_t S, int32_t N, int32_t K, int32_t qtype, int32_t group, int32_t out_type)
+size_t linear_workspace_need(int32_t S, int32_t N, int32_t K, int32_t group, int32_t out_type)
 {
     if (use_rows(S, K))
         return 256;
     return use_tiles(S, N, K, group, out_type) ? tile_plan(S, N, K).total : fold_plan(S, N, K, group).total;
+}
+
+/* The largest need of 1 .. S tokens.  Fewer tokens are fewer tiles, whose split
+ * sums can take more than the whole of a larger call; the fold's plan changes
+ * with every 64 tokens (and at 32), and splits nothing past kWantTiles / 2 tiles. */
+size_t linear_workspace_bytes(int32_t S, int32_t N, int32_t K, int32_t group, int32_t out_type)
+{
+    size_t most = linear_workspace_need(S, N, K, group, out_type);
+    const int64_t ends = min((int64_t)(S + 63) / 64, kWantTiles / n_tiles_of(1, N, 128, 1));
+    for (int64_t t = 0; t <= ends; ++t) {
+        const int32_t fewer = (int32_t)min((int64_t)S, t ? 64 * t : 32);
+        most = max(most, linear_workspace_need(fewer, N, K, group, out_type));
+    }
+    return most;
 }
 
 hipError_t launch_linear_q(const LinearArgs& a, hipStream_t s)

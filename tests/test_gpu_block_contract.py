@@ -62,3 +62,18 @@ def test_linear_keeps_nan(qre, S, N, K, dtype, act):
     bad[S // 2] = True
     assert bool(torch.isnan(got[bad]).all())
     assert torch.equal(got[~bad], clean[~bad])
+
+
+# ---- workspaces of larger batches -----------------------------------------
+
+
+@pytest.mark.parametrize("N,K,bits,dtype", [(10240, 1024, 4, F32), (4096, 4096, 2, BF16), (130, 2080, 8, F32)])
+def test_linear_workspace_serves_smaller_batches(qre, N, K, bits, dtype):
+    """One workspace for the largest batch, calls of every smaller size in it; the same bits as with their own."""
+    most = 1024
+    w, sc, q, d, bank, g = make_linear(qre, most, N, K, bits, 0, "ws")
+    q, d = q.cuda(), d.cuda()
+    ws = qre.linear_workspace(bank, most, dtype)
+    for S in (1, 4, 5, 32, 33, 64, 65, 257, 512, most):
+        got = qre.linear_q(bank, q[:S], d[:S], dtype=dtype, ws=ws)
+        assert torch.equal(got, qre.linear_q(bank, q[:S], d[:S], dtype=dtype)), S
