@@ -166,8 +166,10 @@ int colibri_kv_read(const coli_kv_cache* cache, const coli_kv_batch* batch, void
  * cache heads) is under 2^31.  A query with a NaN or an infinity gets NaN in its
  * own out and lse.  Scores, softmax statistics and sums are fp32; for bf16 the
  * weights p enter the value product rounded to bf16, for fp32 as three bf16
- * terms.  ws as sized by colibri_kv_attention_workspace_bytes for the same
- * batch sizes (0: invalid arguments).
+ * terms.  ws as sized by colibri_kv_attention_workspace_bytes (0: invalid
+ * arguments) for this cache's n_heads and head_dim, this type and number of
+ * heads, and either exactly this n_seq, n_tokens, max_q and max_kv or, if
+ * n_tokens <= n_seq * max_q here, larger ones.
  */
 typedef struct coli_kv_attn {
     const void* q;

@@ -327,7 +327,8 @@ def kv_read(cache: KVCache, page_table: torch.Tensor, cu_q: torch.Tensor, kv_len
 
 def kv_attention_workspace(cache: KVCache, n_seq: int, n_tokens: int, n_heads: int, max_q: int, max_kv: int,
                            dtype: torch.dtype = torch.float32) -> torch.Tensor:
-    """Workspace of kv_attention for these sizes; calls that may overlap need one each."""
+    """Workspace of kv_attention for these sizes and for smaller ones of n_tokens <= n_seq * max_q; calls that may
+    overlap need one each."""
     b = KVBatchDesc(None, None, None, n_seq, 0, n_tokens, max_q)
     a = KVAttnDesc(None, None, None, 0, 0, _type(dtype), n_heads, 1, 0, max_kv, 1.0)
     n = _f().colibri_kv_attention_workspace_bytes(ctypes.byref(cache.desc), ctypes.byref(b), ctypes.byref(a))

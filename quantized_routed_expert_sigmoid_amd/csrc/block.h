@@ -40,6 +40,8 @@ hipError_t launch_kv_append(const coli_kv_cache& c, const coli_kv_batch& b, cons
 hipError_t launch_kv_read(const coli_kv_cache& c, const coli_kv_batch& b, void* k, void* v, int32_t type,
                           hipStream_t s);
 
+/* What one call of these sizes needs; the most that one of these or smaller sizes does. */
+size_t kv_attention_workspace_need(const coli_kv_cache& c, const coli_kv_batch& b, const coli_kv_attn& a);
 size_t kv_attention_workspace_bytes(const coli_kv_cache& c, const coli_kv_batch& b, const coli_kv_attn& a);
 hipError_t launch_kv_attention(const coli_kv_cache& c, const coli_kv_batch& b, const coli_kv_attn& a, void* ws,
                                hipStream_t s);

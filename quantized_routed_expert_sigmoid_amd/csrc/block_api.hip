@@ -211,7 +211,7 @@ int colibri_kv_attention(const coli_kv_cache* cache, const coli_kv_batch* batch,
     const int64_t least = (int64_t)attn->n_heads * cache->head_dim;
     if (!good_stride(attn->q_stride, least, 8) || !good_stride(attn->out_stride, least, 8))
         return COLI_E_INVAL;
-    if (ws_bytes < kv_attention_workspace_bytes(*cache, *batch, *attn))
+    if (ws_bytes < kv_attention_workspace_need(*cache, *batch, *attn))
         return COLI_E_WORKSPACE;
     return hip_status(launch_kv_attention(*cache, *batch, *attn, ws, (hipStream_t)stream));
 }

@@ -830,6 +830,17 @@ constexpr int64_t kTargetUnits = 512;
 constexpr int kMaxSplit = 256;
 constexpr int64_t kMaxSplitRows = 1 << 22; /* bounds the workspace and the join's grid */
 
+/* Bytes of n rows' partial sums, and with their statistics. */
+size_t sums_bytes(size_t n, int32_t D)
+{
+    return (n * D * 4 + kPartAlign - 1) / kPartAlign * kPartAlign;
+}
+
+size_t part_bytes(size_t n, int32_t D)
+{
+    return n == 0 ? kPartAlign : sums_bytes(n, D) + (n * 8 + kPartAlign - 1) / kPartAlign * kPartAlign;
+}
+
 Plan plan_attention(const coli_kv_cache& c, const coli_kv_batch& b, const coli_kv_attn& a)
 {
     Plan p;
@@ -849,10 +860,27 @@ Plan plan_attention(const coli_kv_cache& c, const coli_kv_batch& b, const coli_k
     if ((int64_t)b.n_tokens * a.n_heads > kMaxSplitRows)
         p.nsplit = 1;
     p.units = units * p.nsplit;
-    const size_t n = (size_t)p.nsplit * b.n_tokens * a.n_heads;
-    p.o_bytes = p.nsplit == 1 ? 0 : (n * c.head_dim * 4 + kPartAlign - 1) / kPartAlign * kPartAlign;
-    p.total = p.nsplit == 1 ? kPartAlign : p.o_bytes + (n * 8 + kPartAlign - 1) / kPartAlign * kPartAlign;
+    const size_t n = p.nsplit == 1 ? 0 : (size_t)p.nsplit * b.n_tokens * a.n_heads;
+    p.o_bytes = sums_bytes(n, c.head_dim);
+    p.total = part_bytes(n, c.head_dim);
     return p;
+}
+
+/* The partial sums of any call with sizes up to these and no more rows than
+ * n_seq * max_q.  A call that is split has u < kTargetUnits units (u < 256 of
+ * kTileRows) of at most R rows each in at most (kTargetUnits + u - 1) / u ranges;
+ * and it has no more rows than there are here, in no more ranges than its blocks
+ * or one unit per cache head allow. */
+size_t most_part_bytes(const coli_kv_cache& c, const coli_kv_batch& b, const coli_kv_attn& a)
+{
+    const int64_t rows = (int64_t)max(1, min(b.max_q, b.n_tokens)) * (a.n_heads / c.n_heads);
+    const int64_t R = rows > 32 ? kTileRows : rows <= 16 || a.type == COLI_F32 ? 16 : 32;
+    const int64_t u = min(R == kTileRows ? (int64_t)255 : kTargetUnits - 1,
+                          (int64_t)max(b.n_seq, 1) * c.n_heads * ((rows + R - 1) / R));
+    const int64_t splits = min(min((kTargetUnits + c.n_heads - 1) / c.n_heads,
+                                   ((int64_t)a.max_kv + 4 * kBlk - 1) / (4 * kBlk)), (int64_t)kMaxSplit);
+    const int64_t here = min((int64_t)b.n_tokens * a.n_heads, kMaxSplitRows) * splits;
+    return part_bytes(splits < 2 ? 0 : (size_t)min(here, R * (kTargetUnits + u - 1)), c.head_dim);
 }
 
 template <typename T, int D>
@@ -898,9 +926,15 @@ hipError_t launch_d(const AttnArgs& g, int rows, hipStream_t s)
 
 } // namespace
 
-size_t kv_attention_workspace_bytes(const coli_kv_cache& c, const coli_kv_batch& b, const coli_kv_attn& a)
+size_t kv_attention_workspace_need(const coli_kv_cache& c, const coli_kv_batch& b, const coli_kv_attn& a)
 {
     return plan_attention(c, b, a).total;
+}
+
+/* n_tokens may be above n_seq * max_q, which the second does not cover. */
+size_t kv_attention_workspace_bytes(const coli_kv_cache& c, const coli_kv_batch& b, const coli_kv_attn& a)
+{
+    return max(plan_attention(c, b, a).total, most_part_bytes(c, b, a));
 }
 
 hipError_t launch_kv_attention(const coli_kv_cache& c, const coli_kv_batch& b, const coli_kv_attn& a, void* ws,

@@ -25,3 +25,24 @@ def test_linear_workspace_grows_with_the_batch(L, N, K, bits, group, out_type):
                     1023, 1024, 1025, 2047, 2048, 2049, 4095, 4096, 8191, 8192, 16384, 65535, 65536})
     most = [L.colibri_linear_workspace_bytes(ctypes.byref(w), S, out_type) for S in sizes]
     assert all(a <= b for a, b in zip(most, most[1:])), list(zip(sizes, most))
+
+
+@pytest.mark.parametrize("heads,kv_heads,D", [(64, 8, 128), (8, 1, 64), (4, 4, 256), (48, 3, 192), (16, 16, 128)])
+@pytest.mark.parametrize("type_", [32, 16])
+def test_attention_workspace_grows_with_the_batch(L, heads, kv_heads, D, type_):
+    """A workspace for a batch serves one with fewer sequences, rows, rows of a sequence or cached tokens."""
+    c = block.KVCacheDesc(P, P, P, P, 64, kv_heads, D)
+
+    def size(n_seq, n_tokens, max_q, max_kv):
+        b = block.KVBatchDesc(None, None, None, n_seq, 0, n_tokens, max_q)
+        a = block.KVAttnDesc(None, None, None, 0, 0, type_, heads, 1, 0, max_kv, 1.0)
+        return L.colibri_kv_attention_workspace_bytes(ctypes.byref(c), ctypes.byref(b), ctypes.byref(a))
+
+    seqs, runs, kvs = (1, 2, 3, 5, 8, 16, 31, 32, 64, 100, 300), (1, 2, 3, 4, 5, 8, 9, 33, 128, 700, 2048), (1, 64, 500, 9000, 131072)
+    whole = {(n, q, kv): size(n, n * q, q, kv) for n in seqs for q in runs for kv in kvs}
+    for (n, q, kv), most in whole.items():
+        less = [whole[m, r, k] for m in seqs for r in runs for k in kvs if m <= n and r <= q and k <= kv]
+        assert most >= max(less), (n, q, kv)
+        for tokens in (1, q, (n * q + 1) // 2):
+            assert size(n, tokens, q, kv) <= most, (n, q, kv, tokens)
+        assert most <= 1 << 28  # a few rows in many ranges, or many rows in few

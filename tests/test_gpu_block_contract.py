@@ -77,3 +77,17 @@ def test_linear_workspace_serves_smaller_batches(qre, N, K, bits, dtype):
     for S in (1, 4, 5, 32, 33, 64, 65, 257, 512, most):
         got = qre.linear_q(bank, q[:S], d[:S], dtype=dtype, ws=ws)
         assert torch.equal(got, qre.linear_q(bank, q[:S], d[:S], dtype=dtype)), S
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
+def test_attention_workspace_serves_smaller_batches(qre, dtype):
+    """One workspace for the largest batch; fewer sequences, shorter runs and shorter caches in it."""
+    D, H, Hq, n = 64, 2, 8, 80
+    g, codes, scales, seqs, cache = make_cache(qre, [(40, 700)] * n, H, D, "ws")
+    ws = qre.kv_attention_workspace(cache, n, n * 40, Hq, 40, 700, dtype)
+    q = torch.randn(n * 40, Hq, D, generator=g).to(dtype).cuda()
+    for m, ql, kv in ((80, 40, 700), (80, 1, 700), (16, 1, 700), (1, 1, 700), (1, 40, 700), (3, 7, 500), (1, 1, 30)):
+        s = ref.Seqs([(ql, kv)] * m, seqs.table[:m].contiguous())
+        x = q[:m * ql]
+        got = qre.kv_attention(cache, *dev(s), x, max_q=ql, max_kv=kv, ws=ws)
+        assert torch.equal(got, qre.kv_attention(cache, *dev(s), x, max_q=ql, max_kv=kv)), (m, ql, kv)
