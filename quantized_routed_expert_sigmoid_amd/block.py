@@ -48,9 +48,11 @@ class KVAttnDesc(ctypes.Structure):
 
 
 # the current stream's handle and the current device's number, without the
-# objects that torch.cuda builds around them (a few microseconds a call)
-_raw_stream = torch._C._cuda_getCurrentRawStream
-_current_device = torch._C._cuda_getDevice
+# objects that torch.cuda builds around them (a few microseconds a call) where
+# this torch has them
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 _fns = None  # (the library, its entry points)
 

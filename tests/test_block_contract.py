@@ -1,6 +1,9 @@
 """What the contract of the operators around the layer promises on the host."""
 
 import ctypes
+import os
+import subprocess
+import sys
 
 import pytest
 
@@ -46,3 +49,21 @@ def test_attention_workspace_grows_with_the_batch(L, heads, kv_heads, D, type_):
         for tokens in (1, q, (n * q + 1) // 2):
             assert size(n, tokens, q, kv) <= most, (n, q, kv, tokens)
         assert most <= 1 << 28  # a few rows in many ranges, or many rows in few
+
+
+def test_package_imports_without_private_torch_symbols():
+    """A torch without the handles that the binding takes as a short cut (a CPU build) imports the package."""
+    code = """
+import torch
+for name in ("_cuda_getCurrentRawStream", "_cuda_getDevice"):
+    if hasattr(torch._C, name):
+        delattr(torch._C, name)
+import quantized_routed_expert_sigmoid_amd as qre
+try:
+    qre.add_rms_norm(torch.zeros(2, 64), torch.ones(64))
+except ValueError as e:
+    print("refused:", e)
+"""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "refused: device tensor" in r.stdout, r.stderr
