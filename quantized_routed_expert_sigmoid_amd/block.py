@@ -111,6 +111,13 @@ def _flat(t: Optional[torch.Tensor], dtype: torch.dtype, shape: tuple, what: str
     raise ValueError(f"{what}: contiguous tensor expected")
 
 
+def _room(ws: torch.Tensor):
+    """Address and bytes of a workspace."""
+    if not ws.is_contiguous():
+        raise ValueError("ws: contiguous tensor expected")
+    return ws.data_ptr(), ws.numel() * ws.element_size()
+
+
 def _call(dev: torch.device, name: str, *args):
     """Enqueues on the current stream of the tensors' device, which may not be the current one."""
     fn, index = getattr(_f(), name), dev.index
@@ -227,7 +234,7 @@ def linear_q(bank, xq: torch.Tensor, xd: torch.Tensor, *, bias: Optional[torch.T
     if ws is None:
         ws = _linear_ws(w, S, t, dev)
     _call(dev, "colibri_linear_q", ctypes.byref(w), xq.data_ptr(), xd.data_ptr(), S, _at(bias), _ACTS[activation],
-          _at(residual), out.data_ptr(), t, ws.data_ptr(), ws.numel() * ws.element_size())
+          _at(residual), out.data_ptr(), t, *_room(ws))
     return out
 
 
@@ -371,6 +378,5 @@ def kv_attention(cache: KVCache, page_table: torch.Tensor, cu_q: torch.Tensor, k
         ws = kv_attention_workspace(cache, b.n_seq, T, H, b.max_q, most, q.dtype)
     a = KVAttnDesc(q.data_ptr(), out.data_ptr(), _at(lse), qs, os, _type(q.dtype), H, 1 if causal else 0, window,
                    most, D ** -0.5 if scale is None else scale)
-    _call(dev, "colibri_kv_attention", ctypes.byref(cache.desc), ctypes.byref(b), ctypes.byref(a), ws.data_ptr(),
-          ws.numel() * ws.element_size())
+    _call(dev, "colibri_kv_attention", ctypes.byref(cache.desc), ctypes.byref(b), ctypes.byref(a), *_room(ws))
     return out

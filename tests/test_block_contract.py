@@ -6,6 +6,7 @@ import subprocess
 import sys
 
 import pytest
+import torch
 
 import quantized_routed_expert_sigmoid_amd as qre
 from quantized_routed_expert_sigmoid_amd import block
@@ -67,3 +68,12 @@ except ValueError as e:
     root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
     r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
     assert r.returncode == 0 and "refused: device tensor" in r.stdout, r.stderr
+
+
+def test_workspace_tensors_lie_in_one_piece():
+    """A view with gaps or repeats is refused: its bytes are not the ones that its size counts."""
+    whole = torch.empty(64, dtype=torch.uint8)
+    assert block._room(whole) == (whole.data_ptr(), 64) and block._room(torch.empty(8))[1] == 32
+    for t in (whole[::2], whole[:1].expand(64), whole.view(8, 8).t(), whole.view(8, 8)[:, :4]):
+        with pytest.raises(ValueError, match="ws: contiguous"):
+            block._room(t)

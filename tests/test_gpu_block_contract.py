@@ -91,3 +91,17 @@ def test_attention_workspace_serves_smaller_batches(qre, dtype):
         x = q[:m * ql]
         got = qre.kv_attention(cache, *dev(s), x, max_q=ql, max_kv=kv, ws=ws)
         assert torch.equal(got, qre.kv_attention(cache, *dev(s), x, max_q=ql, max_kv=kv)), (m, ql, kv)
+
+
+def test_workspace_with_gaps_is_refused(qre):
+    w, sc, q, d, bank, g = make_linear(qre, 40, 77, 416, 4, 32, "gaps")
+    n = qre.linear_workspace(bank, 40).numel()
+    for ws in (torch.empty(2 * n, dtype=torch.uint8, device="cuda")[::2],
+               torch.empty(256, dtype=torch.uint8, device="cuda")[:1].expand(n)):
+        with pytest.raises(ValueError, match="ws: contiguous"):
+            qre.linear_q(bank, q.cuda(), d.cuda(), ws=ws)
+    g, codes, scales, seqs, cache = make_cache(qre, [(1, 900)], 1, 64, "gaps")
+    n = qre.kv_attention_workspace(cache, 1, 1, 8, 1, 900).numel()
+    with pytest.raises(ValueError, match="ws: contiguous"):
+        qre.kv_attention(cache, *dev(seqs), torch.randn(1, 8, 64).cuda(), max_kv=900,
+                         ws=torch.empty(2 * n, dtype=torch.uint8, device="cuda")[::2])
