@@ -194,7 +194,7 @@ def linear_workspace(bank, S: int, dtype: torch.dtype = torch.float32) -> torch.
 
 
 def _linear_ws(w, S: int, t: int, dev: torch.device) -> torch.Tensor:
-    n = _f().colibri_linear_workspace_bytes(ctypes.byref(w), S, t)
+    n = _f().colibri_linear_workspace_bytes(ctypes.byref(w), _length(S), t)
     if n == 0:
         raise _qre.ColibriError(_qre.COLI_E_INVAL, "colibri_linear_workspace_bytes")
     return torch.empty(n, dtype=torch.uint8, device=dev)
@@ -275,6 +275,11 @@ class KVCache:
         return cls(k, v, ks, vs, head_dim)
 
 
+def _length(n: int) -> int:
+    """n in 32 bits: beyond them the largest number there is, below zero -1 (which the library refuses)."""
+    return -1 if n < 0 else min(n, 0x7FFFFFFF)
+
+
 def _batch(cache: KVCache, page_table, cu_q, kv_len, n_tokens: int, max_q: Optional[int]) -> KVBatchDesc:
     dev = cache.k.device
     _on(dev, page_table, cu_q, kv_len)
@@ -286,7 +291,7 @@ def _batch(cache: KVCache, page_table, cu_q, kv_len, n_tokens: int, max_q: Optio
     _flat(kv_len, torch.int32, (n,), "kv_len")
     if max_q is None:  # decode and verify steps have equal runs; of prompts nothing is known
         max_q = -(-n_tokens // n) if 0 < n_tokens <= 16 * n else n_tokens
-    return KVBatchDesc(page_table.data_ptr(), cu_q.data_ptr(), kv_len.data_ptr(), n, mp, n_tokens, max_q)
+    return KVBatchDesc(page_table.data_ptr(), cu_q.data_ptr(), kv_len.data_ptr(), n, mp, n_tokens, _length(max_q))
 
 
 def _rows(t: torch.Tensor, n_heads: int, D: int, what: str) -> int:
@@ -338,8 +343,8 @@ def kv_attention_workspace(cache: KVCache, n_seq: int, n_tokens: int, n_heads: i
                            dtype: torch.dtype = torch.float32) -> torch.Tensor:
     """Workspace of kv_attention for these sizes and for smaller ones of n_tokens <= n_seq * max_q; calls that may
     overlap need one each."""
-    b = KVBatchDesc(None, None, None, n_seq, 0, n_tokens, max_q)
-    a = KVAttnDesc(None, None, None, 0, 0, _type(dtype), n_heads, 1, 0, max_kv, 1.0)
+    b = KVBatchDesc(None, None, None, _length(n_seq), 0, _length(n_tokens), _length(max_q))
+    a = KVAttnDesc(None, None, None, 0, 0, _type(dtype), _length(n_heads), 1, 0, _length(max_kv), 1.0)
     n = _f().colibri_kv_attention_workspace_bytes(ctypes.byref(cache.desc), ctypes.byref(b), ctypes.byref(a))
     if n == 0:
         raise _qre.ColibriError(_qre.COLI_E_INVAL, "colibri_kv_attention_workspace_bytes")
@@ -376,7 +381,7 @@ def kv_attention(cache: KVCache, page_table: torch.Tensor, cu_q: torch.Tensor, k
     most = page_table.shape[1] * KV_BLOCK if max_kv is None else max_kv
     if ws is None:
         ws = kv_attention_workspace(cache, b.n_seq, T, H, b.max_q, most, q.dtype)
-    a = KVAttnDesc(q.data_ptr(), out.data_ptr(), _at(lse), qs, os, _type(q.dtype), H, 1 if causal else 0, window,
-                   most, D ** -0.5 if scale is None else scale)
+    a = KVAttnDesc(q.data_ptr(), out.data_ptr(), _at(lse), qs, os, _type(q.dtype), H, 1 if causal else 0, _length(window),
+                   _length(most), D ** -0.5 if scale is None else scale)
     _call(dev, "colibri_kv_attention", ctypes.byref(cache.desc), ctypes.byref(b), ctypes.byref(a), *_room(ws))
     return out

@@ -77,3 +77,10 @@ def test_workspace_tensors_lie_in_one_piece():
     for t in (whole[::2], whole[:1].expand(64), whole.view(8, 8).t(), whole.view(8, 8)[:, :4]):
         with pytest.raises(ValueError, match="ws: contiguous"):
             block._room(t)
+
+
+@pytest.mark.parametrize("given,want", [(0, 0), (7, 7), (-1, -1), (2 ** 31 - 1, 2 ** 31 - 1), (2 ** 31, 2 ** 31 - 1),
+                                        (2 ** 32 + 5, 2 ** 31 - 1), (2 ** 63, 2 ** 31 - 1), (5 - 2 ** 32, -1), (-2 ** 31 - 1, -1)])
+def test_lengths_do_not_wrap(given, want):
+    """A length beyond 32 bits counts as the largest, one below zero stays negative (and is refused)."""
+    assert block._length(given) == want

@@ -105,3 +105,15 @@ def test_workspace_with_gaps_is_refused(qre):
     with pytest.raises(ValueError, match="ws: contiguous"):
         qre.kv_attention(cache, *dev(seqs), torch.randn(1, 8, 64).cuda(), max_kv=900,
                          ws=torch.empty(2 * n, dtype=torch.uint8, device="cuda")[::2])
+
+
+@pytest.mark.parametrize("q_len", [1, 40])
+def test_window_beyond_32_bits_is_no_window(qre, q_len):
+    g, codes, scales, seqs, cache = make_cache(qre, [(q_len, 300)], 2, 64, "wide window")
+    q = torch.randn(q_len, 8, 64, generator=g).cuda()
+    want = qre.kv_attention(cache, *dev(seqs), q)
+    for window in (300, 2 ** 31 - 1, 2 ** 31, 2 ** 32 + 5, 2 ** 63 - 1):
+        assert torch.equal(qre.kv_attention(cache, *dev(seqs), q, window=window), want), window
+    for window in (-1, 5 - 2 ** 32):
+        with pytest.raises(qre.ColibriError):
+            qre.kv_attention(cache, *dev(seqs), q, window=window)
