@@ -24,6 +24,8 @@
  */
 #include "block_device.h"
 
+#include <algorithm>
+
 namespace coli {
 
 namespace {
@@ -845,16 +847,16 @@ Plan plan_attention(const coli_kv_cache& c, const coli_kv_batch& b, const coli_k
 {
     Plan p;
     const int G = a.n_heads / c.n_heads;
-    const int64_t rows = (int64_t)max(1, min(b.max_q, b.n_tokens)) * G;
+    const int64_t rows = (int64_t)std::max(1, std::min(b.max_q, b.n_tokens)) * G;
     p.rows = rows > 32 ? kTileRows : rows <= 16 || a.type == COLI_F32 ? 16 : 32;
     /* At most 2^27 units before the split, which adds none beyond kTargetUnits
      * twice over; a workgroup goes on to the row tiles that are left. */
-    const int64_t pairs = (int64_t)max(b.n_seq, 1) * c.n_heads;
-    p.row_tiles = (int)min((rows + p.rows - 1) / p.rows, max((int64_t)1, ((int64_t)1 << 27) / pairs));
+    const int64_t pairs = (int64_t)std::max(b.n_seq, 1) * c.n_heads;
+    p.row_tiles = (int)std::min((rows + p.rows - 1) / p.rows, std::max<int64_t>(1, ((int64_t)1 << 27) / pairs));
     const int64_t units = pairs * p.row_tiles;
-    const int64_t seen = a.window > 0 ? min((int64_t)a.max_kv, (int64_t)a.window + b.max_q) : a.max_kv;
+    const int64_t seen = a.window > 0 ? std::min<int64_t>(a.max_kv, (int64_t)a.window + b.max_q) : a.max_kv;
     const int64_t blocks = (seen + kBlk - 1) / kBlk, target = kTargetUnits;
-    p.nsplit = (int)max((int64_t)1, min(min((target + units - 1) / units, (blocks + 3) / 4), (int64_t)kMaxSplit));
+    p.nsplit = (int)std::max<int64_t>(1, std::min({(target + units - 1) / units, (blocks + 3) / 4, (int64_t)kMaxSplit}));
     if (p.rows == kTileRows && units >= 256)
         p.nsplit = 1;
     if ((int64_t)b.n_tokens * a.n_heads > kMaxSplitRows)
@@ -873,14 +875,14 @@ Plan plan_attention(const coli_kv_cache& c, const coli_kv_batch& b, const coli_k
  * or one unit per cache head allow. */
 size_t most_part_bytes(const coli_kv_cache& c, const coli_kv_batch& b, const coli_kv_attn& a)
 {
-    const int64_t rows = (int64_t)max(1, min(b.max_q, b.n_tokens)) * (a.n_heads / c.n_heads);
+    const int64_t rows = (int64_t)std::max(1, std::min(b.max_q, b.n_tokens)) * (a.n_heads / c.n_heads);
     const int64_t R = rows > 32 ? kTileRows : rows <= 16 || a.type == COLI_F32 ? 16 : 32;
-    const int64_t u = min(R == kTileRows ? (int64_t)255 : kTargetUnits - 1,
-                          (int64_t)max(b.n_seq, 1) * c.n_heads * ((rows + R - 1) / R));
-    const int64_t splits = min(min((kTargetUnits + c.n_heads - 1) / c.n_heads,
-                                   ((int64_t)a.max_kv + 4 * kBlk - 1) / (4 * kBlk)), (int64_t)kMaxSplit);
-    const int64_t here = min((int64_t)b.n_tokens * a.n_heads, kMaxSplitRows) * splits;
-    return part_bytes(splits < 2 ? 0 : (size_t)min(here, R * (kTargetUnits + u - 1)), c.head_dim);
+    const int64_t u = std::min(R == kTileRows ? 255 : kTargetUnits - 1,
+                               (int64_t)std::max(b.n_seq, 1) * c.n_heads * ((rows + R - 1) / R));
+    const int64_t splits = std::min({(kTargetUnits + c.n_heads - 1) / c.n_heads,
+                                     ((int64_t)a.max_kv + 4 * kBlk - 1) / (4 * kBlk), (int64_t)kMaxSplit});
+    const int64_t here = std::min((int64_t)b.n_tokens * a.n_heads, kMaxSplitRows) * splits;
+    return part_bytes(splits < 2 ? 0 : (size_t)std::min(here, R * (kTargetUnits + u - 1)), c.head_dim);
 }
 
 template <typename T, int D>
@@ -894,10 +896,10 @@ hipError_t launch(const AttnArgs& g, int rows, hipStream_t s)
             if (e != hipSuccess)
                 return e;
         }
-        hipLaunchKernelGGL((kv_attention_tile<T, D>), dim3(min((g.units + 7) / 8 * 8, 1u << 20)), dim3(256), bytes, s,
+        hipLaunchKernelGGL((kv_attention_tile<T, D>), dim3(std::min((g.units + 7) / 8 * 8, 1u << 20)), dim3(256), bytes, s,
                            g);
     } else {
-        const uint32_t grid = min(g.units, 1u << 20);
+        const uint32_t grid = std::min(g.units, 1u << 20);
         if (rows == 16)
             hipLaunchKernelGGL((kv_attention_split<T, 16, D>), dim3(grid), dim3(256), 0, s, g);
         else
@@ -934,7 +936,7 @@ size_t kv_attention_workspace_need(const coli_kv_cache& c, const coli_kv_batch& 
 /* n_tokens may be above n_seq * max_q, which the second does not cover. */
 size_t kv_attention_workspace_bytes(const coli_kv_cache& c, const coli_kv_batch& b, const coli_kv_attn& a)
 {
-    return max(plan_attention(c, b, a).total, most_part_bytes(c, b, a));
+    return std::max(plan_attention(c, b, a).total, most_part_bytes(c, b, a));
 }
 
 hipError_t launch_kv_attention(const coli_kv_cache& c, const coli_kv_batch& b, const coli_kv_attn& a, void* ws,

@@ -17,6 +17,7 @@
  */
 #include "block_device.h"
 
+#include <algorithm>
 #include <type_traits>
 
 namespace coli {
@@ -268,9 +269,9 @@ __global__ __launch_bounds__(kThreads) void kv_read_kernel(coli_kv_cache c, coli
  * and one where the run straddles; longer runs take several turns. */
 dim3 grid_of(const coli_kv_cache& c, const coli_kv_batch& b)
 {
-    const int rows = max(1, min(b.max_q, b.n_tokens));
+    const int rows = std::max(1, std::min(b.max_q, b.n_tokens));
     const int blocks = rows == 1 ? 1 : (rows - 2) / COLI_KV_BLOCK + 2;
-    return dim3((uint32_t)min(blocks, 1024), (uint32_t)c.n_heads * 2, (uint32_t)b.n_seq);
+    return dim3((uint32_t)std::min(blocks, 1024), (uint32_t)c.n_heads * 2, (uint32_t)b.n_seq);
 }
 
 template <typename F>

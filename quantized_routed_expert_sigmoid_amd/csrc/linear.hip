@@ -20,6 +20,8 @@
  */
 #include "block_device.h"
 
+#include <algorithm>
+
 namespace coli {
 
 namespace {
@@ -190,7 +192,7 @@ inline int rows_per_wg(int N)
     int shares = 256;
     while (N / shares >= 32 && shares < (1 << 20))
         shares *= 2;
-    return max(4, min(kMaxRowsWg, (N + shares - 1) / shares));
+    return std::max(4, std::min(kMaxRowsWg, (N + shares - 1) / shares));
 }
 
 template <int BITS, int T, int NU, typename TO>
@@ -956,7 +958,7 @@ hipError_t launch_tiles(const LinearArgs& a, hipStream_t s)
     ta.n_tiles = p.n_tiles;
     ta.t_tiles = p.t_tiles;
     ta.stages = p.stages;
-    const int per = max(1, min(8, p.tiles * p.stages / 512));
+    const int per = std::max(1, std::min(8, p.tiles * p.stages / 512));
     hipLaunchKernelGGL((linear_expand<BITS>), dim3(p.tiles, (p.stages + per - 1) / per), dim3(256), 0, s, a, xh, xs,
                        p.tiles, p.stages, per);
     constexpr int bytes = 2 * TileLds<BITS>::kStage;
@@ -992,7 +994,7 @@ FoldPlan fold_plan(int32_t S, int32_t N, int32_t K, int32_t group)
     p.n_tiles = (N + p.rows - 1) / p.rows;
     p.t_tiles = (S + p.toks - 1) / p.toks;
     const int total = p.n_tiles * p.t_tiles;
-    p.splits = max(1, min(kWantTiles / total, p.stages / 2));
+    p.splits = std::max(1, std::min(kWantTiles / total, p.stages / 2));
     p.total = p.splits > 1 ? (size_t)p.splits * total * p.rows * p.toks * 4 : 256;
     return p;
 }
@@ -1070,11 +1072,9 @@ size_t linear_workspace_need(int32_t S, int32_t N, int32_t K, int32_t group, int
 size_t linear_workspace_bytes(int32_t S, int32_t N, int32_t K, int32_t group, int32_t out_type)
 {
     size_t most = linear_workspace_need(S, N, K, group, out_type);
-    const int64_t ends = min((int64_t)(S + 63) / 64, kWantTiles / n_tiles_of(1, N, 128, 1));
-    for (int64_t t = 0; t <= ends; ++t) {
-        const int32_t fewer = (int32_t)min((int64_t)S, t ? 64 * t : 32);
-        most = max(most, linear_workspace_need(fewer, N, K, group, out_type));
-    }
+    const int ends = std::min((S + 63) / 64, kWantTiles / (int)n_tiles_of(1, N, 128, 1));
+    for (int t = 0; t <= ends; ++t)
+        most = std::max(most, linear_workspace_need(std::min(S, t ? 64 * t : 32), N, K, group, out_type));
     return most;
 }
 

@@ -11,6 +11,8 @@
  */
 #include "block_device.h"
 
+#include <algorithm>
+
 namespace coli {
 
 namespace {
@@ -93,7 +95,7 @@ hipError_t launch(const coli_norm& n, hipStream_t s)
     /* a launch's threads are counted in 32 bits */
     constexpr int kRows = 1 << 22;
     for (int64_t row0 = 0; row0 < n.rows; row0 += kRows) {
-        const dim3 grid((uint32_t)min(n.rows - row0, (int64_t)kRows)), block(kThreads);
+        const dim3 grid((uint32_t)std::min<int64_t>(n.rows - row0, kRows)), block(kThreads);
         if (n.K <= 1024)
             hipLaunchKernelGGL((add_rms_norm_kernel<TX, TR, TY, 1>), grid, block, 0, s, n, row0);
         else if (n.K <= 2048)

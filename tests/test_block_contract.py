@@ -84,3 +84,20 @@ def test_workspace_tensors_lie_in_one_piece():
 def test_lengths_do_not_wrap(given, want):
     """A length beyond 32 bits counts as the largest, one below zero stays negative (and is refused)."""
     assert block._length(given) == want
+
+
+def test_sizes_beyond_32_bits(L):
+    """Plans and workspace sizes are computed in 64 bits: activations of 4 GiB, partial sums of 139 GB (a longest run
+    of rows far below the real one), and a window beside which the cache's length is nothing."""
+    w = qre.QBankDesc(data=P, row_scale=P, n_mat=1, rows=1 << 20, K=1 << 15, qtype=4, group=0)
+    assert L.colibri_linear_workspace_bytes(ctypes.byref(w), 65536, 16) == (1 << 32) + 65536 * 4
+    c = block.KVCacheDesc(P, P, P, P, 64, 8, 128)
+
+    def size(n_tokens, window):
+        b = block.KVBatchDesc(None, None, None, 1, 0, n_tokens, 1)
+        a = block.KVAttnDesc(None, None, None, 0, 0, 32, 64, 1, window, 131072, 1.0)
+        return L.colibri_kv_attention_workspace_bytes(ctypes.byref(c), ctypes.byref(b), ctypes.byref(a))
+
+    assert size(65536, 0) == 64 * 65536 * 64 * (128 * 4 + 8)  # 64 ranges
+    for window in (131072, 2 ** 31 - 2, 2 ** 31 - 1):
+        assert size(65536, window) == size(65536, 0)
