@@ -280,7 +280,23 @@ def _length(n: int) -> int:
     return -1 if n < 0 else min(n, 0x7FFFFFFF)
 
 
-def _batch(cache: KVCache, page_table, cu_q, kv_len, n_tokens: int, max_q: Optional[int]) -> KVBatchDesc:
+def _longest(n_tokens: int, n_seq: int, least: int) -> int:
+    """The longest run of rows to expect of a batch of which nothing else is known.
+
+    Decode and verify steps have equal or nearly equal runs.  Otherwise one sequence may hold most of the rows, and
+    `least` is the run that fills the chip by itself: a longer one takes several turns there, where the shape for it
+    would start workgroups for every sequence as if each were as long (attention, 64 / 8 heads: 200 prompts of 40 rows
+    444 us, 1522 with all rows as the longest run; one prompt of 900 rows among 63 decoding sequences 197 us, 2388 with
+    the rows evenly shared out)."""
+    if n_seq == 0 or n_tokens == 0:
+        return n_tokens
+    even = -(-n_tokens // n_seq)
+    if n_tokens <= 4 * n_seq or (n_tokens <= 16 * n_seq and n_tokens % n_seq == 0):
+        return even
+    return min(n_tokens, max(2 * even, least))
+
+
+def _batch(cache: KVCache, page_table, cu_q, kv_len, n_tokens: int, max_q: Optional[int], least: int) -> KVBatchDesc:
     dev = cache.k.device
     _on(dev, page_table, cu_q, kv_len)
     if not (page_table.dim() == 2):
@@ -289,8 +305,8 @@ def _batch(cache: KVCache, page_table, cu_q, kv_len, n_tokens: int, max_q: Optio
     _flat(page_table, torch.int32, (n, mp), "page_table")
     _flat(cu_q, torch.int32, (n + 1,), "cu_q")
     _flat(kv_len, torch.int32, (n,), "kv_len")
-    if max_q is None:  # decode and verify steps have equal runs; of prompts nothing is known
-        max_q = -(-n_tokens // n) if 0 < n_tokens <= 16 * n else n_tokens
+    if max_q is None:
+        max_q = _longest(n_tokens, n, least)
     return KVBatchDesc(page_table.data_ptr(), cu_q.data_ptr(), kv_len.data_ptr(), n, mp, n_tokens, _length(max_q))
 
 
@@ -315,7 +331,7 @@ def kv_append(cache: KVCache, page_table: torch.Tensor, cu_q: torch.Tensor, kv_l
     ks, vs = _rows(k, H, D, "k"), _rows(v, H, D, "v")
     if not (k.shape[0] == v.shape[0] and k.dtype == v.dtype):
         raise ValueError("k and v: one length and type expected")
-    b = _batch(cache, page_table, cu_q, kv_len, k.shape[0], max_q)
+    b = _batch(cache, page_table, cu_q, kv_len, k.shape[0], max_q, 8192 // H)
     _call(cache.k.device, "colibri_kv_append", ctypes.byref(cache.desc), ctypes.byref(b), k.data_ptr(),
           v.data_ptr(), _type(k.dtype), ks, vs)
 
@@ -332,7 +348,7 @@ def kv_read(cache: KVCache, page_table: torch.Tensor, cu_q: torch.Tensor, kv_len
     _flat(v, dtype, shape, "v")
     k = torch.empty(shape, dtype=dtype, device=dev) if k is None else k
     v = torch.empty(shape, dtype=dtype, device=dev) if v is None else v
-    b = _batch(cache, page_table, cu_q, kv_len, n_tokens, max_q)
+    b = _batch(cache, page_table, cu_q, kv_len, n_tokens, max_q, 8192 // cache.n_heads)
     if n_tokens:
         _call(dev, "colibri_kv_read", ctypes.byref(cache.desc), ctypes.byref(b), k.data_ptr(), v.data_ptr(),
               _type(dtype))
@@ -362,9 +378,10 @@ def kv_attention(cache: KVCache, page_table: torch.Tensor, cu_q: torch.Tensor, k
     tokens up to its own, kv_len[s] - q_len + i, with window > 0 the last
     `window` of them.  lse fp32 [n_tokens][n_heads] receives the log of each
     row's sum.  max_q and max_kv are the expected longest lengths: they shape
-    the launch, not the result (by default the rows shared out evenly, or all
-    of them if that is more than 16 a sequence, and the table's capacity; a
-    max_kv far above the lengths costs time).  ws: see kv_attention_workspace."""
+    the launch, not the result (by default what the numbers of rows and
+    sequences suggest, and the table's capacity; a max_kv far above the lengths
+    costs time, and so does a max_q far from them).  ws: see
+    kv_attention_workspace."""
     dev, D = cache.k.device, cache.head_dim
     if not (q.dim() == 3):
         raise ValueError("q: [n_tokens][n_heads][head_dim] expected")
@@ -377,7 +394,7 @@ def kv_attention(cache: KVCache, page_table: torch.Tensor, cu_q: torch.Tensor, k
         raise ValueError("out: the shape and type of q expected")
     os = _rows(out, H, D, "out")
     _flat(lse, torch.float32, (T, H), "lse")
-    b = _batch(cache, page_table, cu_q, kv_len, T, max_q)
+    b = _batch(cache, page_table, cu_q, kv_len, T, max_q, 65536 // H)
     most = page_table.shape[1] * KV_BLOCK if max_kv is None else max_kv
     if ws is None:
         ws = kv_attention_workspace(cache, b.n_seq, T, H, b.max_q, most, q.dtype)

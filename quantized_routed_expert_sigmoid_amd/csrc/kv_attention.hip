@@ -853,6 +853,12 @@ Plan plan_attention(const coli_kv_cache& c, const coli_kv_batch& b, const coli_k
      * twice over; a workgroup goes on to the row tiles that are left. */
     const int64_t pairs = (int64_t)std::max(b.n_seq, 1) * c.n_heads;
     p.row_tiles = (int)std::min((rows + p.rows - 1) / p.rows, std::max<int64_t>(1, ((int64_t)1 << 27) / pairs));
+    /* An odd number where several sequences fill the chip: workgroups are dealt to
+     * the CUs in turn, and a power of two would give the tiles that short sequences
+     * do have to a few of them (one prompt of 900 among 63 decoding sequences: 334
+     * us with 60 tiles each, 194 with 61; 2000 among 63: 375 with 64, 230 with 65). */
+    if (p.rows == kTileRows && b.n_seq > 1 && pairs * p.row_tiles >= kTargetUnits)
+        p.row_tiles |= 1;
     const int64_t units = pairs * p.row_tiles;
     const int64_t seen = a.window > 0 ? std::min<int64_t>(a.max_kv, (int64_t)a.window + b.max_q) : a.max_kv;
     const int64_t blocks = (seen + kBlk - 1) / kBlk, target = kTargetUnits;

@@ -101,3 +101,12 @@ def test_sizes_beyond_32_bits(L):
     assert size(65536, 0) == 64 * 65536 * 64 * (128 * 4 + 8)  # 64 ranges
     for window in (131072, 2 ** 31 - 2, 2 ** 31 - 1):
         assert size(65536, window) == size(65536, 0)
+
+
+@pytest.mark.parametrize("T,n,least,want", [
+    (0, 0, 1024, 0), (7, 0, 1024, 7), (0, 5, 1024, 0), (64, 64, 1024, 1), (128, 32, 1024, 4), (50, 32, 1024, 2), (160, 32, 1024, 5),
+    (512, 32, 1024, 16), (963, 64, 1024, 963), (2063, 64, 1024, 1024), (8000, 200, 1024, 1024), (32768, 16, 1024, 4096),
+    (2048, 1, 1024, 2048), (5, 1, 1024, 5), (7000, 16, 8192, 7000)])
+def test_expected_run_of_rows(T, n, least, want):
+    """What is taken as the longest run of rows of a sequence where the caller does not say."""
+    assert block._longest(T, n, least) == want

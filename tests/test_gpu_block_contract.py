@@ -117,3 +117,30 @@ def test_window_beyond_32_bits_is_no_window(qre, q_len):
     for window in (-1, 5 - 2 ** 32):
         with pytest.raises(qre.ColibriError):
             qre.kv_attention(cache, *dev(seqs), q, window=window)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
+def test_mixed_batch_without_hints(qre, dtype):
+    """A long prompt among decoding sequences and short runs, no lengths given: append, read-back and attention."""
+    D, H, Hq = 64, 2, 8
+    lens = [(1, 200)] * 20 + [(700, 800)] + [(1, 90)] * 20 + [(0, 64), (30, 30)]
+    g, codes, scales, seqs, cache = make_cache(qre, lens, H, D, "mixed", str(dtype))
+    k, v = torch.randn(seqs.rows, H, D, generator=g).to(dtype), torch.randn(seqs.rows, H, D, generator=g).to(dtype)
+    qre.kv_append(cache, *dev(seqs), k.cuda(), v.cuda())
+    for at, was, sc, new, now, now_sc in zip(ref.page_bytes(D), codes, scales, (k, v), (cache.k, cache.v),
+                                             (cache.k_scale, cache.v_scale)):
+        want, want_sc = ref.append(was, sc, at, seqs, new)
+        assert torch.equal(now.cpu(), want) and torch.equal(now_sc.cpu(), want_sc)
+    kval, vval = (ref.page_values(c.cpu(), s.cpu(), at) for c, s, at in zip(
+        (cache.k, cache.v), (cache.k_scale, cache.v_scale), ref.page_bytes(D)))
+    got_k, got_v = qre.kv_read(cache, *dev(seqs), seqs.rows)
+    for got, val in ((got_k, kval), (got_v, vval)):
+        for s, (q, n) in enumerate(lens):
+            if q:
+                want = ref.tokens(val, seqs.table[s], n, cache.n_pages)[0][n - q:]
+                within(got[seqs.cu[s]:seqs.cu[s + 1]], want, ref.U[F32] * want.abs(), "read")
+    q = torch.randn(seqs.rows, Hq, D, generator=g).to(dtype)
+    want, lse64, sb, vb = ref.attention(kval, vval, seqs, q, D ** -0.5)
+    lse = torch.zeros(seqs.rows, Hq, device="cuda")
+    within(qre.kv_attention(cache, *dev(seqs), q.cuda(), lse=lse), want, ref.attention_tol(want, sb, vb, dtype), "out")
+    within(lse, lse64, ref.lse_tol(sb, lse64, dtype), "lse")
