@@ -164,9 +164,13 @@ int colibri_kv_read(const coli_kv_cache* cache, const coli_kv_batch* batch, void
  * 16-byte aligned, strides multiples of 8, at least n_heads * head_dim; out
  * overlaps nothing.  scale is finite, of either sign; n_tokens * (n_heads /
  * cache heads) is under 2^31.  A query with a NaN or an infinity gets NaN in its
- * own out and lse.  Scores, softmax statistics and sums are fp32; for bf16 the
- * weights p enter the value product rounded to bf16, for fp32 as three bf16
- * terms.  ws as sized by colibri_kv_attention_workspace_bytes (0: invalid
+ * own out and lse.  A query row enters the scores as whole multiples of a unit,
+ * its largest magnitude / 32512 for bf16 and / 8323072 for fp32: a score is off by
+ * at most half of one times |scale| sum_c |k_c|, and what lies 2^16 (fp32: 2^24)
+ * below the row's largest value takes no part.  Their products with the codes are
+ * exact, scores are rounded to fp32 once, softmax statistics and sums are fp32;
+ * for bf16 the weights p enter the value product rounded to bf16 (2^-8), for fp32
+ * as three bf16 terms.  ws as sized by colibri_kv_attention_workspace_bytes (0: invalid
  * arguments) for this cache's n_heads and head_dim, this type and number of
  * heads, and either exactly this n_seq, n_tokens, max_q and max_kv or, if
  * n_tokens <= n_seq * max_q here, larger ones.

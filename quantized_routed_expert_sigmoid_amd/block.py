@@ -380,7 +380,8 @@ def kv_attention(cache: KVCache, page_table: torch.Tensor, cu_q: torch.Tensor, k
     row's sum.  max_q and max_kv are the expected longest lengths: they shape
     the launch, not the result (by default what the numbers of rows and
     sequences suggest, and the table's capacity; a max_kv far above the lengths
-    costs time, and so does a max_q far from them).  ws: see
+    costs time, and so does a max_q far from them).  A score is off by up to the
+    row's largest |q| / 65024 (bf16; fp32: / 2^24) times |scale| sum |k|.  ws: see
     kv_attention_workspace."""
     dev, D = cache.k.device, cache.head_dim
     if not (q.dim() == 3):

@@ -8,12 +8,15 @@
  *
  * Scores on the int8 matrix cores.  A key is code * scale already, so q is
  * written once as a fixed-point number of int8 digits below its row's largest
- * value (two digits, 15 bits, for bf16 queries; three, 23 bits, for fp32):
- * the product with each digit is exact in int32, the codes enter the matrix
- * cores as they lie in memory, and one int32 -> fp32 conversion per score
- * carries q's, the block's and the softmax scale.  Values take the bf16
- * matrix cores: an int8 code is exact in bf16, p times the block's value scale
- * is rounded to bf16 (bf16 outputs) or split into three bf16 terms (fp32).
+ * value (two digits, 15 bits, for bf16 queries; three, 23 bits, for fp32).  That
+ * rounds it by up to half a unit, amax / 65024 or amax / 16646144, whatever the
+ * value's own size: a score is off by that times |scale| sum |k| at most, where
+ * fp32 products of bf16 queries would be exact.  The product with each digit is
+ * exact in int32, the codes enter the matrix cores as they lie in memory, and one
+ * int32 -> fp32 conversion per score carries q's, the block's and the softmax
+ * scale.  Values take the bf16 matrix cores: an int8 code is exact in bf16, p
+ * times the block's value scale is rounded to bf16 (bf16 outputs) or split into
+ * three bf16 terms (fp32).
  *
  * Tiles.  S^T = K Q^T with v_mfma_i32_32x32x32_i8 gives lane (row = l % 32,
  * h = l / 32) the scores of tokens 8 (i / 4) + 4 h + i % 4 of its query row.

@@ -1,10 +1,13 @@
 """What the contract of the operators around the layer promises at its edges, on
 the GPU."""
 
+import math
+
 import pytest
 import torch
 
 from tests import block_ref as ref
+from tests.gpu_common import say
 from tests.test_gpu_block import BF16, F32, dev, make_cache, make_linear, qre, within  # noqa: F401
 
 pytestmark = pytest.mark.gpu
@@ -144,3 +147,125 @@ def test_mixed_batch_without_hints(qre, dtype):
     lse = torch.zeros(seqs.rows, Hq, device="cuda")
     within(qre.kv_attention(cache, *dev(seqs), q.cuda(), lse=lse), want, ref.attention_tol(want, sb, vb, dtype), "out")
     within(lse, lse64, ref.lse_tol(sb, lse64, dtype), "lse")
+
+
+# ---- attention held to the queries that the kernel uses --------------------
+
+
+def fixed_point(q, dtype):
+    """The queries as the kernel takes them: integers of a row's unit, amax / (127 * 256) for bf16 and amax / (127 *
+    65536) for fp32 (fp32 arithmetic step by step). -> integers, units (float64)."""
+    x = q.float()
+    top = torch.tensor(127.0 * (65536 if dtype == F32 else 256))
+    amax = x.abs().amax(-1, keepdim=True)
+    up = amax * torch.where(amax < 2.0 ** -60, 2.0 ** 64, 1.0)
+    lift = torch.where(amax < 2.0 ** -60, torch.tensor(2.0 ** 64), torch.tensor(1.0))
+    f = torch.where(up == 0, torch.tensor(0.0), torch.div(top.expand_as(up), up))
+    n = torch.round(x * lift * f)
+    return n.double(), torch.div(torch.div(up, top), lift).double()
+
+
+def attention_bounds(codes, scales, seqs, q, scale, dtype):
+    """Causal attention in 64 bits on the kernel's fixed-point queries -> out, its bound, lse, its bound.
+
+    With T2 the largest |score| of a row in units of log 2 and W the largest |log2| of a value scale, an exponent
+    passes through five roundings of the score (log2 e, its product with the scale and the unit, the key scale, the
+    conversion), one of log2(w) - m, one of the fma and two of the waves' and ranges' factors: under 2^-24 (10 T2 +
+    8 (T2 + W + 8)), with 128 units for the low digits of fp32 queries; the exponentials' and the logarithm's own
+    errors are under 2^-20 together.  A weight enters the value product rounded once (bf16: 2^-8, three terms for
+    fp32: 2^-23); sums in fp32 pass through fewer than n / 8 + 128 additions."""
+    n_pages, H = codes[0].shape[:2]
+    T, Hq, D = q.shape
+    kval, vval = (ref.page_values(c, s, at) for c, s, at in zip(codes, scales, ref.page_bytes(D)))
+    ints, unit = fixed_point(q, dtype)
+    out, tol = torch.zeros(T, Hq, D, dtype=torch.float64), torch.zeros(T, Hq, D, dtype=torch.float64)
+    lse, lse_tol = torch.zeros(T, Hq, dtype=torch.float64), torch.zeros(T, Hq, dtype=torch.float64)
+    p_err = 2.0 ** -23 if dtype == F32 else 2.0 ** -8
+    for s, (ql, n) in enumerate(seqs.lens):
+        k, _ = ref.tokens(kval, seqs.table[s], n, n_pages)
+        v, _ = ref.tokens(vval, seqs.table[s], n, n_pages)
+        pages = seqs.table[s, :-(-n // ref.BLOCK)].long()
+        hidden = torch.arange(n)[None] > torch.arange(n - ql, n)[:, None]
+        rows = slice(seqs.cu[s], seqs.cu[s] + ql)
+        for h in range(Hq):
+            hk = h // (Hq // H)
+            z = scale * unit[rows, h] * (ints[rows, h] @ k[:, hk].t())
+            t2 = (z.abs().masked_fill(hidden, 0.0).amax(1, keepdim=True)) / math.log(2)
+            z = z.masked_fill(hidden, -math.inf)
+            W = scales[1][pages, hk].double().log2().abs().amax()
+            low = 128 * abs(scale) * unit[rows, h] * scales[0][pages, hk].double().amax() / math.log(2)
+            e = 2.0 ** -24 * (18 * t2 + 8 * (W + 8)) + low + 2.0 ** -20
+            m = z.amax(1, keepdim=True)
+            p = torch.exp(z - m)
+            l = p.sum(1, keepdim=True)
+            p = p / l
+            sums = (n / 8 + 128) * 2.0 ** -24
+            out[rows, h] = p @ v[:, hk]
+            tol[rows, h] = (2 * e + p_err + 2 * sums) * (p @ v[:, hk].abs()) + ref.U[dtype] * out[rows, h].abs() + 1e-30
+            lse[rows, h] = (m + torch.log(l)).squeeze(1)
+            lse_tol[rows, h] = (e + sums).squeeze(1) + 2.0 ** -22 * (1 + lse[rows, h].abs())
+    return out, tol, lse, lse_tol
+
+
+@pytest.mark.parametrize("lens,Hq,H,D", [([(1, 4100)], 8, 1, 128), ([(3, 3000), (3, 130)], 8, 2, 64), ([(6, 4000)], 8, 1, 128),
+                                         ([(70, 3900)], 4, 1, 64), ([(40, 1500), (1, 64)], 8, 2, 192), ([(2, 2500)], 2, 1, 256)])
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
+def test_attention_every_page_counts(qre, lens, Hq, H, D, dtype):
+    """Each page of a long context has a value dim of its own: a page left out, or counted twice, is out of bounds."""
+    say(f"pages {lens} {Hq}/{H} {D} {dtype}")
+    g, codes, scales, seqs, cache = make_cache(qre, lens, H, D, "own dim")
+    scales[1] = (0.5 + torch.rand(cache.n_pages, H, generator=g)) / 60
+    codes[1].zero_()
+    at = ref.page_bytes(D)[1]
+    for s, (_, n) in enumerate(lens):
+        for b in range(-(-n // ref.BLOCK)):
+            page = int(seqs.table[s, b])
+            codes[1][page][:, at[:, b % D]] = torch.randint(1, 128, (H, ref.BLOCK), generator=g).to(torch.int8)
+    cache.v.copy_(codes[1])
+    cache.v_scale.copy_(scales[1])
+    q = torch.randn(seqs.rows, Hq, D, generator=g).to(dtype)
+    want, tol, lse, ltol = attention_bounds(codes, scales, seqs, q, D ** -0.5, dtype)
+    assert bool((tol < 0.05 * want)[want > 0].all())  # zeros, or a page twice, would be found
+    got_lse = torch.zeros(seqs.rows, Hq, device="cuda")
+    for mq, mkv in ((max(x for x, _ in lens), max(n for _, n in lens)), (None, None), (1, 1)):
+        got = qre.kv_attention(cache, *dev(seqs), q.cuda(), max_q=mq, max_kv=mkv, lse=got_lse)
+        within(got, want, tol, f"max_q {mq} max_kv {mkv}")
+        within(got_lse, lse, ltol, "lse")
+
+
+@pytest.mark.parametrize("q_len", [1, 5, 50])
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
+def test_attention_of_sharp_scores(qre, q_len, dtype):
+    """One key far above the rest, value scales 2^12 apart: the result is that key's value, zeros are out of bounds."""
+    D, H, Hq = 128, 2, 4
+    g, codes, scales, seqs, cache = make_cache(qre, [(q_len, 400)], H, D, "sharp scores", v_spread=2.0)
+    q = (30 * torch.randn(q_len, Hq, D, generator=g)).to(dtype)
+    want, tol, lse, ltol = attention_bounds(codes, scales, seqs, q, 0.3, dtype)
+    assert float((tol < 0.1 * want.abs()).double().mean()) > 0.9
+    got_lse = torch.zeros(q_len, Hq, device="cuda")
+    within(qre.kv_attention(cache, *dev(seqs), q.cuda(), scale=0.3, lse=got_lse), want, tol, "sharp")
+    within(got_lse, lse, ltol, "lse")
+
+
+@pytest.mark.parametrize("q_len", [1, 40])
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
+def test_attention_of_an_outlier_channel(qre, q_len, dtype):
+    """One query channel 2000 times the others: a score is off by at most half a unit of the row, amax / 65024 (bf16)
+    or amax / 16646144 (fp32), times scale * sum |k|, and on the unit's integers the bounds are the usual ones."""
+    D, H, Hq = 128, 1, 8
+    g, codes, scales, seqs, cache = make_cache(qre, [(q_len, 300)], H, D, "outlier")
+    codes[0][:, :, ref.page_bytes(D)[0][:, 5]] = 0
+    cache.k.copy_(codes[0])
+    q = torch.randn(q_len, Hq, D, generator=g)
+    q[..., 5] = 2000.0
+    q = q.to(dtype)
+    want, tol, lse, ltol = attention_bounds(codes, scales, seqs, q, D ** -0.5, dtype)
+    got_lse = torch.zeros(q_len, Hq, device="cuda")
+    within(qre.kv_attention(cache, *dev(seqs), q.cuda(), lse=got_lse), want, tol, "outlier")
+    within(got_lse, lse, ltol, "lse")
+    kval, vval = (ref.page_values(c, s, at) for c, s, at in zip(codes, scales, ref.page_bytes(D)))
+    _, exact, _, _ = ref.attention(kval, vval, seqs, q, D ** -0.5)
+    pages = seqs.table[0, :5].long()
+    k_sum = kval[pages].abs().sum(-1).amax()
+    half = 2000.0 / (65024 if dtype == BF16 else 16646144) * (1 + 2.0 ** -20)
+    within(got_lse, exact, half * k_sum * D ** -0.5 + ltol, "lse of the queries themselves")
