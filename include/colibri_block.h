@@ -72,9 +72,11 @@ int colibri_add_rms_norm(const coli_norm* n, coli_stream_t stream);
  * fp32; their order depends on the shape, not on the data, so equal calls give
  * equal bits, but a token's result may differ in the last bits between batch
  * sizes.  Products inside a 32-element block are exact integers; only for bf16
- * outputs of very many tokens (one scale per row) the activations enter the
- * matrix cores rounded to fp16 instead, 2^-12 of their value, an eighth of the
- * output's own rounding.
+ * outputs of very many tokens (one scale per row) the activations xq * xd enter the
+ * matrix cores rounded to fp16 instead, by up to 2^-11 of their value (an eighth of
+ * the output's own 2^-8) or 2^-31 of the token's largest scale, whichever is more.
+ * SiLU is within 2^-23 (|v| + 8) of its value, GELU within 2^-22 of 1 + |v|.  NaN
+ * comes out as NaN.
  * 1 <= rows <= COLI_MAX_LINEAR_ROWS, K <= COLI_MAX_LINEAR_K, K % 32 == 0;
  * xq and W->data 16-byte, out and residual 4-byte aligned.  ws as sized by
  * colibri_linear_workspace_bytes for this bank and type and for S or more

@@ -15,8 +15,10 @@
  * - linear_tiles, bf16 outputs of very many tokens with one scale per row: the
  *   activations are written once as fp16 (linear_expand) and the fp16 matrix
  *   cores sum a whole row in fp32 with nothing to fold.  x = q d is scaled per
- *   token by a power of two and rounded to fp16, 2^-12 of each value, an eighth
- *   of what the output's own rounding to bf16 takes; a weight code is exact.
+ *   token by a power of two and rounded to fp16, by up to 2^-11 of a value, an
+ *   eighth of what the output's own rounding to bf16 takes; below fp16's normal
+ *   range by up to 2^-25 of the scaled value, which is 2^-31 of the token's largest
+ *   scale (127 of it lie above 2^13.98).  A weight code is exact.
  */
 #include "block_device.h"
 
@@ -36,7 +38,7 @@ __device__ __forceinline__ float activate(float v, int act)
 {
     if (act == COLI_ACT_RELU) /* a NaN stays one */
         return v <= 0.0f ? 0.0f : v;
-    if (act == COLI_ACT_SILU) /* 2^-21: one rounding each of the product, the power and the reciprocal */
+    if (act == COLI_ACT_SILU) /* the rounded exponent weighs 2^-23.4 |v|, power, sum, reciprocal and product 2^-21 */
         return v * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(v * -1.44269504088896340736f));
     if (act == COLI_ACT_GELU)
         return 0.5f * v * (1.0f + erff(v * 0.70710678118654752f));

@@ -269,3 +269,67 @@ def test_attention_of_an_outlier_channel(qre, q_len, dtype):
     k_sum = kval[pages].abs().sum(-1).amax()
     half = 2000.0 / (65024 if dtype == BF16 else 16646144) * (1 + 2.0 ** -20)
     within(got_lse, exact, half * k_sum * D ** -0.5 + ltol, "lse of the queries themselves")
+
+
+# ---- linear: plans and ranges ---------------------------------------------
+
+
+def linear_bound(y, A, K, dtype, half_prec=None):
+    """fp32 sums of K products (K / 16 + 40 roundings at most: blocks of 16 and more are summed by one instruction),
+    the scales' product by two roundings and, with half_prec = (|W|, largest scale of each token), activations in
+    fp16: half a step is 2^-11 of a value, or of the token's largest scale 2^-31 where the value leaves fp16's normal
+    range (the power of two puts 127 times that scale above 2^13.98, a subnormal's half step is 2^-25)."""
+    tol = ((K / 16 + 40) * 2.0 ** -24 + 2.0 ** -22) * A + ref.U[dtype] * y.abs() + 1e-36
+    if half_prec is not None:
+        w_sum, top = half_prec
+        tol = tol + 2.0 ** -11 * A + 2.0 ** -31 * top[:, None] * w_sum[None]
+    return tol
+
+
+@pytest.mark.parametrize("S,N,K,bits,group", [
+    (64, 200, 960, 8, 96), (40, 130, 960, 4, 160), (33, 70, 1920, 2, 96), (300, 257, 480, 4, 160), (70, 300, 640, 8, 64),
+    (20, 130, 1280, 4, 64), (9, 4101, 1120, 2, 160), (129, 64, 288, 8, 96), (2049, 2050, 480, 4, 96), (2049, 2050, 320, 2, 160),
+    (2049, 2050, 320, 8, 64)])
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
+def test_linear_groups_across_stages(qre, S, N, K, bits, group, dtype):
+    """Scale groups that neither divide a stage of 128 nor are multiples of it end inside stages and run across them."""
+    say(f"linear {S} x {N} x {K} int{bits} group {group} {dtype}")
+    w, sc, q, d, bank, g = make_linear(qre, S, N, K, bits, group, "groups")
+    y, A = ref.linear(w, sc, bits, group, q, d, None, None, None)
+    within(qre.linear_q(bank, q.cuda(), d.cuda(), dtype=dtype), y, linear_bound(y, A, K, dtype), "groups")
+
+
+@pytest.mark.parametrize("bits", [8, 4, 2])
+def test_linear_half_precision_range(qre, bits):
+    """Blocks of a token 2^10 to 2^28 apart in the form that holds activations in fp16; each weight row sees one of
+    them only, so that what a small block loses shows."""
+    S, N, K = 7700, 2100, 128
+    w, sc, q, d, bank, g = make_linear(qre, S, N, K, bits, 0, "half")
+    by = 32 * bits // 8
+    rows = torch.arange(N)
+    for b in range(4):
+        w[rows % 4 != b, by * b:by * (b + 1)] = 0
+    bank.data.copy_(w[None])
+    d = torch.rand(S, 1, generator=g) + 0.5
+    d = d * torch.tensor([1.0, 2.0 ** -24, 2.0 ** -28, 2.0 ** -10])
+    y, A = ref.linear(w, sc, bits, 0, q, d, None, None, None)
+    codes = ref.weight_codes(w, bits).double().abs().sum(1) * sc.double().abs()[:, 0]
+    tol = linear_bound(y, A, K, BF16, (codes, d.amax(1).double()))
+    assert float((tol < 0.1 * A)[:, 1::4].double().mean()) > 0.9
+    within(qre.linear_q(bank, q.cuda(), d.cuda(), dtype=BF16), y, tol, "range")
+
+
+@pytest.mark.parametrize("S", [1, 8])
+def test_linear_activations_over_their_range(qre, S):
+    """SiLU within 2^-23 (|v| + 8) of its value (the exponent's rounding grows with |v|), GELU within 2^-22 of 1 + |v|;
+    v is the bias."""
+    N, K = 4096, 128
+    v = torch.linspace(-86, 86, N)
+    bank = qre.QBank(torch.zeros(1, N, K, dtype=torch.uint8, device="cuda"), torch.ones(1, N, device="cuda"), 8)
+    q, d = torch.ones(S, K, dtype=torch.int8, device="cuda"), torch.ones(S, K // 32, device="cuda")
+    x = v.double()
+    silu, gelu = x * torch.special.expit(x), x * torch.special.ndtr(x)
+    for act, want, tol in (("silu", silu, 2.0 ** -23 * (x.abs() + 8) * silu.abs() + 1e-37),
+                           ("gelu", gelu, 2.0 ** -22 * (1 + x.abs())), ("relu", x.clamp(min=0), torch.zeros(N).double())):
+        got = qre.linear_q(bank, q, d, bias=v.cuda(), activation=act)
+        within(got, want.expand(S, N), tol.expand(S, N), act)
