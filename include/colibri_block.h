@@ -139,8 +139,8 @@ typedef struct coli_kv_batch {
  * that the block held before are requantised, c' = rnd(c * (s * (1/s'))), new
  * ones get rnd(v * (1/s')), rnd rounding half away from zero and clamping to
  * [-127, 127]; s' = 0 gives codes 0.  Rows with a negative token number are
- * skipped.  Values are finite.  A page that is written belongs to one sequence
- * of the batch.  16-byte (fp32) or 8-byte (bf16) aligned, strides multiples
+ * skipped.  Values are finite.  A page that is written stands once in the batch's
+ * table, in one place of one sequence.  16-byte (fp32) or 8-byte (bf16) aligned, strides multiples
  * of 4, at least n_heads * head_dim.
  */
 int colibri_kv_append(const coli_kv_cache* cache, const coli_kv_batch* batch, const void* k, const void* v,

@@ -8,7 +8,7 @@ import torch
 
 from tests import block_ref as ref
 from tests.gpu_common import say
-from tests.test_gpu_block import BF16, F32, dev, make_cache, make_linear, qre, within  # noqa: F401
+from tests.test_gpu_block import BF16, F32, block_forward, dev, gen, make_block, make_cache, make_linear, qre, within  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -333,3 +333,64 @@ def test_linear_activations_over_their_range(qre, S):
                            ("gelu", gelu, 2.0 ** -22 * (1 + x.abs())), ("relu", x.clamp(min=0), torch.zeros(N).double())):
         got = qre.linear_q(bank, q, d, bias=v.cuda(), activation=act)
         within(got, want.expand(S, N), tol.expand(S, N), act)
+
+
+# ---- as they are used -----------------------------------------------------
+
+
+def test_decode_steps_against_plain_forms(qre):
+    """A prompt, then token by token: every operator of every step against its plain form on the kernels' own inputs,
+    and the steps' parts together give what the block gives."""
+    B = make_block(qre)
+    hid, D, nh, nk = 256, B["D"], B["heads"], B["kv"]
+    g = gen("decode steps")
+    table = torch.randperm(12, generator=g).view(2, 6).int()
+    cache = B["cache"]
+    at = ref.page_bytes(D)
+    for t in (cache.k, cache.v):
+        t.zero_()
+    for t in (cache.k_scale, cache.v_scale):
+        t.fill_(float("nan"))  # pages that no token was written to
+    for lens in ([(62, 62), (33, 33)], [(1, 63), (1, 34)], [(1, 64), (1, 35)], [(1, 65), (1, 36)], [(3, 68), (3, 39)]):
+        sq = ref.Seqs(lens, table)
+        args, mq = dev(sq), max(q for q, _ in lens)
+        h, delta = torch.randn(sq.rows, hid, generator=g).cuda(), torch.randn(sq.rows, hid, generator=g).cuda()
+        held = [t.clone() for t in (cache.k, cache.v, cache.k_scale, cache.v_scale)]
+        whole = [t.clone() for t in block_forward(qre, B, h, delta, *args, max_q=mq)]
+        after = [t.clone() for t in (cache.k, cache.v, cache.k_scale, cache.v_scale)]
+        for t, x in zip((cache.k, cache.v, cache.k_scale, cache.v_scale), held):
+            t.copy_(x)
+
+        n = qre.add_rms_norm(delta, B["n1"], 1e-5, residual=h, y_dtype=F32)
+        t, y = ref.add_rms_norm(delta.cpu(), h.cpu(), B["n1"].cpu(), 1e-5)
+        within(n.sum, t, 2.0 ** -23 * t.abs(), "sum")
+        within(n.y, y, 2.0 ** -17 * y.abs(), "norm")
+        qkv = qre.linear_q(B["qkv"], n.q, n.d, bias=B["bias"])
+        w, A = ref.linear(B["qkv"].data[0].cpu(), B["qkv"].scale[0].cpu(), 4, 0, n.q.cpu(), n.d.cpu(), B["bias"].cpu(),
+                          None, None)
+        within(qkv, w, linear_bound(w, A, hid, F32), "qkv")
+        q, k, v = qkv.view(-1, nh + 2 * nk, D).split([nh, nk, nk], dim=1)
+        qre.kv_append(cache, *args, k, v, max_q=mq)
+        for a, was, sc, new, now, now_sc in zip(at, held[:2], held[2:], (k, v), (cache.k, cache.v),
+                                                (cache.k_scale, cache.v_scale)):
+            want, want_sc = ref.append(was.cpu(), sc.cpu(), a, sq, new.cpu())
+            fresh = ~torch.isnan(want_sc)
+            assert torch.equal(now_sc.cpu()[fresh], want_sc[fresh]) and bool(torch.isnan(now_sc.cpu()[~fresh]).all())
+            assert torch.equal(now.cpu(), want)
+        a = qre.kv_attention(cache, *args, q, max_q=mq)
+        codes = [cache.k.cpu(), cache.v.cpu()]
+        scales = [cache.k_scale.cpu().nan_to_num(1.0), cache.v_scale.cpu().nan_to_num(1.0)]
+        want, tol, _, _ = attention_bounds(codes, scales, sq, q.cpu().contiguous(), D ** -0.5, F32)
+        assert bool((tol < 0.01 * want.abs().amax()).all())
+        within(a, want, tol, "attention")
+        oq, od = qre.quantize_q8_0(a.view(sq.rows, -1))
+        s = qre.linear_q(B["o"], oq, od, residual=n.sum)
+        w, A = ref.linear(B["o"].data[0].cpu(), B["o"].scale[0].cpu(), 8, 0, oq.cpu(), od.cpu(), None, None, n.sum.cpu())
+        within(s, w, linear_bound(w, A, nh * D, F32), "output projection")
+        m = qre.add_rms_norm(s, B["n2"], 1e-5, y_dtype=F32, q8=False)
+        _, y = ref.add_rms_norm(s.cpu(), None, B["n2"].cpu(), 1e-5)
+        within(m.y, y, 2.0 ** -17 * y.abs(), "second norm")
+        assert torch.equal(s, whole[0]) and torch.equal(qre.moe_layer_forward(B["layer"], m.y), whole[1])
+        for t, x in zip((cache.k, cache.v, cache.k_scale, cache.v_scale), after):
+            assert torch.equal(t.nan_to_num(0.0) if t.is_floating_point() else t,
+                               x.nan_to_num(0.0) if x.is_floating_point() else x)
