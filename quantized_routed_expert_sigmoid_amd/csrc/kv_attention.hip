@@ -385,7 +385,7 @@ __device__ __forceinline__ float softmax_tile(float* t, float c, float w, float&
  * wave reads whole lines of a page).  The next piece's keys are in flight
  * under this piece's softmax and value product, its values under the next
  * scores.  Bound by the cache's bytes: 131071 tokens of 8 heads of 128 dims, fp32
- * queries, 51 us (5.3 TB/s); 32 sequences of up to 9000, 4 queries each, bf16, 97
+ * queries, 48 us (5.6 TB/s); 32 sequences of up to 9000, 4 queries each, bf16, 95
  * us (4.6 TB/s; ranges are equal shares of a sequence, the longest end last).
  * Twice as many ranges cost 25 % (each loads its query digits and joins four
  * waves).  A piece is a block, or half a block where the registers hold no more.
@@ -586,7 +586,7 @@ __global__ __launch_bounds__(256, R == 32 && D > 128 ? 1 : 2) void kv_attention_
  * Bound by the VALU: about 11 instructions per score and row, the exponential
  * four times the others, beside 33 + 32 cycles of the matrix cores for 64
  * scores.  Measured: 4 prompts of up to 2047 tokens over up to 4095, 64 / 8 heads
- * of 128 dims, bf16, 503 us = 0.77 PFLOP/s; a wave's matrix-core and VALU phases
+ * of 128 dims, bf16, 491 us = 0.79 PFLOP/s; a wave's matrix-core and VALU phases
  * follow each other, and two waves of a SIMD cover them in part.
  */
 constexpr int kTileRows = 128;

@@ -72,8 +72,8 @@ constexpr int kMaxRowsWg = 256; /* weight rows of a workgroup, most */
  * ahead of the products.  A unit lies inside one 32-element block, so its
  * exact integer dot product takes one pair of scales.  Rows longer than 64 NU
  * units go in several rounds, their sums kept in LDS.  Bound by the weights'
- * bytes: 1 x 10240 x 6144 int4 6.7 us (4.7 TB/s), 4 x 6144 x 8192 int8 with groups of
- * 128 11.5 us (4.4 TB/s).
+ * bytes: 1 x 10240 x 6144 int4 9.4 us with the weights in HBM (3.3 TB/s; 6.6 from the
+ * last-level cache), 4 x 6144 x 8192 int8 with groups of 128 13.4 us (3.9 TB/s; 11.4).
  */
 template <int BITS, int T, int NU, bool GROUPED, typename TO>
 __global__ __launch_bounds__(256) void linear_rows_kernel(LinearArgs a, int rows_wg)
@@ -425,7 +425,7 @@ struct TileArgs {
  * products, 36 KB of an int4 step, so that two workgroups share a CU.  Weights
  * stay packed in LDS and are unpacked by the waves that multiply them.  Lane
  * (l % 32, h = l / 32) of instruction i of a step takes k = 16 i + 8 h .. + 7.
- * Measured: 4096 x 10240 x 6144 int4 466 us and 24 us of linear_expand, 1.05
+ * Measured: 4096 x 10240 x 6144 int4 460 us and 23 us of linear_expand, 1.07
  * PFLOP/s (a bf16 library product of 8192^3: 1.45); without the unpacking 65 us
  * less; the matrix cores are busy half of the time, at 1.9 GHz.
  */
@@ -592,8 +592,9 @@ __global__ __launch_bounds__(256, 2) void linear_tiles(LinearArgs a, TileArgs ta
  * travel packed from memory to LDS one stage ahead.  Codes of fewer bits are
  * unpacked to the top of their bytes, 2^(8 - bits) times their value, which
  * the row's scale takes out again.  Measured: 2048 x 4096 x 4096 int4, fp32 out,
- * 88 us (780 TFLOP/s; the VALU's limit is 1.26 P), with groups of 128 111 us; 16 x
- * 10240 x 6144 int4 16 us, bound by the latency of its stages.
+ * 88 us (780 TFLOP/s; the VALU's limit is 1.26 P), with groups of 128 112 us; 16 x
+ * 10240 x 6144 int4 17 us with the weights in HBM (15 from the last-level cache), bound
+ * by the latency of its stages.
  */
 constexpr int kStageK = 128;
 
