@@ -190,11 +190,11 @@ def add_rms_norm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6, *,
 def linear_workspace(bank, S: int, dtype: torch.dtype = torch.float32) -> torch.Tensor:
     """Workspace of linear_q for any number of tokens up to S and outputs of this type; calls that may overlap need
     one each."""
-    return _linear_ws(bank.desc(), S, _type(dtype), bank.data.device)
+    return _linear_ws(bank.desc(), _length(S), _type(dtype), bank.data.device)
 
 
 def _linear_ws(w, S: int, t: int, dev: torch.device) -> torch.Tensor:
-    n = _f().colibri_linear_workspace_bytes(ctypes.byref(w), _length(S), t)
+    n = _f().colibri_linear_workspace_bytes(ctypes.byref(w), S, t)
     if n == 0:
         raise _qre.ColibriError(_qre.COLI_E_INVAL, "colibri_linear_workspace_bytes")
     return torch.empty(n, dtype=torch.uint8, device=dev)
@@ -233,8 +233,11 @@ def linear_q(bank, xq: torch.Tensor, xd: torch.Tensor, *, bias: Optional[torch.T
         out = torch.empty(S, w.rows, dtype=dtype, device=dev)
     if ws is None:
         ws = _linear_ws(w, S, t, dev)
+        room = ws.data_ptr(), ws.numel()
+    else:
+        room = _room(ws)
     _call(dev, "colibri_linear_q", ctypes.byref(w), xq.data_ptr(), xd.data_ptr(), S, _at(bias), _ACTS[activation],
-          _at(residual), out.data_ptr(), t, *_room(ws))
+          _at(residual), out.data_ptr(), t, *room)
     return out
 
 
@@ -275,9 +278,12 @@ class KVCache:
         return cls(k, v, ks, vs, head_dim)
 
 
+_MOST = 0x7FFFFFFF
+
+
 def _length(n: int) -> int:
     """n in 32 bits: beyond them the largest number there is, below zero -1 (which the library refuses)."""
-    return -1 if n < 0 else min(n, 0x7FFFFFFF)
+    return -1 if n < 0 else min(n, _MOST)
 
 
 def _longest(n_tokens: int, n_seq: int, least: int) -> int:
@@ -307,7 +313,9 @@ def _batch(cache: KVCache, page_table, cu_q, kv_len, n_tokens: int, max_q: Optio
     _flat(kv_len, torch.int32, (n,), "kv_len")
     if max_q is None:
         max_q = _longest(n_tokens, n, least)
-    return KVBatchDesc(page_table.data_ptr(), cu_q.data_ptr(), kv_len.data_ptr(), n, mp, n_tokens, _length(max_q))
+    elif not 0 <= max_q <= _MOST:
+        max_q = _length(max_q)
+    return KVBatchDesc(page_table.data_ptr(), cu_q.data_ptr(), kv_len.data_ptr(), n, mp, n_tokens, max_q)
 
 
 def _rows(t: torch.Tensor, n_heads: int, D: int, what: str) -> int:
@@ -399,7 +407,9 @@ def kv_attention(cache: KVCache, page_table: torch.Tensor, cu_q: torch.Tensor, k
     most = page_table.shape[1] * KV_BLOCK if max_kv is None else max_kv
     if ws is None:
         ws = kv_attention_workspace(cache, b.n_seq, T, H, b.max_q, most, q.dtype)
-    a = KVAttnDesc(q.data_ptr(), out.data_ptr(), _at(lse), qs, os, _type(q.dtype), H, 1 if causal else 0, _length(window),
-                   _length(most), D ** -0.5 if scale is None else scale)
+    if not (0 <= window <= _MOST and 0 <= most <= _MOST):
+        window, most = _length(window), _length(most)
+    a = KVAttnDesc(q.data_ptr(), out.data_ptr(), _at(lse), qs, os, _type(q.dtype), H, 1 if causal else 0, window, most,
+                   D ** -0.5 if scale is None else scale)
     _call(dev, "colibri_kv_attention", ctypes.byref(cache.desc), ctypes.byref(b), ctypes.byref(a), *_room(ws))
     return out

@@ -1075,6 +1075,8 @@ size_t linear_workspace_need(int32_t S, int32_t N, int32_t K, int32_t group, int
 size_t linear_workspace_bytes(int32_t S, int32_t N, int32_t K, int32_t group, int32_t out_type)
 {
     size_t most = linear_workspace_need(S, N, K, group, out_type);
+    if (use_rows(S, K)) /* and so do fewer tokens */
+        return most;
     const int ends = std::min((S + 63) / 64, kWantTiles / (int)n_tiles_of(1, N, 128, 1));
     for (int t = 0; t <= ends; ++t)
         most = std::max(most, linear_workspace_need(std::min(S, t ? 64 * t : 32), N, K, group, out_type));
