@@ -32,38 +32,38 @@ DEV = "cuda"
 def listed():
     return [
         # the token of one decode step: latency
-        {"name": "embed, one token", "op": "embed", "n": 1, "rows": 131071, "k": 6144, "bits": 4, "group": 0,
+        {"name": "embed one token", "op": "embed", "n": 1, "rows": 131071, "k": 6144, "bits": 4, "group": 0,
          "dtype": "f32"},
         # a prompt's tokens from a table with group scales
-        {"name": "embed, prompt", "op": "embed", "n": 8191, "rows": 131071, "k": 6144, "bits": 8, "group": 128,
+        {"name": "embed prompt", "op": "embed", "n": 8191, "rows": 131071, "k": 6144, "bits": 8, "group": 128,
          "dtype": "bf16"},
         # query, key and value projection of one decoded token
-        {"name": "linear, one token", "op": "linear", "s": 1, "n": 10240, "k": 6144, "bits": 4, "act": "none",
+        {"name": "linear one token", "op": "linear", "s": 1, "n": 10240, "k": 6144, "bits": 4, "act": "none",
          "bias": True, "residual": False, "dtype": "bf16"},
         # the vocabulary's projection of a decode batch: one large bank read once
-        {"name": "linear, vocabulary", "op": "linear", "s": 13, "n": 131071, "k": 6144, "bits": 8, "act": "none",
+        {"name": "linear vocabulary", "op": "linear", "s": 13, "n": 131071, "k": 6144, "bits": 8, "act": "none",
          "bias": False, "residual": False, "dtype": "f32"},
         # a short ragged prompt, two-bit weights, odd sizes
-        {"name": "linear, odd sizes", "op": "linear", "s": 333, "n": 4101, "k": 2080, "bits": 2, "act": "silu",
+        {"name": "linear odd sizes", "op": "linear", "s": 333, "n": 4101, "k": 2080, "bits": 2, "act": "silu",
          "bias": True, "residual": True, "dtype": "f32"},
         # query, key and value projection of a long prompt
-        {"name": "linear, prompt", "op": "linear", "s": 4096, "n": 10240, "k": 6144, "bits": 8, "act": "none",
+        {"name": "linear prompt", "op": "linear", "s": 4096, "n": 10240, "k": 6144, "bits": 8, "act": "none",
          "bias": True, "residual": False, "dtype": "bf16"},
         # one chat's next token: latency
-        {"name": "logits, one row", "op": "logits", "n_seq": 1, "drafts": 1, "v": 131071, "history": 701, "bias": 20,
+        {"name": "logits one row", "op": "logits", "n_seq": 1, "drafts": 1, "v": 131071, "history": 701, "bias": 20,
          "masked": True, "write": False, "dtype": "f32"},
         # a verify step of a serving batch, all adjusted logits wanted
-        {"name": "logits, verify batch", "op": "logits", "n_seq": 32, "drafts": 4, "v": 151003, "history": 4001,
+        {"name": "logits verify batch", "op": "logits", "n_seq": 32, "drafts": 4, "v": 151003, "history": 4001,
          "bias": 300, "masked": True, "write": True, "dtype": "bf16"},
         # a decode step of long contexts
-        {"name": "logits, long contexts", "op": "logits", "n_seq": 48, "drafts": 1, "v": 200001, "history": 131072,
+        {"name": "logits long contexts", "op": "logits", "n_seq": 48, "drafts": 1, "v": 200001, "history": 131072,
          "bias": 0, "masked": False, "write": True, "dtype": "f32"},
         # a verify step's pages: four tokens more for each sequence, the rejected ones taken back: latency
-        {"name": "pages, verify step", "op": "pages", "kind": "verify", "n_seq": 64, "max_kv": 9000, "hkv": 8, "d": 128},
+        {"name": "pages verify step", "op": "pages", "kind": "verify", "n_seq": 64, "max_kv": 9000, "hkv": 8, "d": 128},
         # a step of a beam search: the losing half freed, the other forked, one token each, the shared last pages copied
-        {"name": "pages, beams", "op": "pages", "kind": "beams", "n_seq": 256, "max_kv": 4001, "hkv": 8, "d": 128},
+        {"name": "pages beams", "op": "pages", "kind": "beams", "n_seq": 256, "max_kv": 4001, "hkv": 8, "d": 128},
         # half of the sequences end and the rest move together
-        {"name": "pages, compact", "op": "pages", "kind": "compact", "n_seq": 96, "max_kv": 9000, "hkv": 8, "d": 128},
+        {"name": "pages compact", "op": "pages", "kind": "compact", "n_seq": 96, "max_kv": 9000, "hkv": 8, "d": 128},
     ]
 
 
