@@ -1,0 +1,118 @@
+/*
+ * colibri_step.h -- C ABI of the operators of a serving step, part of
+ * libcolibri.so: what lies between token ids and the next token ids around the
+ * layers and the operators of colibri_block.h.  The embedding lookup, the paged
+ * cache's sequences from step to step, the linear product with one activation
+ * scale per token, and what is done to logits.
+ *
+ * The conventions at the top of colibri.h hold, and its status codes, banks and
+ * streams are used, as are the element types, activations and cache of
+ * colibri_block.h.  What lives in device memory is read by the kernels, so every
+ * call here can be captured into a graph and replayed on changed contents.
+ * Equal calls give equal bits.
+ */
+#ifndef COLIBRI_STEP_H
+#define COLIBRI_STEP_H
+
+#include "colibri_block.h"
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+/* Types of token ids in colibri_embed_q. */
+enum { COLI_I32 = 4, COLI_I64 = 8 };
+
+/*
+ * Embedding lookup: rows of a bank of one matrix [rows][K],
+ *   out[i][c] = (code(ids[i], c) * scale(ids[i], c)) * scale
+ * in fp32, rounded once more to out_type.  An id outside [0, rows) (padding)
+ * gives a row of zeros.  ids: id_type [n]; out: out_type [n][K], 16-byte aligned.
+ * rows <= COLI_MAX_LINEAR_ROWS, K <= COLI_MAX_LINEAR_K, n <= COLI_MAX_TOKENS; scale
+ * is finite.  n == 0 is a no-op.
+ */
+int colibri_embed_q(const coli_qbank* W, const void* ids, int32_t id_type, int32_t n, float scale, void* out,
+                    int32_t out_type, coli_stream_t stream);
+
+/*
+ * The sequences of a paged cache, whose page numbers are shared by the caches of
+ * all layers.  Sequence s has kv_len[s] tokens; with blocks = ceil(kv_len[s] / 64)
+ * the entries page_table[s][0 .. blocks-1] hold its pages, the others are not
+ * read.  refs[p] is the number of entries that hold page p: 0 for a free page, more
+ * than 1 for one that sequences share.  refs int32 [n_pages], page_table int32
+ * [n_seq][max_pages] and kv_len int32 [n_seq] are device memory and are the page_table
+ * and kv_len of a coli_kv_batch of these sequences.  An empty state has refs and
+ * kv_len 0.  An entry outside [0, n_pages) holds no page.  kv_len is taken as at
+ * least 0 and at most max_pages * 64.  n_pages <= COLI_MAX_PAGES.
+ */
+#define COLI_MAX_PAGES (1 << 26)
+
+typedef struct coli_kv_pages {
+    int32_t* refs;
+    int32_t* page_table;
+    int32_t* kv_len;
+    int32_t n_pages, n_seq, max_pages;
+} coli_kv_pages;
+
+/* Workspace of colibri_kv_extend and colibri_kv_compact for these sizes (the
+ * pointers are not looked at; 0: invalid sizes). */
+size_t colibri_kv_pages_workspace_bytes(const coli_kv_pages* pages);
+
+/*
+ * Room for add[s] more tokens of each sequence (add[s] <= 0: none), as
+ * colibri_kv_append needs it: the blocks that the new tokens touch get pages of
+ * their own.  New blocks take free pages; where the last block is partly filled
+ * and its page is shared (refs > 1 before the call), the sequence leaves that page
+ * for a free one, and src[s] and dst[s] become the two page numbers: the caller
+ * copies src to dst in every layer's cache (colibri_kv_copy) before another call
+ * changes pages; else both are -1.  Sequences are served in order, each with the
+ * lowest free pages that are left, its copy's first.  granted[s] = add[s] and
+ * kv_len[s] grows by it; or granted[s] = 0 and nothing of the sequence changes:
+ * where it would outgrow max_pages, or where the needs of this and the earlier
+ * sequences together (those that outgrow their table apart) are more than the pages
+ * that were free.  add, granted, src, dst int32 [n_seq] without overlap.
+ */
+int colibri_kv_extend(const coli_kv_pages* pages, const int32_t* add, int32_t* granted, int32_t* src, int32_t* dst,
+                      void* ws, size_t ws_bytes, coli_stream_t stream);
+
+/*
+ * Shortens sequences: where 0 <= new_len[s] < kv_len[s] the blocks from
+ * ceil(new_len[s] / 64) on are given up (their entries become -1, a page that no entry
+ * holds any more is free) and kv_len[s] = new_len[s]; 0 frees the sequence, a
+ * negative number leaves it as it is.  new_len int32 [n_seq].
+ */
+int colibri_kv_trim(const coli_kv_pages* pages, const int32_t* new_len, coli_stream_t stream);
+
+/*
+ * Forks sequences: child[i], an empty one, becomes parent[i]'s equal and shares its
+ * pages; nothing is copied before one of them grows (colibri_kv_extend).  Skipped
+ * are pairs i with a number outside [0, n_seq), whose child is not empty, whose
+ * child an earlier pair names too, or whose parent is any pair's child.  parent
+ * and child int32 [n].  n <= COLI_MAX_SEQS; n == 0 is a no-op.
+ */
+int colibri_kv_fork(const coli_kv_pages* pages, const int32_t* parent, const int32_t* child, int32_t n,
+                    coli_stream_t stream);
+
+/*
+ * Moves the used pages (refs > 0) together: with n_live of them, the used pages from
+ * n_live on take the places of the free ones below it, both in ascending order.
+ * Tables and refs follow; src[j] -> dst[j] are the moves, whose copies the caller makes
+ * (colibri_kv_copy) in every layer's cache, the rest of src and dst is -1.  src, dst
+ * int32 [n_pages / 2] and n_live int32 [1], without overlap.
+ */
+int colibri_kv_compact(const coli_kv_pages* pages, int32_t* src, int32_t* dst, int32_t* n_live, void* ws,
+                       size_t ws_bytes, coli_stream_t stream);
+
+/*
+ * Copies pages with their scales, page src[i] of `from` to page dst[i] of `to` (the
+ * same cache, or one of as many heads and dims).  Pairs with a number outside its
+ * cache are skipped.  No page is written twice, and none that is read.  src, dst int32
+ * [n].  n == 0 is a no-op.
+ */
+int colibri_kv_copy(const coli_kv_cache* from, const coli_kv_cache* to, const int32_t* src, const int32_t* dst,
+                    int32_t n, coli_stream_t stream);
+
+#ifdef __cplusplus
+}
+#endif
+#endif

@@ -506,3 +506,6 @@ def tier_verify_step(tiers: Sequence[TieredLayer], x: torch.Tensor, out: torch.T
 # The operators around the layer (block.py).
 from .block import (KVCache, NormResult, add_rms_norm, kv_append, kv_attention, kv_attention_workspace,  # noqa: E402
                     kv_page_shape, kv_read, linear_q, linear_workspace)
+# The operators of a serving step (step.py).
+from .step import (KVExtend, KVMoves, KVPages, embed_q, kv_compact, kv_copy, kv_extend, kv_fork,  # noqa: E402
+                   kv_pages_workspace, kv_trim)

@@ -1,0 +1,512 @@
+/*
+ * kv_pages.hip -- the sequences of a paged cache from step to step: room for new
+ * tokens, shortening and freeing, forks, moving the used pages together, and the
+ * copies of pages that follow (include/colibri_step.h gives the rules).
+ *
+ * All but the copy work on a few integers and cost their launches: they are split
+ * where one workgroup's turns over the pages would cost more than a second launch.
+ * Which page goes where follows from counts in page and sequence order alone,
+ * never from the order in which workgroups run.
+ */
+#include "block_device.h"
+#include "step.h"
+
+#include <algorithm>
+
+namespace coli {
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kOwn = 16;                    /* pages of a thread */
+constexpr int kSlice = kThreads * kOwn;     /* and of a workgroup */
+
+__device__ __forceinline__ int len_of(const coli_kv_pages& p, int s)
+{
+    return (int)min((int64_t)max(p.kv_len[s], 0), (int64_t)p.max_pages * COLI_KV_BLOCK);
+}
+
+__device__ __forceinline__ int blocks_of(int64_t len)
+{
+    return (int)((len + COLI_KV_BLOCK - 1) / COLI_KV_BLOCK);
+}
+
+__device__ __forceinline__ bool is_page(const coli_kv_pages& p, int page)
+{
+    return (uint32_t)page < (uint32_t)p.n_pages;
+}
+
+/* Which of N consecutive pages are free, bit i for page first + i; pages past
+ * the last are neither free nor used. */
+template <int N>
+__device__ __forceinline__ uint32_t free_of(const coli_kv_pages& p, int first, uint32_t& there)
+{
+    uint32_t f = 0;
+    there = 0;
+    int r[N];
+#pragma unroll
+    for (int i = 0; i < N; i += 4)
+        if (first + i + 4 <= p.n_pages) { /* whatever the alignment */
+            __builtin_memcpy(r + i, p.refs + first + i, 16);
+        } else {
+            for (int j = 0; j < 4; ++j)
+                r[i + j] = first + i + j < p.n_pages ? p.refs[first + i + j] : 0;
+        }
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        const bool in = first + i < p.n_pages;
+        there |= in ? 1u << i : 0;
+        f |= in && r[i] <= 0 ? 1u << i : 0;
+    }
+    return f;
+}
+
+/* Sum over the values of the threads before this one, and over all. */
+template <int T>
+__device__ __forceinline__ int scan(int v, int* waves, int& total)
+{
+    const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
+    int x = v;
+#pragma unroll
+    for (int m = 1; m < 64; m *= 2) {
+        const int y = __shfl_up(x, m, 64);
+        x += lane >= m ? y : 0;
+    }
+    __syncthreads(); /* the scan before has been read */
+    if (lane == 63)
+        waves[wv] = x;
+    __syncthreads();
+    int before = 0;
+    total = 0;
+#pragma unroll
+    for (int i = 0; i < T / 64; ++i) {
+        before += i < wv ? waves[i] : 0;
+        total += waves[i];
+    }
+    return before + x - v;
+}
+
+template <typename T>
+__device__ __forceinline__ T sum_all(T v, T* waves)
+{
+    for (int m = 32; m >= 1; m >>= 1)
+        v += __shfl_xor(v, m, 64);
+    __syncthreads();
+    if ((threadIdx.x & 63) == 0)
+        waves[threadIdx.x >> 6] = v;
+    __syncthreads();
+    v = 0;
+    for (int i = 0; i < (int)(blockDim.x / 64); ++i)
+        v += waves[i];
+    return v;
+}
+
+/* ---- extend --------------------------------------------------------------- */
+
+/* What sequence s wants. */
+struct Want {
+    int len, add, have, want; /* tokens; blocks before and after */
+    int last, old;            /* a partly filled last block whose page is shared, and that page; or -1 */
+    int need;                 /* pages, at most one more than there are; -1: it would outgrow its table */
+};
+
+__device__ __forceinline__ Want want_of(const coli_kv_pages& p, const int32_t* add, int s)
+{
+    Want w;
+    w.len = len_of(p, s);
+    w.add = add[s];
+    w.last = w.old = -1;
+    w.have = w.want = blocks_of(w.len);
+    w.need = 0;
+    if (w.add <= 0)
+        return w;
+    const int64_t len = (int64_t)w.len + w.add;
+    if (len > (int64_t)p.max_pages * COLI_KV_BLOCK || len > 0x7FFFFFFF) {
+        w.need = -1;
+        return w;
+    }
+    w.want = blocks_of(len);
+    if (w.len % COLI_KV_BLOCK) {
+        const int last = w.len / COLI_KV_BLOCK, old = p.page_table[(int64_t)s * p.max_pages + last];
+        if (is_page(p, old) && p.refs[old] > 1) {
+            w.last = last;
+            w.old = old;
+        }
+    }
+    w.need = (int)min((int64_t)w.want - w.have + (w.last >= 0), (int64_t)p.n_pages + 1);
+    return w;
+}
+
+/* Gives sequence s its pages, the list's entries from `at` on (at + need of them
+ * are there); LANES threads, this one `lane`, share the work. */
+template <int LANES>
+__device__ __forceinline__ void give(const coli_kv_pages& p, const Want& w, int s, int64_t at, const int32_t* list,
+                                     int lane, int32_t* granted, int32_t* src, int32_t* dst)
+{
+    int32_t* row = p.page_table + (int64_t)s * p.max_pages;
+    const int shared = w.last >= 0;
+    for (int b = w.have + lane; b < w.want; b += LANES) {
+        const int page = list[at + shared + b - w.have];
+        row[b] = page;
+        p.refs[page] = 1;
+    }
+    if (lane == 0) {
+        int from = -1, to = -1;
+        if (shared) {
+            from = w.old;
+            to = list[at];
+            row[w.last] = to;
+            p.refs[to] = 1;
+            atomicAdd(p.refs + from, -1);
+        }
+        src[s] = from;
+        dst[s] = to;
+        granted[s] = max(w.add, 0);
+        if (w.add > 0)
+            p.kv_len[s] = w.len + w.add;
+    }
+}
+
+__device__ __forceinline__ void refuse(int s, int32_t* granted, int32_t* src, int32_t* dst)
+{
+    granted[s] = 0;
+    src[s] = dst[s] = -1;
+}
+
+/* Pools and batches of up to 2^15 pages and 2^10 sequences in one launch: a thread
+ * holds 32 pages and one sequence. */
+constexpr int kOneThreads = 1024, kOnePages = 32;
+
+__global__ __launch_bounds__(kOneThreads) void extend_one(coli_kv_pages p, const int32_t* add, int32_t* granted,
+                                                          int32_t* src, int32_t* dst, int32_t* list)
+{
+    __shared__ int waves[kOneThreads / 64];
+    __shared__ Want wants[kOneThreads];
+    __shared__ int befores[kOneThreads];
+    const int t = threadIdx.x;
+    uint32_t there;
+    uint32_t f = free_of<kOnePages>(p, t * kOnePages, there);
+    Want w = {};
+    if (t < p.n_seq)
+        w = want_of(p, add, t);
+    int needed, n_free;
+    const int before = scan<kOneThreads>(max(w.need, 0), waves, needed);
+    int rank = scan<kOneThreads>(__popc(f), waves, n_free);
+    for (; f && rank < needed; f &= f - 1)
+        list[rank++] = t * kOnePages + __ffs(f) - 1;
+    wants[t] = w;
+    befores[t] = before;
+    __syncthreads();
+    for (int s = t / 64; s < p.n_seq; s += kOneThreads / 64) {
+        const Want v = wants[s];
+        if (v.need >= 0 && (v.need == 0 || befores[s] + v.need <= n_free))
+            give<64>(p, v, s, befores[s], list, t & 63, granted, src, dst);
+        else if ((t & 63) == 0)
+            refuse(s, granted, src, dst);
+    }
+}
+
+/* Any number: needs and counts, then the list of free pages, then the sequences. */
+struct PagesWs {
+    int32_t* list;  /* [n_pages]; compact: the place of each moved page among them */
+    int32_t* need;  /* [n_seq] */
+    int32_t* count; /* [slices]: extend: free pages, compact: used ones */
+    int slices;
+};
+
+__global__ __launch_bounds__(kThreads) void extend_count(coli_kv_pages p, const int32_t* add, PagesWs ws)
+{
+    __shared__ int waves[kThreads / 64];
+    const int s = blockIdx.x * kThreads + threadIdx.x;
+    if (s < p.n_seq)
+        ws.need[s] = want_of(p, add, s).need;
+    if ((int)blockIdx.x < ws.slices) {
+        uint32_t there;
+        const int n = sum_all<int>(__popc(free_of<kOwn>(p, blockIdx.x * kSlice + threadIdx.x * kOwn, there)), waves);
+        if (threadIdx.x == 0)
+            ws.count[blockIdx.x] = n;
+    }
+}
+
+/* Sum of v[0 .. n-1], negative numbers as 0. */
+__device__ __forceinline__ int64_t sum_of(const int32_t* v, int n, int64_t* waves)
+{
+    int64_t x = 0;
+    for (int i = threadIdx.x; i < n; i += kThreads)
+        x += max(v[i], 0);
+    return sum_all(x, waves);
+}
+
+__global__ __launch_bounds__(kThreads) void extend_list(coli_kv_pages p, PagesWs ws)
+{
+    __shared__ int waves[kThreads / 64];
+    __shared__ int64_t waves64[kThreads / 64];
+    const int base = (int)sum_of(ws.count, blockIdx.x, waves64);
+    const int first = blockIdx.x * kSlice + threadIdx.x * kOwn;
+    uint32_t there;
+    int total;
+    uint32_t f = free_of<kOwn>(p, first, there);
+    int rank = base + scan<kThreads>(__popc(f), waves, total);
+    for (; f; f &= f - 1)
+        ws.list[rank++] = first + __ffs(f) - 1;
+}
+
+__global__ __launch_bounds__(kThreads) void extend_give(coli_kv_pages p, const int32_t* add, int32_t* granted,
+                                                        int32_t* src, int32_t* dst, PagesWs ws)
+{
+    __shared__ int64_t waves[kThreads / 64];
+    __shared__ Want want;
+    const int s = blockIdx.x;
+    const int64_t before = sum_of(ws.need, s, waves), n_free = sum_of(ws.count, ws.slices, waves);
+    if (threadIdx.x == 0) {
+        /* refs of shared pages are going down in other workgroups: what the first
+         * launch saw of them is in its need */
+        Want w = want_of(p, add, s);
+        w.need = ws.need[s];
+        if (w.need > 0) {
+            const bool shared = w.need > w.want - w.have && w.need <= p.n_pages;
+            w.last = shared ? w.len / COLI_KV_BLOCK : -1;
+            w.old = shared ? p.page_table[(int64_t)s * p.max_pages + w.last] : -1;
+        } else {
+            w.last = w.old = -1;
+        }
+        want = w;
+    }
+    __syncthreads();
+    const Want w = want;
+    if (w.need >= 0 && (w.need == 0 || before + w.need <= n_free))
+        give<kThreads>(p, w, s, before, ws.list, threadIdx.x, granted, src, dst);
+    else if (threadIdx.x == 0)
+        refuse(s, granted, src, dst);
+}
+
+/* ---- trim, fork ----------------------------------------------------------- */
+
+__global__ __launch_bounds__(kThreads) void trim_kernel(coli_kv_pages p, const int32_t* new_len)
+{
+    const int s = blockIdx.x, len = len_of(p, s), to = new_len[s];
+    if (to < 0 || to >= len)
+        return;
+    __syncthreads(); /* every thread has read the length */
+    int32_t* row = p.page_table + (int64_t)s * p.max_pages;
+    for (int b = blocks_of(to) + threadIdx.x; b < blocks_of(len); b += kThreads) {
+        const int page = row[b];
+        if (is_page(p, page))
+            atomicAdd(p.refs + page, -1);
+        row[b] = -1;
+    }
+    if (threadIdx.x == 0)
+        p.kv_len[s] = to;
+}
+
+__global__ __launch_bounds__(kThreads) void fork_kernel(coli_kv_pages p, const int32_t* parent, const int32_t* child,
+                                                        int n)
+{
+    const int i = blockIdx.x, a = parent[i], c = child[i];
+    bool skip = (uint32_t)a >= (uint32_t)p.n_seq || (uint32_t)c >= (uint32_t)p.n_seq;
+    for (int j = threadIdx.x; j < n; j += kThreads) {
+        const int x = child[j];
+        skip |= x == a || (j < i && x == c);
+    }
+    if (__syncthreads_or(skip))
+        return;
+    /* only this workgroup writes the child's state, and none the parent's */
+    const bool empty = p.kv_len[c] <= 0;
+    const int len = len_of(p, a), blocks = blocks_of(len);
+    __syncthreads();
+    if (!empty)
+        return;
+    const int32_t* from = p.page_table + (int64_t)a * p.max_pages;
+    int32_t* to = p.page_table + (int64_t)c * p.max_pages;
+    for (int b = threadIdx.x; b < blocks; b += kThreads) {
+        const int page = from[b];
+        to[b] = page;
+        if (is_page(p, page))
+            atomicAdd(p.refs + page, 1);
+    }
+    if (threadIdx.x == 0)
+        p.kv_len[c] = len;
+}
+
+/* ---- compact -------------------------------------------------------------- */
+
+__global__ __launch_bounds__(kThreads) void compact_count(coli_kv_pages p, PagesWs ws)
+{
+    __shared__ int waves[kThreads / 64];
+    uint32_t there;
+    const uint32_t f = free_of<kOwn>(p, blockIdx.x * kSlice + threadIdx.x * kOwn, there);
+    const int n = sum_all<int>(__popc(there & ~f), waves);
+    if (threadIdx.x == 0)
+        ws.count[blockIdx.x] = n;
+}
+
+/* With n_live used pages, `low` of them below n_live, there are n_live - low moves;
+ * a used page of rank r among the used ones moves as number r - low, a free page q
+ * below n_live is place q - (its rank among the used ones). */
+__global__ __launch_bounds__(kThreads) void compact_list(coli_kv_pages p, int32_t* src, int32_t* dst, int32_t* n_live,
+                                                         PagesWs ws)
+{
+    __shared__ int waves[kThreads / 64];
+    __shared__ int64_t waves64[kThreads / 64];
+    const int live = (int)sum_of(ws.count, ws.slices, waves64), edge = live / kSlice; /* the slice that n_live lies in */
+    uint32_t there;
+    uint32_t f = free_of<kOwn>(p, edge * kSlice + threadIdx.x * kOwn, there);
+    const int inside = min(max(live - (edge * kSlice + (int)threadIdx.x * kOwn), 0), kOwn);
+    const int low =
+        (int)sum_of(ws.count, edge, waves64) + sum_all<int>(__popc(there & ~f & ((1u << inside) - 1)), waves);
+    const int first = blockIdx.x * kSlice + threadIdx.x * kOwn;
+    f = free_of<kOwn>(p, first, there);
+    int total;
+    const int base = (int)sum_of(ws.count, blockIdx.x, waves64);
+    int rank = base + scan<kThreads>(__popc(there & ~f), waves, total);
+    for (int i = 0; i < kOwn && first + i < p.n_pages; ++i) {
+        const int page = first + i;
+        const bool used = !(f >> i & 1), moves = used && page >= live;
+        ws.list[page] = moves ? rank - low : -1;
+        if (moves)
+            src[rank - low] = page;
+        else if (!used && page < live)
+            dst[page - rank] = page;
+        rank += used;
+    }
+    const int moves = live - low, half = p.n_pages / 2;
+    for (int i = 0; i < kOwn / 2; ++i) {
+        const int j = blockIdx.x * (kSlice / 2) + threadIdx.x * (kOwn / 2) + i;
+        if (j >= moves && j < half)
+            src[j] = dst[j] = -1;
+    }
+    if (first == 0)
+        *n_live = live;
+}
+
+/* The moves' refs and every sequence's table: workgroups from n_seq on take the
+ * former. */
+__global__ __launch_bounds__(kThreads) void compact_apply(coli_kv_pages p, const int32_t* src, const int32_t* dst,
+                                                          PagesWs ws)
+{
+    if ((int)blockIdx.x >= p.n_seq) {
+        const int j0 = ((int)blockIdx.x - p.n_seq) * (kSlice / 2);
+        for (int j = j0 + threadIdx.x; j < min(j0 + kSlice / 2, p.n_pages / 2); j += kThreads)
+            if (src[j] >= 0) {
+                p.refs[dst[j]] = p.refs[src[j]];
+                p.refs[src[j]] = 0;
+            }
+        return;
+    }
+    int32_t* row = p.page_table + (int64_t)blockIdx.x * p.max_pages;
+    const int blocks = blocks_of(len_of(p, blockIdx.x));
+    for (int b = threadIdx.x; b < blocks; b += kThreads) {
+        const int page = row[b];
+        const int j = is_page(p, page) ? ws.list[page] : -1;
+        if (j >= 0)
+            row[b] = dst[j];
+    }
+}
+
+/* ---- copy ----------------------------------------------------------------- */
+
+constexpr int kCopyUnits = 4; /* 16-byte pieces of a thread and turn */
+
+/* blockIdx.x: keys or values and the chunk of a page, blockIdx.y: the pair. */
+__global__ __launch_bounds__(kThreads) void copy_kernel(coli_kv_cache from, coli_kv_cache to, const int32_t* src,
+                                                        const int32_t* dst, int n, int chunks)
+{
+    const bool key = (int)blockIdx.x < chunks;
+    const int chunk = blockIdx.x - (key ? 0 : chunks), H = from.n_heads;
+    const int units = H * (COLI_KV_BLOCK * from.head_dim / 16); /* up to 2^20 */
+    for (int64_t i = blockIdx.y; i < n; i += gridDim.y) {
+        const int a = src[i], b = dst[i];
+        if ((uint32_t)a >= (uint32_t)from.n_pages || (uint32_t)b >= (uint32_t)to.n_pages)
+            continue;
+        const uint4* x = (const uint4*)(key ? from.k : from.v) + (int64_t)a * units;
+        uint4* y = (uint4*)(key ? to.k : to.v) + (int64_t)b * units;
+        const int u0 = chunk * (kThreads * kCopyUnits) + threadIdx.x;
+        uint4 r[kCopyUnits];
+#pragma unroll
+        for (int j = 0; j < kCopyUnits; ++j)
+            r[j] = x[min(u0 + j * kThreads, units - 1)];
+#pragma unroll
+        for (int j = 0; j < kCopyUnits; ++j)
+            if (u0 + j * kThreads < units)
+                y[u0 + j * kThreads] = r[j];
+        if (chunk == 0) {
+            const float* xs = (key ? from.k_scale : from.v_scale) + (int64_t)a * H;
+            float* ys = (key ? to.k_scale : to.v_scale) + (int64_t)b * H;
+            for (int h = threadIdx.x; h < H; h += kThreads)
+                ys[h] = xs[h];
+        }
+    }
+}
+
+int slices_of(int32_t n_pages)
+{
+    return (int)(((int64_t)n_pages + kSlice - 1) / kSlice);
+}
+
+PagesWs lay_out(const coli_kv_pages& p, void* ws)
+{
+    PagesWs w;
+    w.slices = slices_of(p.n_pages);
+    w.list = (int32_t*)ws;
+    w.need = w.list + p.n_pages;
+    w.count = w.need + p.n_seq;
+    return w;
+}
+
+} // namespace
+
+size_t kv_pages_workspace_bytes(int32_t n_pages, int32_t n_seq)
+{
+    const size_t n = ((size_t)n_pages + n_seq + slices_of(n_pages)) * 4;
+    return (n + 255) / 256 * 256;
+}
+
+hipError_t launch_kv_extend(const coli_kv_pages& p, const int32_t* add, int32_t* granted, int32_t* src, int32_t* dst,
+                            void* ws, hipStream_t s)
+{
+    const PagesWs w = lay_out(p, ws);
+    if (p.n_seq <= kOneThreads && p.n_pages <= kOneThreads * kOnePages) {
+        hipLaunchKernelGGL(extend_one, dim3(1), dim3(kOneThreads), 0, s, p, add, granted, src, dst, w.list);
+        return hipGetLastError();
+    }
+    const int grid = std::max(w.slices, (p.n_seq + kThreads - 1) / kThreads);
+    hipLaunchKernelGGL(extend_count, dim3(grid), dim3(kThreads), 0, s, p, add, w);
+    hipLaunchKernelGGL(extend_list, dim3(w.slices), dim3(kThreads), 0, s, p, w);
+    hipLaunchKernelGGL(extend_give, dim3(p.n_seq), dim3(kThreads), 0, s, p, add, granted, src, dst, w);
+    return hipGetLastError();
+}
+
+hipError_t launch_kv_trim(const coli_kv_pages& p, const int32_t* new_len, hipStream_t s)
+{
+    hipLaunchKernelGGL(trim_kernel, dim3(p.n_seq), dim3(kThreads), 0, s, p, new_len);
+    return hipGetLastError();
+}
+
+hipError_t launch_kv_fork(const coli_kv_pages& p, const int32_t* parent, const int32_t* child, int32_t n,
+                          hipStream_t s)
+{
+    hipLaunchKernelGGL(fork_kernel, dim3(n), dim3(kThreads), 0, s, p, parent, child, n);
+    return hipGetLastError();
+}
+
+hipError_t launch_kv_compact(const coli_kv_pages& p, int32_t* src, int32_t* dst, int32_t* n_live, void* ws,
+                             hipStream_t s)
+{
+    const PagesWs w = lay_out(p, ws);
+    hipLaunchKernelGGL(compact_count, dim3(w.slices), dim3(kThreads), 0, s, p, w);
+    hipLaunchKernelGGL(compact_list, dim3(w.slices), dim3(kThreads), 0, s, p, src, dst, n_live, w);
+    hipLaunchKernelGGL(compact_apply, dim3(p.n_seq + w.slices), dim3(kThreads), 0, s, p, src, dst, w);
+    return hipGetLastError();
+}
+
+hipError_t launch_kv_copy(const coli_kv_cache& from, const coli_kv_cache& to, const int32_t* src, const int32_t* dst,
+                          int32_t n, hipStream_t s)
+{
+    const int units = from.n_heads * (COLI_KV_BLOCK * from.head_dim / 16);
+    const int chunks = (units + kThreads * kCopyUnits - 1) / (kThreads * kCopyUnits);
+    hipLaunchKernelGGL(copy_kernel, dim3(2 * chunks, std::min(n, 65535)), dim3(kThreads), 0, s, from, to, src, dst, n,
+                       chunks);
+    return hipGetLastError();
+}
+
+} // namespace coli

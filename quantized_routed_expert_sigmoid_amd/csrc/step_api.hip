@@ -1,0 +1,182 @@
+/*
+ * step_api.hip -- the C ABI of the operators of a serving step (declared in
+ * include/colibri_step.h): argument validation on the host, then one launcher.
+ * Nothing here synchronises or allocates.
+ */
+#include "layer.h"
+#include "step.h"
+
+#include <math.h>
+
+using namespace coli;
+
+namespace {
+
+bool is_type(int32_t t)
+{
+    return t == COLI_F32 || t == COLI_BF16;
+}
+
+/* A bank of one matrix, of the sizes that the operators around the layer take. */
+int check_matrix(const coli_qbank* W)
+{
+    if (!W || !W->data || !W->row_scale || W->n_mat != 1 || W->rows < 1 || W->K < 32 || W->K % 32)
+        return COLI_E_INVAL;
+    if (W->rows > COLI_MAX_LINEAR_ROWS || W->K > COLI_MAX_LINEAR_K)
+        return COLI_E_UNSUPPORTED;
+    return check_bank(W, 1, W->rows, W->K);
+}
+
+int check_pages_sizes(const coli_kv_pages* p)
+{
+    if (!p || p->n_pages < 1 || p->n_seq < 0 || p->max_pages < 0)
+        return COLI_E_INVAL;
+    if (p->n_pages > COLI_MAX_PAGES || p->n_seq > COLI_MAX_SEQS || p->max_pages > COLI_MAX_SEQ_PAGES)
+        return COLI_E_UNSUPPORTED;
+    return COLI_OK;
+}
+
+int check_pages(const coli_kv_pages* p)
+{
+    const int st = check_pages_sizes(p);
+    if (st)
+        return st;
+    if (!p->refs || (p->n_seq > 0 && !p->kv_len) || (p->n_seq > 0 && p->max_pages > 0 && !p->page_table))
+        return COLI_E_INVAL;
+    if (!aligned(p->refs, 4) || !aligned(p->kv_len, 4) || !aligned(p->page_table, 4))
+        return COLI_E_UNSUPPORTED;
+    return COLI_OK;
+}
+
+int check_pages_ws(const coli_kv_pages* p, const void* ws, size_t ws_bytes)
+{
+    if (!ws)
+        return COLI_E_INVAL;
+    if (!aligned(ws, kAlign))
+        return COLI_E_UNSUPPORTED;
+    return ws_bytes < kv_pages_workspace_bytes(p->n_pages, p->n_seq) ? COLI_E_WORKSPACE : COLI_OK;
+}
+
+int check_copy_cache(const coli_kv_cache* c)
+{
+    if (!c || !c->k || !c->v || !c->k_scale || !c->v_scale || c->n_pages < 1 || c->n_heads < 1)
+        return COLI_E_INVAL;
+    if (c->head_dim != 64 && c->head_dim != 128 && c->head_dim != 192 && c->head_dim != 256)
+        return COLI_E_UNSUPPORTED;
+    if (c->n_heads > COLI_MAX_KV_HEADS || !aligned(c->k, 16) || !aligned(c->v, 16) || !aligned(c->k_scale, 4) ||
+        !aligned(c->v_scale, 4))
+        return COLI_E_UNSUPPORTED;
+    return COLI_OK;
+}
+
+} // namespace
+
+extern "C" {
+
+int colibri_embed_q(const coli_qbank* W, const void* ids, int32_t id_type, int32_t n, float scale, void* out,
+                    int32_t out_type, coli_stream_t stream)
+{
+    const int st = check_matrix(W);
+    if (st)
+        return st;
+    if (n < 0 || !isfinite(scale))
+        return COLI_E_INVAL;
+    if (n > COLI_MAX_TOKENS || !is_type(out_type) || (id_type != COLI_I32 && id_type != COLI_I64))
+        return COLI_E_UNSUPPORTED;
+    if (n == 0)
+        return COLI_OK;
+    if (!ids || !out)
+        return COLI_E_INVAL;
+    if (!aligned(ids, (size_t)id_type) || !aligned(out, 16))
+        return COLI_E_UNSUPPORTED;
+    return hip_status(launch_embed_q(*W, ids, id_type, n, scale, out, out_type, (hipStream_t)stream));
+}
+
+size_t colibri_kv_pages_workspace_bytes(const coli_kv_pages* pages)
+{
+    return check_pages_sizes(pages) ? 0 : kv_pages_workspace_bytes(pages->n_pages, pages->n_seq);
+}
+
+int colibri_kv_extend(const coli_kv_pages* pages, const int32_t* add, int32_t* granted, int32_t* src, int32_t* dst,
+                      void* ws, size_t ws_bytes, coli_stream_t stream)
+{
+    int st = check_pages(pages);
+    if (st)
+        return st;
+    if (pages->n_seq == 0)
+        return COLI_OK;
+    if (!add || !granted || !src || !dst)
+        return COLI_E_INVAL;
+    if (!aligned(add, 4) || !aligned(granted, 4) || !aligned(src, 4) || !aligned(dst, 4))
+        return COLI_E_UNSUPPORTED;
+    if ((st = check_pages_ws(pages, ws, ws_bytes)))
+        return st;
+    return hip_status(launch_kv_extend(*pages, add, granted, src, dst, ws, (hipStream_t)stream));
+}
+
+int colibri_kv_trim(const coli_kv_pages* pages, const int32_t* new_len, coli_stream_t stream)
+{
+    const int st = check_pages(pages);
+    if (st)
+        return st;
+    if (pages->n_seq == 0)
+        return COLI_OK;
+    if (!new_len)
+        return COLI_E_INVAL;
+    if (!aligned(new_len, 4))
+        return COLI_E_UNSUPPORTED;
+    return hip_status(launch_kv_trim(*pages, new_len, (hipStream_t)stream));
+}
+
+int colibri_kv_fork(const coli_kv_pages* pages, const int32_t* parent, const int32_t* child, int32_t n,
+                    coli_stream_t stream)
+{
+    const int st = check_pages(pages);
+    if (st)
+        return st;
+    if (n < 0)
+        return COLI_E_INVAL;
+    if (n > COLI_MAX_SEQS)
+        return COLI_E_UNSUPPORTED;
+    if (n == 0 || pages->n_seq == 0)
+        return COLI_OK;
+    if (!parent || !child)
+        return COLI_E_INVAL;
+    if (!aligned(parent, 4) || !aligned(child, 4))
+        return COLI_E_UNSUPPORTED;
+    return hip_status(launch_kv_fork(*pages, parent, child, n, (hipStream_t)stream));
+}
+
+int colibri_kv_compact(const coli_kv_pages* pages, int32_t* src, int32_t* dst, int32_t* n_live, void* ws,
+                       size_t ws_bytes, coli_stream_t stream)
+{
+    int st = check_pages(pages);
+    if (st)
+        return st;
+    if (!n_live || (pages->n_pages > 1 && (!src || !dst))) /* one page never moves */
+        return COLI_E_INVAL;
+    if (!aligned(src, 4) || !aligned(dst, 4) || !aligned(n_live, 4))
+        return COLI_E_UNSUPPORTED;
+    if ((st = check_pages_ws(pages, ws, ws_bytes)))
+        return st;
+    return hip_status(launch_kv_compact(*pages, src, dst, n_live, ws, (hipStream_t)stream));
+}
+
+int colibri_kv_copy(const coli_kv_cache* from, const coli_kv_cache* to, const int32_t* src, const int32_t* dst,
+                    int32_t n, coli_stream_t stream)
+{
+    int st = check_copy_cache(from);
+    if (st || (st = check_copy_cache(to)))
+        return st;
+    if (n < 0 || from->n_heads != to->n_heads || from->head_dim != to->head_dim)
+        return COLI_E_INVAL;
+    if (n == 0)
+        return COLI_OK;
+    if (!src || !dst)
+        return COLI_E_INVAL;
+    if (!aligned(src, 4) || !aligned(dst, 4))
+        return COLI_E_UNSUPPORTED;
+    return hip_status(launch_kv_copy(*from, *to, src, dst, n, (hipStream_t)stream));
+}
+
+} // extern "C"

@@ -1,0 +1,138 @@
+"""What the operators of a serving step refuse, on the host: the C ABI returns an
+error before anything is enqueued (no GPU is needed), and the binding raises on
+tensors that do not fit."""
+
+import ctypes
+
+import pytest
+import torch
+
+import quantized_routed_expert_sigmoid_amd as qre
+from quantized_routed_expert_sigmoid_amd import block, step
+
+P = 1 << 20  # a well aligned address that no call here may touch
+OK, INVAL, UNSUP, WS = 0, 1, 2, 3
+BIG = 1 << 50
+r = ctypes.byref
+
+
+@pytest.fixture(scope="module")
+def L():
+    block._f()
+    return step._g()
+
+
+def bank(**kw):
+    d = dict(data=P, row_scale=P, n_mat=1, rows=5, K=64, qtype=4, group=0)
+    d.update(kw)
+    return qre.QBankDesc(**d)
+
+
+BANK_BAD = [(dict(n_mat=2), INVAL), (dict(rows=0), INVAL), (dict(K=40), INVAL), (dict(K=0), INVAL), (dict(data=None), INVAL),
+            (dict(row_scale=None), INVAL), (dict(qtype=5), UNSUP), (dict(rows=(1 << 20) + 1), UNSUP),
+            (dict(K=(1 << 15) + 32), UNSUP), (dict(data=P + 4), UNSUP), (dict(row_scale=P + 2), UNSUP)]
+
+
+@pytest.mark.parametrize("kw,st", BANK_BAD + [(dict(group=48), INVAL), (dict(group=-32), INVAL), (dict(group=128), INVAL)])
+def test_embed_bank(L, kw, st):
+    assert L.colibri_embed_q(r(bank(**kw)), P, 4, 1, 1.0, P, 32, None) == st
+
+
+@pytest.mark.parametrize("args,st", [
+    ((None, 4, 1, 1.0, P, 32), INVAL), ((P, 4, 1, 1.0, None, 32), INVAL), ((P, 4, -1, 1.0, P, 32), INVAL),
+    ((P, 4, 1, float("nan"), P, 32), INVAL), ((P, 4, 1, float("inf"), P, 32), INVAL), ((P, 2, 1, 1.0, P, 32), UNSUP),
+    ((P, 4, 1, 1.0, P, 8), UNSUP), ((P, 4, 65537, 1.0, P, 32), UNSUP), ((P + 2, 4, 1, 1.0, P, 32), UNSUP),
+    ((P + 4, 8, 1, 1.0, P, 32), UNSUP), ((P, 4, 1, 1.0, P + 8, 16), UNSUP), ((None, 4, 0, 1.0, None, 32), OK)])
+def test_embed(L, args, st):
+    assert L.colibri_embed_q(r(bank()), *args, None) == st
+    assert L.colibri_embed_q(None, P, 4, 1, 1.0, P, 32, None) == INVAL
+
+
+def pages(**kw):
+    d = dict(refs=P, page_table=P, kv_len=P, n_pages=9, n_seq=3, max_pages=4)
+    d.update(kw)
+    return step.KVPagesDesc(**d)
+
+
+def five(L, p):
+    return (L.colibri_kv_extend(r(p), P, P, P, P, P, BIG, None), L.colibri_kv_trim(r(p), P, None),
+            L.colibri_kv_fork(r(p), P, P, 2, None), L.colibri_kv_compact(r(p), P, P, P, P, BIG, None))
+
+
+@pytest.mark.parametrize("kw,st", [
+    (dict(n_pages=0), INVAL), (dict(n_seq=-1), INVAL), (dict(max_pages=-1), INVAL), (dict(n_pages=(1 << 26) + 1), UNSUP),
+    (dict(n_seq=65536), UNSUP), (dict(max_pages=(1 << 24) + 1), UNSUP), (dict(refs=None), INVAL), (dict(kv_len=None), INVAL),
+    (dict(page_table=None), INVAL), (dict(refs=P + 2), UNSUP), (dict(kv_len=P + 1), UNSUP), (dict(page_table=P + 3), UNSUP)])
+def test_pages(L, kw, st):
+    assert five(L, pages(**kw)) == (st,) * 4
+
+
+def test_pages_null_and_empty(L):
+    assert L.colibri_kv_trim(None, P, None) == INVAL and L.colibri_kv_pages_workspace_bytes(None) == 0
+    assert five(L, pages(n_seq=0, page_table=None, kv_len=None))[:3] == (OK,) * 3
+    assert L.colibri_kv_fork(r(pages()), None, None, 0, None) == OK
+    assert L.colibri_kv_pages_workspace_bytes(r(pages(n_pages=0))) == 0
+    assert L.colibri_kv_pages_workspace_bytes(r(pages(refs=None))) >= 4 * (9 + 3)
+
+
+@pytest.mark.parametrize("i", range(4))
+def test_extend(L, i):
+    def call(a, ws=P, n=BIG):
+        return L.colibri_kv_extend(r(pages()), *a, ws, n, None)
+    assert call([None if j == i else P for j in range(4)]) == INVAL
+    assert call([P + 2 if j == i else P for j in range(4)]) == UNSUP
+    assert call([P] * 4, None) == INVAL and call([P] * 4, P + 64) == UNSUP and call([P] * 4, P, 0) == WS
+
+
+def test_trim_fork_compact(L):
+    p = pages()
+    assert L.colibri_kv_trim(r(p), None, None) == INVAL and L.colibri_kv_trim(r(p), P + 1, None) == UNSUP
+    for a, st in [((None, P, 1), INVAL), ((P, None, 1), INVAL), ((P, P, -1), INVAL), ((P, P, 65536), UNSUP),
+                  ((P + 2, P, 1), UNSUP), ((P, P + 2, 1), UNSUP)]:
+        assert L.colibri_kv_fork(r(p), *a, None) == st
+    for a, st in [((None, P, P, P, BIG), INVAL), ((P, None, P, P, BIG), INVAL), ((P, P, None, P, BIG), INVAL),
+                  ((P, P, P, None, BIG), INVAL), ((P, P, P, P + 16, BIG), UNSUP), ((P, P, P, P, 16), WS),
+                  ((P + 2, P, P, P, BIG), UNSUP), ((P, P, P + 2, P, BIG), UNSUP)]:
+        assert L.colibri_kv_compact(r(p), *a, None) == st
+
+
+def cache(**kw):
+    d = dict(k=P, v=P, k_scale=P, v_scale=P, n_pages=4, n_heads=2, head_dim=64)
+    d.update(kw)
+    return block.KVCacheDesc(**d)
+
+
+@pytest.mark.parametrize("kw,st", [
+    (dict(k=None), INVAL), (dict(v=None), INVAL), (dict(k_scale=None), INVAL), (dict(v_scale=None), INVAL),
+    (dict(n_pages=0), INVAL), (dict(n_heads=0), INVAL), (dict(head_dim=96), UNSUP), (dict(n_heads=1025), UNSUP),
+    (dict(k=P + 8), UNSUP), (dict(v_scale=P + 1), UNSUP), (dict(n_heads=3), INVAL), (dict(head_dim=128), INVAL)])
+def test_copy_caches(L, kw, st):
+    assert L.colibri_kv_copy(r(cache(**kw)), r(cache()), P, P, 1, None) == st
+    assert L.colibri_kv_copy(r(cache()), r(cache(**kw)), P, P, 1, None) == st
+
+
+def test_copy(L):
+    def call(*a):
+        return L.colibri_kv_copy(r(cache()), r(cache()), *a, None)
+    assert call(None, P, 1) == INVAL and call(P, None, 1) == INVAL and call(P, P, -1) == INVAL
+    assert call(P + 2, P, 1) == UNSUP and call(P, P + 2, 1) == UNSUP and call(None, None, 0) == OK
+    assert L.colibri_kv_copy(None, r(cache()), P, P, 1, None) == INVAL
+
+
+def test_binding_refuses():
+    with pytest.raises(ValueError, match="device tensor"):
+        qre.embed_q(None, torch.zeros(2, dtype=torch.int32))
+    with pytest.raises(ValueError, match="device tensor"):
+        qre.KVPages.empty(2, 3, 4, device="cpu")
+
+
+def test_library_exports_every_declared_symbol(L):
+    import os
+    import re
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    with open(os.path.join(root, "include", "colibri_step.h")) as f:
+        text = re.sub(r"/\*.*?\*/", "", f.read(), flags=re.S)
+    names = set(re.findall(r"\b(colibri_\w+)\s*\(", text))
+    assert names
+    for name in names:
+        assert hasattr(L, name), name
