@@ -112,6 +112,59 @@ int colibri_kv_compact(const coli_kv_pages* pages, int32_t* src, int32_t* dst, i
 int colibri_kv_copy(const coli_kv_cache* from, const coli_kv_cache* to, const int32_t* src, const int32_t* dst,
                     int32_t n, coli_stream_t stream);
 
+/*
+ * What a step does to its logits before a token is chosen, and the choice of the
+ * best one.  For each row, in fp32 and in this order, v = logits[t] and
+ *   1. t among the row's tokens:            v = v > 0 ? v / repetition : v * repetition
+ *   2. t among them count > 0 times since the first generated one:
+ *                                           v = v - (frequency * count + presence)
+ *   3. t among the row's biases:            v = v + (their sum, in the list's order)
+ *   4. t not allowed by the row's mask:     v = -inf
+ * Outputs, each of which may be null, but not all: out = v rounded to type;
+ * token = the lowest t of the largest v before that rounding, -1 where every v is
+ * -inf; lse = log sum_t exp(v), -inf there (softmax statistics in fp32).  A row with
+ * NaN gets its first NaN's t, and NaN.
+ *
+ * Steps 1 and 2 where penalties is not null, fp32 [rows][3] of repetition (not 0),
+ * frequency and presence: the row's tokens are tokens[spans[r][0] .. spans[r][2]-1], the
+ * generated ones those from spans[r][1] on (spans int32 [rows][3], tokens int32
+ * [n_tokens]; rows may share tokens, as the drafts of one sequence do).  Step 3 where
+ * cu_bias is not null: entries cu_bias[r] .. cu_bias[r+1]-1 of bias_ids int32 and
+ * bias fp32 [n_bias].  Step 4 where mask is not null: bit t % 32 of word
+ * mask[mask_of[r]][t / 32] is set where t is allowed; mask uint32 [n_masks] rows
+ * mask_stride words apart, mask_of int32 [rows]; a mask_of outside [0, n_masks)
+ * allows all.  Tokens and ids outside [0, vocab) count for nothing; spans and
+ * cu_bias are taken inside their lists.
+ *
+ * logits and out: type [rows][vocab], rows logits_stride and out_stride elements apart,
+ * at least vocab; out may be logits (same stride), no other overlap.  rows <=
+ * COLI_MAX_SEQS, 1 <= vocab <= COLI_MAX_VOCAB.  ws as sized by
+ * colibri_logits_workspace_bytes for these or more rows and vocab (0: invalid sizes),
+ * needed for token and lse.  rows == 0 is a no-op.
+ */
+#define COLI_MAX_VOCAB (1 << 20)
+
+typedef struct coli_logits {
+    const void* logits;
+    void* out;
+    int32_t* token;
+    float* lse;
+    const int32_t* tokens;
+    const int32_t* spans;
+    const float* penalties;
+    const float* bias;
+    const int32_t* bias_ids;
+    const int32_t* cu_bias;
+    const uint32_t* mask;
+    const int32_t* mask_of;
+    int64_t logits_stride, out_stride, mask_stride;
+    int32_t type, rows, vocab;
+    int32_t n_tokens, n_bias, n_masks;
+} coli_logits;
+
+size_t colibri_logits_workspace_bytes(int32_t rows, int32_t vocab);
+int colibri_adjust_logits(const coli_logits* a, void* ws, size_t ws_bytes, coli_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

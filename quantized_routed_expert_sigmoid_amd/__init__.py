@@ -507,5 +507,5 @@ def tier_verify_step(tiers: Sequence[TieredLayer], x: torch.Tensor, out: torch.T
 from .block import (KVCache, NormResult, add_rms_norm, kv_append, kv_attention, kv_attention_workspace,  # noqa: E402
                     kv_page_shape, kv_read, linear_q, linear_workspace)
 # The operators of a serving step (step.py).
-from .step import (KVExtend, KVMoves, KVPages, embed_q, kv_compact, kv_copy, kv_extend, kv_fork,  # noqa: E402
-                   kv_pages_workspace, kv_trim)
+from .step import (KVExtend, KVMoves, KVPages, LogitsResult, adjust_logits, embed_q, kv_compact, kv_copy,  # noqa: E402
+                   kv_extend, kv_fork, kv_pages_workspace, kv_trim, logits_workspace)

@@ -1,6 +1,7 @@
 /*
  * step.h -- internal launch interface of the operators of a serving step: the
- * embedding lookup (embed.hip) and the paged cache's sequences (kv_pages.hip).
+ * embedding lookup (embed.hip), the paged cache's sequences (kv_pages.hip) and what
+ * is done to logits (logits.hip).
  * step_api.hip validates; the launchers assume validated arguments.
  */
 #ifndef COLI_STEP_H
@@ -27,6 +28,9 @@ hipError_t launch_kv_compact(const coli_kv_pages& p, int32_t* src, int32_t* dst,
                              hipStream_t s);
 hipError_t launch_kv_copy(const coli_kv_cache& from, const coli_kv_cache& to, const int32_t* src, const int32_t* dst,
                           int32_t n, hipStream_t s);
+
+size_t logits_workspace_bytes(int32_t rows, int32_t vocab);
+hipError_t launch_adjust_logits(const coli_logits& a, void* ws, hipStream_t s);
 
 } // namespace coli
 

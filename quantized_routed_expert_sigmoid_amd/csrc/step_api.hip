@@ -179,4 +179,51 @@ int colibri_kv_copy(const coli_kv_cache* from, const coli_kv_cache* to, const in
     return hip_status(launch_kv_copy(*from, *to, src, dst, n, (hipStream_t)stream));
 }
 
+size_t colibri_logits_workspace_bytes(int32_t rows, int32_t vocab)
+{
+    if (rows < 0 || rows > COLI_MAX_SEQS || vocab < 1 || vocab > COLI_MAX_VOCAB)
+        return 0;
+    return logits_workspace_bytes(rows, vocab);
+}
+
+int colibri_adjust_logits(const coli_logits* a, void* ws, size_t ws_bytes, coli_stream_t stream)
+{
+    if (!a || a->rows < 0 || a->vocab < 1)
+        return COLI_E_INVAL;
+    if (a->rows > COLI_MAX_SEQS || a->vocab > COLI_MAX_VOCAB || !is_type(a->type))
+        return COLI_E_UNSUPPORTED;
+    if (a->n_tokens < 0 || a->n_bias < 0 || a->n_masks < 0)
+        return COLI_E_INVAL;
+    if (a->rows == 0)
+        return COLI_OK;
+    if (!a->logits || (!a->out && !a->token && !a->lse))
+        return COLI_E_INVAL;
+    if (a->penalties && (!a->spans || (a->n_tokens > 0 && !a->tokens)))
+        return COLI_E_INVAL;
+    if (a->cu_bias && a->n_bias > 0 && (!a->bias || !a->bias_ids))
+        return COLI_E_INVAL;
+    const int64_t words = ((int64_t)a->vocab + 31) / 32, far = (int64_t)1 << 40;
+    if (a->mask && (!a->mask_of || a->mask_stride < words))
+        return COLI_E_INVAL;
+    if (a->logits_stride < a->vocab || (a->out && a->out_stride < a->vocab) ||
+        (a->out == a->logits && a->out_stride != a->logits_stride))
+        return COLI_E_INVAL;
+    if (a->logits_stride > far || a->out_stride > far || a->mask_stride > far)
+        return COLI_E_UNSUPPORTED;
+    const size_t by = a->type == COLI_F32 ? 4 : 2;
+    if (!aligned(a->logits, by) || !aligned(a->out, by) || !aligned(a->token, 4) || !aligned(a->lse, 4) ||
+        !aligned(a->tokens, 4) || !aligned(a->spans, 4) || !aligned(a->penalties, 4) || !aligned(a->bias, 4) ||
+        !aligned(a->bias_ids, 4) || !aligned(a->cu_bias, 4) || !aligned(a->mask, 4) || !aligned(a->mask_of, 4))
+        return COLI_E_UNSUPPORTED;
+    if (a->token || a->lse) {
+        if (!ws)
+            return COLI_E_INVAL;
+        if (!aligned(ws, kAlign))
+            return COLI_E_UNSUPPORTED;
+        if (ws_bytes < logits_workspace_bytes(a->rows, a->vocab))
+            return COLI_E_WORKSPACE;
+    }
+    return hip_status(launch_adjust_logits(*a, ws, (hipStream_t)stream));
+}
+
 } // extern "C"

@@ -16,7 +16,7 @@ import torch
 
 import quantized_routed_expert_sigmoid_amd as _qre
 
-from .block import KVCache, _at, _call, _dev, _f32, _flat, _i32, _i64, _on, _room, _type, _vp
+from .block import KVCache, _at, _call, _dev, _f32, _flat, _i32, _i64, _length, _on, _room, _type, _vp
 
 _IDS = {torch.int32: 4, torch.int64: 8}
 
@@ -25,6 +25,14 @@ class KVPagesDesc(ctypes.Structure):
     """coli_kv_pages"""
     _fields_ = [("refs", _vp), ("page_table", _vp), ("kv_len", _vp), ("n_pages", _i32), ("n_seq", _i32),
                 ("max_pages", _i32)]
+
+
+class LogitsDesc(ctypes.Structure):
+    """coli_logits"""
+    _fields_ = ([(n, _vp) for n in ("logits", "out", "token", "lse", "tokens", "spans", "penalties", "bias", "bias_ids",
+                                    "cu_bias", "mask", "mask_of")]
+                + [(n, _i64) for n in ("logits_stride", "out_stride", "mask_stride")]
+                + [(n, _i32) for n in ("type", "rows", "vocab", "n_tokens", "n_bias", "n_masks")])
 
 
 _fns = None  # (the library,)
@@ -43,7 +51,9 @@ def _g():
                 ("colibri_kv_trim", ci, [_vp, _vp, _vp]),
                 ("colibri_kv_fork", ci, [_vp, _vp, _vp, _i32, _vp]),
                 ("colibri_kv_compact", ci, [_vp, _vp, _vp, _vp, _vp, sz, _vp]),
-                ("colibri_kv_copy", ci, [_vp, _vp, _vp, _vp, _i32, _vp])]:
+                ("colibri_kv_copy", ci, [_vp, _vp, _vp, _vp, _i32, _vp]),
+                ("colibri_logits_workspace_bytes", sz, [_i32, _i32]),
+                ("colibri_adjust_logits", ci, [_vp, _vp, sz, _vp])]:
             fn = getattr(L, name)
             fn.restype, fn.argtypes = res, args
         _fns = (L,)
@@ -208,3 +218,96 @@ def kv_copy(cache: KVCache, src: torch.Tensor, dst: torch.Tensor, *, to: Optiona
     _flat(dst, torch.int32, src.shape, "dst")
     _do(dev, "colibri_kv_copy", ctypes.byref(cache.desc), ctypes.byref(to.desc), src.data_ptr(), dst.data_ptr(),
         src.shape[0])
+
+
+# ---------------------------------------------------------------------------
+
+
+class LogitsResult(NamedTuple):
+    """logits [rows][vocab] or None; token int32 [rows]; lse fp32 [rows]."""
+    logits: Optional[torch.Tensor]
+    token: Optional[torch.Tensor]
+    lse: Optional[torch.Tensor]
+
+
+def logits_workspace(rows: int, vocab: int, device="cuda") -> torch.Tensor:
+    """Workspace of adjust_logits for up to this many rows and tokens; calls that may overlap need one each."""
+    n = _g().colibri_logits_workspace_bytes(_length(rows), _length(vocab))
+    if n == 0:
+        raise _qre.ColibriError(_qre.COLI_E_INVAL, "colibri_logits_workspace_bytes")
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def _row_stride(t: torch.Tensor, shape: tuple, what: str) -> int:
+    if t.shape != shape:
+        raise ValueError(f"{what}: shape {tuple(shape)} expected, got {tuple(t.shape)}")
+    if shape[1] > 1 and t.stride(1) != 1:
+        raise ValueError(f"{what}: contiguous rows expected")
+    return t.stride(0) if shape[0] > 1 else shape[1]
+
+
+def adjust_logits(logits: torch.Tensor, *, tokens: Optional[torch.Tensor] = None, spans: Optional[torch.Tensor] = None,
+                  penalties: Optional[torch.Tensor] = None, bias: Optional[torch.Tensor] = None,
+                  bias_ids: Optional[torch.Tensor] = None, cu_bias: Optional[torch.Tensor] = None,
+                  mask: Optional[torch.Tensor] = None, mask_of: Optional[torch.Tensor] = None, write: bool = True,
+                  best: bool = True, out: Optional[torch.Tensor] = None,
+                  ws: Optional[torch.Tensor] = None) -> LogitsResult:
+    """Penalties, biases and a mask on logits [rows][vocab] (fp32 or bf16, rows may be strided),
+    in this order and in fp32; with `write` the result (in out, which may be logits, if
+    given), with `best` each row's best token and the log of its sum.
+
+    penalties fp32 [rows][3]: repetition (divides positive, multiplies other logits of
+    tokens that occur), frequency (times the count among the generated ones) and
+    presence, both subtracted.  spans int32 [rows][3]: the row's tokens are
+    tokens[spans[r][0]:spans[r][2]], those from spans[r][1] on were generated.
+    bias, bias_ids [n] with cu_bias int32 [rows + 1]: row r's entries are cu_bias[r] ..
+    cu_bias[r + 1] - 1; a token's are added up.  mask int32 [n_masks][words]: bit
+    t % 32 of word t // 32 allows token t; mask_of int32 [rows] names each row's mask, -1
+    none.  A row in which nothing is left gets token -1 and lse -inf."""
+    dev = _dev(logits)
+    if logits.dim() != 2:
+        raise ValueError("logits: [rows][vocab] expected")
+    rows, V = logits.shape
+    t = _type(logits.dtype)
+    _on(dev, tokens, spans, penalties, bias, bias_ids, cu_bias, mask, mask_of, out, ws)
+    ls = os = _row_stride(logits, (rows, V), "logits")
+    if (penalties is None) != (spans is None) or (penalties is None) != (tokens is None):
+        raise ValueError("tokens, spans and penalties: all or none expected")
+    if (bias is None) != (bias_ids is None) or (bias is None) != (cu_bias is None):
+        raise ValueError("bias, bias_ids and cu_bias: all or none expected")
+    if (mask is None) != (mask_of is None):
+        raise ValueError("mask and mask_of: both or none expected")
+    if penalties is not None:
+        _flat(tokens, torch.int32, (tokens.numel(),), "tokens")
+        _flat(spans, torch.int32, (rows, 3), "spans")
+        _flat(penalties, torch.float32, (rows, 3), "penalties")
+    if bias is not None:
+        _flat(bias_ids, torch.int32, (bias_ids.numel(),), "bias_ids")
+        _flat(bias, torch.float32, (bias_ids.numel(),), "bias")
+        _flat(cu_bias, torch.int32, (rows + 1,), "cu_bias")
+    ms = 0
+    if mask is not None:
+        if mask.dtype != torch.int32:
+            raise TypeError(f"mask: {torch.int32} expected, got {mask.dtype}")
+        if mask.dim() != 2 or mask.shape[1] < (V + 31) // 32:
+            raise ValueError(f"mask: [n_masks][{(V + 31) // 32}] expected, got {tuple(mask.shape)}")
+        ms = _row_stride(mask, tuple(mask.shape), "mask")
+        _flat(mask_of, torch.int32, (rows,), "mask_of")
+    if out is not None:
+        if not write:
+            raise ValueError("out: nothing is written without `write`")
+        if out.dtype != logits.dtype:
+            raise TypeError(f"out: {logits.dtype} expected, got {out.dtype}")
+        os = _row_stride(out, (rows, V), "out")
+    elif write:
+        out, os = torch.empty(rows, V, dtype=logits.dtype, device=dev), V
+    token = torch.empty(rows, dtype=torch.int32, device=dev) if best else None
+    lse = torch.empty(rows, dtype=torch.float32, device=dev) if best else None
+    if best and ws is None:
+        ws = logits_workspace(rows, V, dev)
+    a = LogitsDesc(logits.data_ptr(), _at(out), _at(token), _at(lse), _at(tokens), _at(spans), _at(penalties), _at(bias),
+                   _at(bias_ids), _at(cu_bias), _at(mask), _at(mask_of), ls, os, ms, t, rows, V,
+                   0 if tokens is None else tokens.numel(), 0 if bias is None else bias.numel(),
+                   0 if mask is None else mask.shape[0])
+    _do(dev, "colibri_adjust_logits", ctypes.byref(a), *(_room(ws) if ws is not None else (None, 0)))
+    return LogitsResult(out, token, lse)

@@ -111,3 +111,62 @@ class Pages:
             self.refs[a], self.refs[b] = 0, self.refs[a]
         pad = [-1] * (n // 2 - len(src))
         return src + pad, dst + pad, [live]
+
+
+# ---- logits ---------------------------------------------------------------
+
+
+def adjust_row(x, tokens, span, penalties, ids, bias, words, dtype):
+    """One row's adjusted logits in `dtype`, and the sum of the magnitudes that were rounded."""
+    x = x.to(dtype)
+    V, A = x.numel(), x.abs().double()
+    if penalties is not None:
+        rep, freq, pres = (float(v) for v in penalties)
+        first, made, end = max(int(span[0]), 0), int(span[1]), min(int(span[2]), len(tokens))
+        part = tokens[first:max(end, first)]
+        inside = (part >= 0) & (part < V)
+        late = torch.arange(first, max(end, first)) >= made
+        seen = torch.bincount(part[inside].long(), minlength=V) > 0
+        count = torch.bincount(part[inside & late].long(), minlength=V)
+        rep, freq, pres = (torch.tensor(v, dtype=dtype) for v in (rep, freq, pres))
+        x = torch.where(seen, torch.where(x > 0, x / rep, x * rep), x)
+        A = A + x.abs().double()
+        less = freq * count.to(dtype) + pres
+        x = torch.where(count > 0, x - less, x)
+        A = A + (count > 0) * (x.abs() + (freq * count).abs() + less.abs()).double()
+    if ids is not None:
+        add = torch.zeros(V, dtype=dtype)
+        for t, b in zip(ids.tolist(), bias):
+            if 0 <= t < V:
+                add[t] = add[t] + b.to(dtype)
+                A[t] += add[t].abs().double()
+        x = x + add
+        A = A + x.abs().double()
+    if words is not None:
+        t = torch.arange(V)
+        ok = (words.long()[t // 32] >> (t % 32)) & 1
+        x = torch.where(ok > 0, x, torch.tensor(-math.inf, dtype=dtype))
+    return x, A
+
+
+def best(x):
+    """Lowest index of the largest value (the first NaN's, -1 where all is -inf)."""
+    nan = torch.isnan(x).nonzero()
+    if len(nan):
+        return int(nan[0])
+    top = x.max()
+    return -1 if top == -math.inf else int((x == top).nonzero()[0])
+
+
+def logits_tol(x, A, dtype):
+    """Every operation is rounded once, by at most 2^-24 of its result; A holds their magnitudes."""
+    return U[torch.float32] * A.nan_to_num(posinf=0.0) + U[dtype] * 1.001 * (dtype != torch.float32) * x.abs().nan_to_num(
+        posinf=0.0) + 1e-37
+
+
+def lse_tol(x, A, lse):
+    """Sums pass through at most 40 additions of positive numbers; a term's exponent is off by three roundings
+    of d = v - largest, and d exp(-d) < 0.37; the exponential by 2^-22: together under 2^-18.  The values' own errors
+    and the result's three roundings come on top."""
+    own = (U[torch.float32] * A)[torch.isfinite(x)]
+    return 2.0 ** -18 + (float(own.max()) if len(own) else 0.0) + 3 * 2.0 ** -24 * (abs(lse) if math.isfinite(lse) else 0.0)

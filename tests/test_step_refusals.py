@@ -136,3 +136,43 @@ def test_library_exports_every_declared_symbol(L):
     assert names
     for name in names:
         assert hasattr(L, name), name
+
+
+def logits(**kw):
+    d = dict({n: P for n in ("logits", "out", "token", "lse", "tokens", "spans", "penalties", "bias", "bias_ids", "cu_bias",
+                             "mask", "mask_of")}, logits_stride=100, out_stride=100, mask_stride=4, type=32, rows=2,
+             vocab=100, n_tokens=5, n_bias=5, n_masks=1)
+    d.update(kw)
+    return step.LogitsDesc(**d)
+
+
+@pytest.mark.parametrize("kw,st", [
+    (dict(rows=-1), INVAL), (dict(vocab=0), INVAL), (dict(rows=65536), UNSUP), (dict(vocab=(1 << 20) + 1, logits_stride=1 << 21,
+                                                                                     out_stride=1 << 21), UNSUP),
+    (dict(type=8), UNSUP), (dict(n_tokens=-1), INVAL), (dict(n_bias=-1), INVAL), (dict(n_masks=-1), INVAL),
+    (dict(logits=None), INVAL), (dict(out=None, token=None, lse=None), INVAL), (dict(spans=None), INVAL),
+    (dict(tokens=None), INVAL), (dict(bias=None), INVAL), (dict(bias_ids=None), INVAL), (dict(mask_of=None), INVAL),
+    (dict(mask_stride=3), INVAL), (dict(logits_stride=99), INVAL), (dict(out_stride=99, out=P + 4096), INVAL),
+    (dict(out_stride=101), INVAL), (dict(logits_stride=1 << 41, out=P + 4096), UNSUP), (dict(logits=P + 2), UNSUP),
+    (dict(out=P + 2), UNSUP), (dict(token=P + 2), UNSUP), (dict(lse=P + 1), UNSUP), (dict(tokens=P + 2), UNSUP),
+    (dict(spans=P + 2), UNSUP), (dict(penalties=P + 2), UNSUP), (dict(bias=P + 2), UNSUP), (dict(bias_ids=P + 2), UNSUP),
+    (dict(cu_bias=P + 2), UNSUP), (dict(mask=P + 2), UNSUP), (dict(mask_of=P + 2), UNSUP), (dict(logits=P + 1, type=16), UNSUP),
+    (dict(rows=0, logits=None), OK)])
+def test_logits(L, kw, st):
+    assert L.colibri_adjust_logits(r(logits(**kw)), P, BIG, None) == st
+
+
+def test_logits_workspace(L):
+    assert L.colibri_adjust_logits(None, P, BIG, None) == INVAL
+    assert L.colibri_adjust_logits(r(logits()), None, BIG, None) == INVAL
+    assert L.colibri_adjust_logits(r(logits()), P + 64, BIG, None) == UNSUP
+    assert L.colibri_adjust_logits(r(logits()), P, 0, None) == WS
+    for rows, vocab in ((-1, 5), (65536, 5), (1, 0), (1, (1 << 20) + 1)):
+        assert L.colibri_logits_workspace_bytes(rows, vocab) == 0
+    sizes = [L.colibri_logits_workspace_bytes(rows, v) for rows in (0, 1, 7, 65535) for v in (1, 4096, 4097, 1 << 20)]
+    assert all(sizes) and sizes == sorted(sizes[:4]) + sorted(sizes[4:8]) + sorted(sizes[8:12]) + sorted(sizes[12:])
+
+
+def test_logits_binding_refuses():
+    with pytest.raises(ValueError, match="device tensor"):
+        qre.adjust_logits(torch.zeros(2, 5))
