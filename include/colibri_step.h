@@ -113,6 +113,33 @@ int colibri_kv_copy(const coli_kv_cache* from, const coli_kv_cache* to, const in
                     int32_t n, coli_stream_t stream);
 
 /*
+ * Quantisation with one scale per token: for each row of x (type [rows][K], rows
+ * x_stride elements apart)
+ *   d = max |v| / 127,  q = clamp(round half away from zero (v * (1/d)), -127, 127)
+ * in fp32 as in colibri_quantize_q8_0, d = 0 and codes 0 for a row of zeros.  q int8
+ * [rows][K] (16-byte aligned), d fp32 [rows].  x 16-byte (fp32) or 8-byte (bf16) aligned,
+ * x_stride a multiple of 4, at least K.  K % 32 == 0, K <= COLI_MAX_LINEAR_K; values
+ * are finite.  rows == 0 is a no-op.
+ */
+int colibri_quantize_i8(const void* x, int32_t type, int64_t x_stride, int32_t rows, int32_t K, int8_t* q, float* d,
+                        coli_stream_t stream);
+
+/*
+ * colibri_linear_q for activations with one scale per token, for W a bank of one
+ * matrix [rows][K] with one scale per row (group 0), int8, int4 or int2:
+ *   out[t][r] = act(scale(r) * xd[t] * sum_k code(r, k) * xq[t][k] + bias[r]) + residual[t][r]
+ * The sum is exact in int32; it and the scales' product are rounded to fp32, whose
+ * product with the bias added is rounded once.  A token's result is the same in any
+ * batch.  xq int8 [S][K], xd fp32 [S]; bias, act, residual, out, alignments, limits and ws
+ * (sized by colibri_linear_i8_workspace_bytes for S or more tokens) as in
+ * colibri_linear_q.
+ */
+size_t colibri_linear_i8_workspace_bytes(const coli_qbank* W, int32_t S, int32_t out_type);
+int colibri_linear_i8(const coli_qbank* W, const int8_t* xq, const float* xd, int32_t S, const float* bias,
+                      int32_t act, const void* residual, void* out, int32_t out_type, void* ws, size_t ws_bytes,
+                      coli_stream_t stream);
+
+/*
  * What a step does to its logits before a token is chosen, and the choice of the
  * best one.  For each row, in fp32 and in this order, v = logits[t] and
  *   1. t among the row's tokens:            v = v > 0 ? v / repetition : v * repetition

@@ -1,7 +1,8 @@
 /*
  * step.h -- internal launch interface of the operators of a serving step: the
- * embedding lookup (embed.hip), the paged cache's sequences (kv_pages.hip) and what
- * is done to logits (logits.hip).
+ * embedding lookup (embed.hip), the paged cache's sequences (kv_pages.hip), the
+ * linear product with one activation scale per token (linear_i8.hip) and what is done
+ * to logits (logits.hip).
  * step_api.hip validates; the launchers assume validated arguments.
  */
 #ifndef COLI_STEP_H
@@ -28,6 +29,26 @@ hipError_t launch_kv_compact(const coli_kv_pages& p, int32_t* src, int32_t* dst,
                              hipStream_t s);
 hipError_t launch_kv_copy(const coli_kv_cache& from, const coli_kv_cache& to, const int32_t* src, const int32_t* dst,
                           int32_t n, hipStream_t s);
+
+hipError_t launch_quantize_i8(const void* x, int32_t type, int64_t stride, int32_t rows, int32_t K, int8_t* q, float* d,
+                              hipStream_t s);
+
+struct LinearI8Args {
+    const void* w;
+    const float* w_scale;
+    const int8_t* xq;
+    const float* xd;
+    const float* bias;
+    const void* residual;
+    void* out;
+    void* ws;
+    int32_t S, N, K, qtype, act, out_type;
+};
+
+/* What one call of S tokens needs; the most that one of 1 .. S tokens does. */
+size_t linear_i8_workspace_need(int32_t S, int32_t N, int32_t K);
+size_t linear_i8_workspace_bytes(int32_t S, int32_t N, int32_t K);
+hipError_t launch_linear_i8(const LinearI8Args& a, hipStream_t s);
 
 size_t logits_workspace_bytes(int32_t rows, int32_t vocab);
 hipError_t launch_adjust_logits(const coli_logits& a, void* ws, hipStream_t s);

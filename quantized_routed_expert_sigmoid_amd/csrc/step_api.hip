@@ -27,6 +27,16 @@ int check_matrix(const coli_qbank* W)
     return check_bank(W, 1, W->rows, W->K);
 }
 
+int check_linear_i8(const coli_qbank* W, int32_t S, int32_t out_type)
+{
+    const int st = check_matrix(W);
+    if (st)
+        return st;
+    if (S < 0)
+        return COLI_E_INVAL;
+    return W->group || S > COLI_MAX_TOKENS || !is_type(out_type) ? COLI_E_UNSUPPORTED : COLI_OK;
+}
+
 int check_pages_sizes(const coli_kv_pages* p)
 {
     if (!p || p->n_pages < 1 || p->n_seq < 0 || p->max_pages < 0)
@@ -177,6 +187,49 @@ int colibri_kv_copy(const coli_kv_cache* from, const coli_kv_cache* to, const in
     if (!aligned(src, 4) || !aligned(dst, 4))
         return COLI_E_UNSUPPORTED;
     return hip_status(launch_kv_copy(*from, *to, src, dst, n, (hipStream_t)stream));
+}
+
+int colibri_quantize_i8(const void* x, int32_t type, int64_t x_stride, int32_t rows, int32_t K, int8_t* q, float* d,
+                        coli_stream_t stream)
+{
+    if (rows < 0 || K < 32 || K % 32)
+        return COLI_E_INVAL;
+    if (rows > COLI_MAX_TOKENS || K > COLI_MAX_LINEAR_K || !is_type(type))
+        return COLI_E_UNSUPPORTED;
+    if (rows == 0)
+        return COLI_OK;
+    if (!x || !q || !d || x_stride < K || x_stride % 4)
+        return COLI_E_INVAL;
+    if (!aligned(x, type == COLI_F32 ? 16 : 8) || !aligned(q, 16) || !aligned(d, 4) || x_stride > (int64_t)1 << 40)
+        return COLI_E_UNSUPPORTED;
+    return hip_status(launch_quantize_i8(x, type, x_stride, rows, K, q, d, (hipStream_t)stream));
+}
+
+size_t colibri_linear_i8_workspace_bytes(const coli_qbank* W, int32_t S, int32_t out_type)
+{
+    return check_linear_i8(W, S, out_type) ? 0 : linear_i8_workspace_bytes(S, W->rows, W->K);
+}
+
+int colibri_linear_i8(const coli_qbank* W, const int8_t* xq, const float* xd, int32_t S, const float* bias,
+                      int32_t act, const void* residual, void* out, int32_t out_type, void* ws, size_t ws_bytes,
+                      coli_stream_t stream)
+{
+    const int st = check_linear_i8(W, S, out_type);
+    if (st)
+        return st;
+    if (act < COLI_ACT_NONE || act > COLI_ACT_GELU)
+        return COLI_E_INVAL;
+    if (S == 0)
+        return COLI_OK;
+    if (!xq || !xd || !out || !ws)
+        return COLI_E_INVAL;
+    if (!aligned(xq, 16) || !aligned(xd, 4) || !aligned(bias, 4) || !aligned(residual, 4) || !aligned(out, 4) ||
+        !aligned(ws, kAlign))
+        return COLI_E_UNSUPPORTED;
+    if (ws_bytes < linear_i8_workspace_need(S, W->rows, W->K))
+        return COLI_E_WORKSPACE;
+    const LinearI8Args a = {W->data, W->row_scale, xq, xd, bias, residual, out, ws, S, W->rows, W->K, W->qtype, act, out_type};
+    return hip_status(launch_linear_i8(a, (hipStream_t)stream));
 }
 
 size_t colibri_logits_workspace_bytes(int32_t rows, int32_t vocab)

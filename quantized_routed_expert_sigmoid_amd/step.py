@@ -16,7 +16,7 @@ import torch
 
 import quantized_routed_expert_sigmoid_amd as _qre
 
-from .block import KVCache, _at, _call, _dev, _f32, _flat, _i32, _i64, _length, _on, _room, _type, _vp
+from .block import _ACTS, KVCache, _at, _call, _dev, _f32, _flat, _i32, _i64, _length, _on, _room, _type, _vp
 
 _IDS = {torch.int32: 4, torch.int64: 8}
 
@@ -52,6 +52,9 @@ def _g():
                 ("colibri_kv_fork", ci, [_vp, _vp, _vp, _i32, _vp]),
                 ("colibri_kv_compact", ci, [_vp, _vp, _vp, _vp, _vp, sz, _vp]),
                 ("colibri_kv_copy", ci, [_vp, _vp, _vp, _vp, _i32, _vp]),
+                ("colibri_quantize_i8", ci, [_vp, _i32, _i64, _i32, _i32, _vp, _vp, _vp]),
+                ("colibri_linear_i8_workspace_bytes", sz, [_vp, _i32, _i32]),
+                ("colibri_linear_i8", ci, [_vp, _vp, _vp, _i32, _vp, _i32, _vp, _vp, _i32, _vp, sz, _vp]),
                 ("colibri_logits_workspace_bytes", sz, [_i32, _i32]),
                 ("colibri_adjust_logits", ci, [_vp, _vp, sz, _vp])]:
             fn = getattr(L, name)
@@ -218,6 +221,69 @@ def kv_copy(cache: KVCache, src: torch.Tensor, dst: torch.Tensor, *, to: Optiona
     _flat(dst, torch.int32, src.shape, "dst")
     _do(dev, "colibri_kv_copy", ctypes.byref(cache.desc), ctypes.byref(to.desc), src.data_ptr(), dst.data_ptr(),
         src.shape[0])
+
+
+# ---------------------------------------------------------------------------
+
+
+def quantize_i8(x: torch.Tensor):
+    """x [rows][K] fp32 or bf16 (rows may be strided) -> (codes int8 [rows][K], scales fp32
+    [rows]): 8 bits with one scale per row, what linear_i8 takes."""
+    dev = _dev(x)
+    if x.dim() != 2:
+        raise ValueError("x: [rows][K] expected")
+    rows, K = x.shape
+    t = _type(x.dtype)
+    stride = _row_stride(x, (rows, K), "x")
+    q = torch.empty(rows, K, dtype=torch.int8, device=dev)
+    d = torch.empty(rows, dtype=torch.float32, device=dev)
+    _do(dev, "colibri_quantize_i8", x.data_ptr(), t, stride, rows, K, q.data_ptr(), d.data_ptr())
+    return q, d
+
+
+def linear_i8_workspace(bank, S: int, dtype: torch.dtype = torch.float32) -> torch.Tensor:
+    """Workspace of linear_i8 for any number of tokens up to S; calls that may overlap need one each."""
+    return _linear_i8_ws(bank.desc(), _length(S), _type(dtype), bank.data.device)
+
+
+def _linear_i8_ws(w, S: int, t: int, dev: torch.device) -> torch.Tensor:
+    n = _g().colibri_linear_i8_workspace_bytes(ctypes.byref(w), S, t)
+    if n == 0:
+        raise _qre.ColibriError(_qre.COLI_E_INVAL, "colibri_linear_i8_workspace_bytes")
+    return torch.empty(n, dtype=torch.uint8, device=dev)
+
+
+def linear_i8(bank, xq: torch.Tensor, xd: torch.Tensor, *, bias: Optional[torch.Tensor] = None,
+              activation: Optional[str] = None, residual: Optional[torch.Tensor] = None,
+              dtype: Optional[torch.dtype] = None, out: Optional[torch.Tensor] = None,
+              ws: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """linear_q for activations with one scale per token (quantize_i8): xq int8 [S][K],
+    xd fp32 [S], and banks with one scale per row.  The sums are exact in whole
+    numbers and run at the int8 matrix cores' rate; the activations are as fine as
+    their token's largest value allows, where linear_q's scale each 32 of them."""
+    dev = _dev(xq)
+    if activation not in _ACTS:
+        raise ValueError(f"activation: one of {[a for a in _ACTS if a]} expected, got {activation!r}")
+    w = bank.desc()
+    if not (xq.dim() == 2 and xq.shape[1] == w.K):
+        raise ValueError(f"xq: [S][{w.K}] expected, got {tuple(xq.shape)}")
+    S = xq.shape[0]
+    given = out if out is not None else residual
+    dtype = dtype or (given.dtype if given is not None else torch.float32)
+    t = _type(dtype)
+    _on(dev, xd, bias, residual, out, ws, bank.data, bank.scale)
+    _flat(xq, torch.int8, (S, w.K), "xq")
+    _flat(xd, torch.float32, (S,), "xd")
+    _flat(bias, torch.float32, (w.rows,), "bias")
+    _flat(residual, dtype, (S, w.rows), "residual")
+    _flat(out, dtype, (S, w.rows), "out")
+    _bank_scales(bank, w)
+    if out is None:
+        out = torch.empty(S, w.rows, dtype=dtype, device=dev)
+    ws = _linear_i8_ws(w, S, t, dev) if ws is None else ws
+    _do(dev, "colibri_linear_i8", ctypes.byref(w), xq.data_ptr(), xd.data_ptr(), S, _at(bias), _ACTS[activation],
+        _at(residual), out.data_ptr(), t, *_room(ws))
+    return out
 
 
 # ---------------------------------------------------------------------------

@@ -26,6 +26,42 @@ def embed_tol(want, dtype):
     return (2 * U[torch.float32] * (1 + U[torch.float32]) + U[dtype] * 1.001 * (dtype != torch.float32)) * want.abs() + 1e-37
 
 
+# ---- linear product -------------------------------------------------------
+
+
+def quantize(x):
+    """Codes and scales of [rows][K] by the rule's fp32 operations."""
+    x = x.float()
+    d = x.abs().amax(1) / 127.0
+    v = x * torch.where(d > 0, 1.0 / d, torch.zeros(()))[:, None]
+    return round_half_away(v).clamp(-127, 127).to(torch.int8), d
+
+
+def linear(data, scale, bits, xq, xd, bias, act, residual):
+    """-> (out, the value before the bias, before the activation)."""
+    z = (xq.double() @ weight_codes(data, bits).double().t()) * scale.double() * xd.double()[:, None]
+    y = u = z + bias.double() if bias is not None else z
+    if act == "relu":
+        y = torch.where(y > 0, y, 0.0)
+    elif act == "silu":
+        y = y * torch.special.expit(y)
+    elif act == "gelu":
+        y = y * torch.special.ndtr(y)
+    return (y + residual.double() if residual is not None else y), z, u
+
+
+def linear_tol(y, z, u, act, dtype):
+    """The sum (exact in whole numbers) and the scales' product are rounded, their product with the bias
+    once; an activation's slope is under 1.2, its own error as in include/colibri_block.h; the residual's sum and
+    the result are rounded."""
+    e = 1.2 * (2.01 * U[torch.float32] * z.abs() + U[torch.float32] * u.abs())
+    if act == "silu":
+        e = e + 2.0 ** -23 * (u.abs() + 8)
+    elif act == "gelu":
+        e = e + 2.0 ** -22 * (1 + u.abs())
+    return e + U[torch.float32] * y.abs() * 1.01 + U[dtype] * 1.001 * (dtype != torch.float32) * y.abs() + 1e-37
+
+
 # ---- pages ----------------------------------------------------------------
 
 

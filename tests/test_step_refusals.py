@@ -176,3 +176,53 @@ def test_logits_workspace(L):
 def test_logits_binding_refuses():
     with pytest.raises(ValueError, match="device tensor"):
         qre.adjust_logits(torch.zeros(2, 5))
+
+
+@pytest.mark.parametrize("a,st", [
+    ((None, 32, 64, 2, 64, P, P), INVAL), ((P, 32, 64, 2, 64, None, P), INVAL), ((P, 32, 64, 2, 64, P, None), INVAL),
+    ((P, 32, 64, -1, 64, P, P), INVAL), ((P, 32, 64, 2, 48, P, P), INVAL), ((P, 32, 64, 2, 0, P, P), INVAL),
+    ((P, 32, 60, 2, 64, P, P), INVAL), ((P, 32, 66, 2, 64, P, P), INVAL), ((P, 8, 64, 2, 64, P, P), UNSUP),
+    ((P, 32, 1 << 41, 2, 64, P, P), UNSUP), ((P, 32, 32800, 2, 32800, P, P), UNSUP), ((P, 32, 64, 65537, 64, P, P), UNSUP),
+    ((P + 8, 32, 64, 2, 64, P, P), UNSUP), ((P + 4, 16, 64, 2, 64, P, P), UNSUP), ((P, 32, 64, 2, 64, P + 8, P), UNSUP),
+    ((P, 32, 64, 2, 64, P, P + 2), UNSUP), ((None, 32, 64, 0, 64, None, None), OK)])
+def test_quantize(L, a, st):
+    assert L.colibri_quantize_i8(*a, None) == st
+
+
+@pytest.mark.parametrize("kw,st", BANK_BAD + [(dict(group=32), UNSUP), (dict(group=48), INVAL)])
+def test_linear_bank(L, kw, st):
+    w = bank(**kw)
+    assert L.colibri_linear_i8(r(w), P, P, 1, None, 0, None, P, 32, P, BIG, None) == st
+    assert L.colibri_linear_i8_workspace_bytes(r(w), 1, 32) == 0
+
+
+@pytest.mark.parametrize("a,st", [
+    ((None, P, 1, P, 0, P, P, 32, P, BIG), INVAL), ((P, None, 1, P, 0, P, P, 32, P, BIG), INVAL),
+    ((P, P, -1, P, 0, P, P, 32, P, BIG), INVAL), ((P, P, 65537, P, 0, P, P, 32, P, BIG), UNSUP),
+    ((P, P, 1, P, 4, P, P, 32, P, BIG), INVAL), ((P, P, 1, P, -1, P, P, 32, P, BIG), INVAL),
+    ((P, P, 1, P, 0, P, None, 32, P, BIG), INVAL), ((P, P, 1, P, 0, P, P, 8, P, BIG), UNSUP),
+    ((P, P, 1, P, 0, P, P, 32, None, BIG), INVAL), ((P, P, 1, P, 0, P, P, 32, P, 0), WS),
+    ((P + 4, P, 1, P, 0, P, P, 32, P, BIG), UNSUP), ((P, P + 2, 1, P, 0, P, P, 32, P, BIG), UNSUP),
+    ((P, P, 1, P + 1, 0, P, P, 32, P, BIG), UNSUP), ((P, P, 1, P, 0, P + 2, P, 32, P, BIG), UNSUP),
+    ((P, P, 1, P, 0, P, P + 2, 32, P, BIG), UNSUP), ((P, P, 1, P, 0, P, P, 32, P + 64, BIG), UNSUP),
+    ((None, None, 0, None, 0, None, None, 32, None, 0), OK)])
+def test_linear(L, a, st):
+    assert L.colibri_linear_i8(r(bank()), *a, None) == st
+
+
+def test_linear_null(L):
+    assert L.colibri_linear_i8(None, P, P, 1, None, 0, None, P, 32, P, BIG, None) == INVAL
+    assert L.colibri_linear_i8_workspace_bytes(None, 1, 32) == 0
+    assert L.colibri_linear_i8_workspace_bytes(r(bank()), -1, 32) == 0
+    assert L.colibri_linear_i8_workspace_bytes(r(bank()), 0, 32) > 0
+
+
+@pytest.mark.parametrize("N,K", [(10240, 6144), (4096, 4096), (130, 2080), (64, 512), (1, 32768), (32768, 2048), (2100, 224),
+                                 (16, 128)])
+@pytest.mark.parametrize("bits", [8, 4])
+def test_linear_workspace_grows_with_the_batch(L, N, K, bits):
+    """A workspace for S tokens serves every smaller batch: its size never falls."""
+    w = bank(rows=N, K=K, qtype=bits)
+    sizes = sorted(set(range(1, 1300, 7)) | {64, 65, 128, 129, 256, 257, 2047, 2048, 2049, 4096, 8192, 16384, 32767, 32768, 65536})
+    most = [L.colibri_linear_i8_workspace_bytes(r(w), S, 32) for S in sizes]
+    assert all(a <= b for a, b in zip(most, most[1:])), list(zip(sizes, most))
