@@ -134,113 +134,80 @@ __device__ __forceinline__ v4i operand(const Codes32<BITS>& c, int half)
     return codes_i8<BITS>(r);
 }
 
-/*
- * A workgroup takes 16 R rows x 16 T tokens, its W waves the row's steps of 128 k in
- * turn.  Lane (c = l % 16, g = l / 16) of a step reads the 32 codes from 32 g on of
- * row and of token c: a row's step is one or two whole lines.  Both operands of
- * v_mfma_i32_16x16x64_i8 take their k in this order, so any order is right.  The next
- * U steps travel under the products of these.
- */
-template <int BITS, int R, int T, int W, int U, typename TO>
-__global__ __launch_bounds__(W * 64) void i8_rows(LinearI8Args a)
-{
-    __shared__ int part[W][R * T][256];
-    const int lane = threadIdx.x & 63, wv = wave_of(), c = lane & 15, g = lane >> 4;
-    const int n0 = blockIdx.x * (16 * R), t0 = blockIdx.y * (16 * T);
-    const int steps = (a.K + 127) / 128;
-    const int64_t row_bytes = (int64_t)a.K * BITS / 8;
-    const uint8_t* w[R];
-    const int8_t* x[T];
-#pragma unroll
-    for (int r = 0; r < R; ++r)
-        w[r] = (const uint8_t*)a.w + min(n0 + 16 * r + c, a.N - 1) * row_bytes;
-#pragma unroll
-    for (int t = 0; t < T; ++t)
-        x[t] = a.xq + (int64_t)min(t0 + 16 * t + c, a.S - 1) * a.K;
+constexpr int kRowsWaves = 8;
 
-    Codes32<BITS> wc[2][U][R];
-    Codes32<8> xc[2][U][T];
-    auto load = [&](int first, int p) {
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int k = (first + u * W) * 128 + g * 32, at = min(k, a.K - 32);
-#pragma unroll
-            for (int r = 0; r < R; ++r)
-                wc[p][u][r] = load_codes<BITS>(w[r] + at * BITS / 8);
-#pragma unroll
-            for (int t = 0; t < T; ++t)
-                xc[p][u][t] = load_codes<8>((const uint8_t*)x[t] + at);
-        }
+/*
+ * A workgroup takes 16 rows x 16 tokens, its waves the row's steps of 128 k in turn, one
+ * ahead of the products.  Lane (c = l % 16, g = l / 16) of a step reads the 32 codes from 32 g
+ * on of row and of token c: a row's step is a whole line, half or a quarter of one.  Both
+ * operands of v_mfma_i32_16x16x64_i8 take their k in this order, so any order is right.  Bound by
+ * the weights' bytes and the latency of two or three loads in turn: 1 x 10240 x 6144 with
+ * the weights in HBM int4 9.3 us, int8 14.1 (4.5 TB/s).
+ */
+template <int BITS, typename TO>
+__global__ __launch_bounds__(kRowsWaves * 64) void i8_rows(LinearI8Args a)
+{
+    constexpr int W = kRowsWaves;
+    __shared__ int part[W][256];
+    const int lane = threadIdx.x & 63, wv = wave_of(), c = lane & 15, g = lane >> 4;
+    const int n0 = blockIdx.x * 16, t0 = blockIdx.y * 16, steps = (a.K + 127) / 128;
+    const uint8_t* w = (const uint8_t*)a.w + min(n0 + c, a.N - 1) * ((int64_t)a.K * BITS / 8);
+    const uint8_t* x = (const uint8_t*)a.xq + (int64_t)min(t0 + c, a.S - 1) * a.K;
+    Codes32<BITS> wc[2];
+    Codes32<8> xc[2];
+    auto load = [&](int step, int p) {
+        const int at = min(step * 128 + g * 32, a.K - 32);
+        wc[p] = load_codes<BITS>(w + at * BITS / 8);
+        xc[p] = load_codes<8>(x + at);
     };
-    v4i acc[R][T];
+    v4i acc = {0, 0, 0, 0};
+    auto multiply = [&](int step, int p) {
+        const bool in = step * 128 + g * 32 < a.K; /* past the row's end: zeros */
 #pragma unroll
-    for (int r = 0; r < R; ++r)
-#pragma unroll
-        for (int t = 0; t < T; ++t)
-            acc[r][t] = v4i{0, 0, 0, 0};
-    auto multiply = [&](int first, int p) {
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const bool in = (first + u * W) * 128 + g * 32 < a.K; /* past the row's end: zeros */
-            v4i xo[T][2];
-#pragma unroll
-            for (int t = 0; t < T; ++t)
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    xo[t][i] = operand<8>(xc[p][u][t], i);
-                    xo[t][i] = in ? xo[t][i] : v4i{0, 0, 0, 0};
-                }
-#pragma unroll
-            for (int r = 0; r < R; ++r)
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const v4i wo = operand<BITS>(wc[p][u][r], i);
-#pragma unroll
-                    for (int t = 0; t < T; ++t)
-                        acc[r][t] = __builtin_amdgcn_mfma_i32_16x16x64_i8(wo, xo[t][i], acc[r][t], 0, 0, 0);
-                }
+        for (int i = 0; i < 2; ++i) {
+            const v4i xo = operand<8>(xc[p], i);
+            acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(operand<BITS>(wc[p], i), in ? xo : v4i{0, 0, 0, 0}, acc, 0, 0, 0);
         }
     };
     load(wv, 0);
-    for (int s = wv; s < steps; s += 2 * U * W) {
-        load(s + U * W, 1);
+    for (int s = wv; s < steps; s += 2 * W) {
+        load(s + W, 1);
         multiply(s, 0);
-        load(s + 2 * U * W, 0);
-        multiply(s + U * W, 1);
+        load(s + 2 * W, 0);
+        multiply(s + W, 1);
     }
-#pragma unroll
-    for (int r = 0; r < R; ++r)
-#pragma unroll
-        for (int t = 0; t < T; ++t)
-            *(v4i*)(part[wv][r * T + t] + lane * 4) = acc[r][t];
+    *(v4i*)(part[wv] + lane * 4) = acc;
     __syncthreads();
-    for (int i = wv; i < R * T; i += W) {
-        v4i sum = {0, 0, 0, 0};
+    if (wv)
+        return;
+    v4i sum = {0, 0, 0, 0};
 #pragma unroll
-        for (int j = 0; j < W; ++j)
-            sum += *(const v4i*)(part[j][i] + lane * 4);
-        const int tok = t0 + 16 * (i % T) + c, n = n0 + 16 * (i / T) + 4 * g;
-        const int e[4] = {sum[0], sum[1], sum[2], sum[3]};
-        float v[4];
-        finish4(a, 1.0f / (float)(1 << (8 - BITS)), a.xd[min(tok, a.S - 1)], n, e, v);
-        activate_all<4>(v, a.act);
-        store_rows<TO>(a, tok, n, v);
-    }
+    for (int j = 0; j < W; ++j)
+        sum += *(const v4i*)(part[j] + lane * 4);
+    const int tok = t0 + c, n = n0 + 4 * g, e[4] = {sum[0], sum[1], sum[2], sum[3]};
+    float v[4];
+    finish4(a, 1.0f / (float)(1 << (8 - BITS)), a.xd[min(tok, a.S - 1)], n, e, v);
+    activate_all<4>(v, a.act);
+    store_rows<TO>(a, tok, n, v);
 }
 
 /* ---- many tokens ---------------------------------------------------------- */
 
-constexpr int kStageK = 64; /* k of a stage: two instructions deep */
-constexpr int kStages = 4;
-
-/* A workgroup of WR x WT waves, a wave of 32 RR rows x 32 TT tokens. */
-template <int BITS, int RR, int TT, int WR, int WT>
+/* A workgroup of WR x WT waves, a wave of 32 RR rows x 32 TT tokens; ST stages of KB
+ * depths of 32 k in LDS. */
+template <int BITS, int RR, int TT, int WR, int WT, int KB, int ST>
 struct TileShape {
-    static constexpr int kWaves = WR * WT, kRows = 32 * RR * WR, kTok = 32 * TT * WT;
-    static constexpr int kXC = kStageK / kChunk, kWC = kStageK * BITS / 8 / kChunk; /* chunks of a token, of a row: 4; 4, 2, 1 */
-    static constexpr int kX = kTok * kStageK, kW = kRows * kStageK * BITS / 8, kStage = kX + kW;
-    static constexpr int kXRuns = kX / 1024 / kWaves, kWRuns = (kW / 1024 + kWaves - 1) / kWaves;
-    static constexpr int kLoads = kXRuns + kWRuns; /* of a wave and stage; where there are fewer runs than waves, waves load the same one */
+    static constexpr int kWaves = WR * WT, kRows = 32 * RR * WR, kTok = 32 * TT * WT, kK = 32 * KB;
+    static constexpr int kXC = kK / kChunk, kWC = kK * BITS / 8 / kChunk; /* chunks of a token, of a row */
+    static constexpr int kX = kTok * kK, kW = kRows * kK * BITS / 8, kStage = kX + kW;
+    /* the last step takes the stages' place: of each wave 32 tokens x 64 rows (32) in fp32, tokens 16 bytes further apart */
+    static constexpr int kOutRow = (RR > 1 ? 64 : 32) + 4, kOut = 32 * kOutRow;
+    /* behind both: the rows' scales and biases, the tokens' scales */
+    static constexpr int kScales = std::max(kStage * ST, kOut * 4 * kWaves), kLds = kScales + (2 * kRows + kTok) * 4;
+    /* loads of a wave and stage; where there are fewer runs than waves, waves load the same one, so that
+     * every wave counts alike */
+    static constexpr int kXRuns = (kX / 1024 + kWaves - 1) / kWaves, kWRuns = (kW / 1024 + kWaves - 1) / kWaves;
+    static constexpr int kLoads = kXRuns + kWRuns;
 };
 
 struct I8TileArgs {
@@ -249,17 +216,18 @@ struct I8TileArgs {
 };
 
 /*
- * Stages of 64 k travel from memory to LDS three ahead.  A wave reads the operands of
- * one instruction depth (32 k) while the products of the one before run; the wait
- * for the next stage and the workgroup's barrier lie in the middle of a stage, under
- * its first half's products.  Lane (col = l % 32, h = l / 32) of an operand takes k =
- * 16 h .. + 15 of row or token col.
+ * Stages travel from memory to LDS ST ahead.  A wave reads the operands of one depth (32
+ * k) while the products of the depth before run.  When the last depth of a stage is
+ * read the stage's buffer is free: the wait for the next stage and the workgroup's barrier
+ * lie there, under the last depth's products, and the stage ST further goes into the
+ * buffer.  Lane (col = l % 32, h = l / 32) of an operand takes k = 16 h .. + 15 of row
+ * or token col.
  */
-template <int BITS, int RR, int TT, int WR, int WT, int PER_CU, typename TO>
+template <int BITS, int RR, int TT, int WR, int WT, int KB, int ST, int PER_CU, typename TO>
 __global__ __launch_bounds__(WR* WT * 64, PER_CU* WR* WT / 4) void i8_tiles(LinearI8Args a, I8TileArgs ta)
 {
-    using L = TileShape<BITS, RR, TT, WR, WT>;
-    constexpr int WC = L::kWC, XB = L::kX, NW = L::kWaves;
+    using L = TileShape<BITS, RR, TT, WR, WT, KB, ST>;
+    constexpr int WC = L::kWC, XC = L::kXC, XB = L::kX, NW = L::kWaves;
     extern __shared__ __align__(1024) uint8_t lds[];
     const int lane = threadIdx.x & 63, wv = wave_of(), h = lane >> 5, col = lane & 31;
     const int unit = (int)xcd_unit(), total = ta.n_tiles * ta.t_tiles;
@@ -270,43 +238,63 @@ __global__ __launch_bounds__(WR* WT * 64, PER_CU* WR* WT / 4) void i8_tiles(Line
     const int wr = wv % WR * 32 * RR, wt = wv / WR * 32 * TT; /* the wave's rows and tokens in the tile */
     const int share = (ta.stages + ta.splits - 1) / ta.splits;
     const int s0 = split * share, s1 = min(s0 + share, ta.stages);
-    const int row_bytes = (int)((int64_t)a.K * BITS / 8);
+    const int row_bytes = (int)((int64_t)a.K * BITS / 8), depths = a.K / 32;
 
     /* Slot c of a token or row holds chunk c ^ f, so that 16 of them read at one
      * chunk fall into different banks. */
-    auto xswz = [](int t) { return t / 4 % 4; };
+    auto xswz = [](int t) { return t / (16 / XC) % XC; };
     auto wswz = [](int n) { return n / (16 / WC) % WC; };
     const uint32_t lds0 = lds_address(lds);
     const uint8_t* w0 = (const uint8_t*)a.w + (int64_t)wg.n0 * row_bytes;
     const int8_t* x0 = a.xq + (int64_t)wg.tok0 * a.K;
-    int xrow[L::kXRuns], xchunk[L::kXRuns], wrow[L::kWRuns], wchunk[L::kWRuns];
-#pragma unroll
-    for (int i = 0; i < L::kXRuns; ++i) {
-        const int slot = (i * NW + wv) * 64 + lane, t = slot / L::kXC;
-        xrow[i] = min(t, a.S - 1 - wg.tok0) * a.K;
-        xchunk[i] = (slot % L::kXC ^ xswz(t)) * kChunk;
-    }
-#pragma unroll
-    for (int i = 0; i < L::kWRuns; ++i) {
-        const int slot = (i * NW + wv) % (L::kW / 1024) * 64 + lane, n = slot / WC;
-        wrow[i] = min(n, a.N - 1 - wg.n0) * row_bytes;
-        wchunk[i] = (slot % WC ^ wswz(n)) * kChunk;
-    }
-    /* Load i of a stage; past the row's end its last bytes, past the last stage that
-     * one (loaded and not used). */
-    auto fetch1 = [&](int stage, int i) {
-        const uint32_t buf = lds0 + stage % kStages * L::kStage;
-        stage = min(stage, ta.stages - 1);
-        if (i < L::kXRuns) {
-            const int k = stage * kStageK, b = min(k, a.K - kChunk);
-            to_lds(x0 + b, xrow[i] + min(k + xchunk[i], a.K - kChunk) - b, buf + (i * NW + wv) * 1024);
+    /* Each lane's row (token) and chunk of its runs, as offsets from the stage's first byte less 16: a partly filled last
+     * stage loads the row's last bytes again for what lies behind them. */
+    const int last = ta.stages - 1, x_left = a.K - last * L::kK, w_left = row_bytes - last * (WC * kChunk);
+    uint32_t xoff[L::kXRuns], woff[L::kWRuns];
+    auto aim = [&](int x_most, int w_most) {
+        each<L::kXRuns>([&](auto i) {
+            const int slot = (i * NW + wv) % (L::kX / 1024) * 64 + lane, t = slot / XC;
+            xoff[i] = min(t, a.S - 1 - wg.tok0) * a.K + min((slot % XC ^ xswz(t)) * kChunk, x_most - kChunk) + 16;
+        });
+        each<L::kWRuns>([&](auto i) {
+            const int slot = (i * NW + wv) % (L::kW / 1024) * 64 + lane, n = slot / WC;
+            woff[i] = min(n, a.N - 1 - wg.n0) * row_bytes + min((slot % WC ^ wswz(n)) * kChunk, w_most - kChunk) + 16;
+        });
+    };
+    /* Before the loads of a stage; past the last one that one is loaded and not used. */
+    auto aim_at = [&](int stage) {
+        if (stage >= last && x_left < L::kK)
+            aim(x_left, w_left);
+    };
+    auto fetch1 = [&](int stage, auto i) {
+        const uint32_t buf = lds0 + (stage - s0) % ST * L::kStage;
+        const int64_t k = min(stage, last);
+        if constexpr (i < L::kXRuns) {
+            to_lds(x0 + k * L::kK - 16, xoff[i], buf + (i * NW + wv) % (L::kX / 1024) * 1024);
         } else {
-            const int j = i - L::kXRuns;
-            const int k = stage * (WC * kChunk), last = row_bytes - kChunk, b = min(k, last);
-            to_lds(w0 + b, wrow[j] + min(k + wchunk[j], last) - b,
-                   buf + XB + (j * NW + wv) % (L::kW / 1024) * 1024);
+            constexpr int j = i - L::kXRuns;
+            to_lds(w0 + k * (WC * kChunk) - 16, woff[j], buf + XB + (j * NW + wv) % (L::kW / 1024) * 1024);
         }
     };
+    const float* scales = (const float*)(lds + L::kScales); /* [rows], then the biases [rows], then [tokens] */
+    if (ta.splits == 1) {
+        constexpr int kRowRuns = (L::kRows + 63) / 64, kTokRuns = (L::kTok + 63) / 64;
+        for (int i = wv; i < kRowRuns + kTokRuns; i += NW) {
+            const bool row = i < kRowRuns;
+            const int at = (row ? i : i - kRowRuns) * 64 + lane; /* less than 64 are there: past them the last one again */
+            if (row) {
+                const uint32_t off = (uint32_t)min(wg.n0 + min(at, L::kRows - 1), a.N - 1) * 4;
+                if (L::kRows >= 64 || lane < L::kRows) {
+                    word_to_lds(a.w_scale, off, lds0 + L::kScales + i * 256);
+                    if (a.bias)
+                        word_to_lds(a.bias, off, lds0 + L::kScales + L::kRows * 4 + i * 256);
+                }
+            } else if (L::kTok >= 64 || lane < L::kTok) {
+                word_to_lds(a.xd, (uint32_t)min(wg.tok0 + min(at, L::kTok - 1), a.S - 1) * 4,
+                            lds0 + L::kScales + L::kRows * 8 + (i - kRowRuns) * 256);
+            }
+        }
+    }
     v16i acc[RR][TT];
 #pragma unroll
     for (int r = 0; r < RR; ++r)
@@ -316,60 +304,61 @@ __global__ __launch_bounds__(WR* WT * 64, PER_CU* WR* WT / 4) void i8_tiles(Line
             for (int i = 0; i < 16; ++i)
                 acc[r][t][i] = 0;
 
-    const bool odd = a.K % kStageK != 0; /* the last stage has one depth only */
     RawCodes<BITS> wf[2][RR];
     v4i xf[2][TT];
     auto read1 = [&](int stage, auto kb, auto i) {
-        const uint8_t* buf = lds + stage % kStages * L::kStage;
-        if constexpr (i < RR) {
-            const int n = wr + i * 32 + col;
-            const int cc = BITS == 8 ? 2 * kb + h : BITS == 4 ? +kb : 0;
-            /* an int2 row's odd last depth was loaded with the one before it */
-            const int half = BITS == 2 && odd && stage == ta.stages - 1 ? 1 : +kb;
-            wf[kb][i] = read_codes<BITS>(buf + XB + (n * WC + (cc ^ wswz(n))) * kChunk, half, h);
+        const uint8_t* buf = lds + (stage - s0) % ST * L::kStage;
+        /* row part 0, the tokens' parts, the other rows': as the products need them */
+        constexpr int r = i == 0 ? 0 : i - TT;
+        if constexpr (i == 0 || i > TT) {
+            const int n = wr + r * 32 + col;
+            const int c = BITS == 8 ? 2 * kb + h : BITS == 4 ? +kb : kb / 2;
+            /* an odd last depth of an int2 row was loaded with the one before it */
+            const int half = BITS == 2 && (depths & 1) && stage * KB + kb == depths - 1 ? 1 : kb & 1;
+            wf[kb & 1][r] = read_codes<BITS>(buf + XB + (n * WC + (c ^ wswz(n))) * kChunk, half, h);
         } else {
-            const int t = wt + (i - RR) * 32 + col;
-            xf[kb][i - RR] = *(const v4i*)(buf + (t * L::kXC + ((2 * kb + h) ^ xswz(t))) * kChunk);
+            const int t = wt + (i - 1) * 32 + col;
+            xf[kb & 1][i - 1] = *(const v4i*)(buf + (t * XC + ((2 * kb + h) ^ xswz(t))) * kChunk);
         }
     };
     constexpr int kReads = RR + TT, kMul = RR * TT;
-    const std::integral_constant<int, 0> first{};
-    const std::integral_constant<int, 1> second{};
-    for (int s = 0; s < kStages - 1; ++s)
+    /* reads are issued under the first half of the products, so that the last has come when it is needed */
+    constexpr int kEach = (2 * kReads + kMul - 1) / kMul;
+    static_assert(KB % 2 == 0 && ST >= 2);
+    aim(L::kK, WC * kChunk);
+    for (int s = 0; s < ST; ++s) {
+        aim_at(s0 + s);
         each<L::kLoads>([&](auto i) { fetch1(s0 + s, i); });
-    arrive_all<L::kLoads*(kStages - 2)>();
-    each<kReads>([&](auto i) { read1(s0, first, i); });
+    }
+    arrive_all<L::kLoads*(ST - 1)>();
+    each<kReads>([&](auto i) { read1(s0, std::integral_constant<int, 0>(), i); });
     for (int stage = s0; stage < s1; ++stage) {
-        /* the products of one depth, and after product m its share of what else is to be issued */
-        auto multiply = [&](auto kb, auto other) {
+        each<KB>([&](auto kb) {
+            if constexpr (kb == KB - 1) { /* stage + 1 is there, and every wave has read this one */
+                arrive_all<L::kLoads*(ST - 2)>();
+                aim_at(stage + ST);
+            }
+            if constexpr (kb > 0) /* depths past the row's end take no part */
+                if (stage * KB + kb >= depths) {
+                    asm volatile(""); /* a branch: as selections these would cost every stage */
+                    each<TT>([&](auto t) { xf[kb & 1][t] = v4i{0, 0, 0, 0}; });
+                }
             v4i wo[RR];
-            each<RR>([&](auto r) { wo[r] = codes_i8<BITS>(wf[kb][r]); });
+            each<RR>([&](auto r) { wo[r] = codes_i8<BITS>(wf[kb & 1][r]); });
             each<kMul>([&](auto m) {
                 acc[m / TT][m % TT] =
-                    __builtin_amdgcn_mfma_i32_32x32x32_i8(wo[m / TT], xf[kb][m % TT], acc[m / TT][m % TT], 0, 0, 0);
-                other(m);
+                    __builtin_amdgcn_mfma_i32_32x32x32_i8(wo[m / TT], xf[kb & 1][m % TT], acc[m / TT][m % TT], 0, 0, 0);
+                /* this product's share of the next depth's reads, and of the loads */
+                each<kReads>([&](auto i) {
+                    if constexpr (i / kEach == m)
+                        read1(kb == KB - 1 ? stage + 1 : stage, std::integral_constant<int, (kb + 1) % KB>(), i);
+                });
+                if constexpr (kb == KB - 1)
+                    each<L::kLoads>([&](auto i) {
+                        if constexpr (i * kMul / L::kLoads == m)
+                            fetch1(stage + ST, i);
+                    });
                 __builtin_amdgcn_sched_barrier(0);
-            });
-        };
-        multiply(first, [&](auto m) {
-            each<kReads>([&](auto i) {
-                if constexpr (i * kMul / kReads == m)
-                    read1(stage, second, i);
-            });
-        });
-        /* stage + 1 is there, and every wave has left stage - 1 */
-        arrive_all<L::kLoads*(kStages - 3)>();
-        /* the second depth of an odd row's last stage takes no part */
-        const int part = odd && stage == ta.stages - 1 ? 0 : -1;
-        each<TT>([&](auto t) { xf[1][t] &= part; });
-        multiply(second, [&](auto m) {
-            each<kReads>([&](auto i) {
-                if constexpr (i * kMul / kReads == m)
-                    read1(stage + 1, first, i);
-            });
-            each<L::kLoads>([&](auto i) {
-                if constexpr (i * kMul / L::kLoads == m)
-                    fetch1(stage + kStages - 1, i);
             });
         });
     }
@@ -383,21 +372,39 @@ __global__ __launch_bounds__(WR* WT * 64, PER_CU* WR* WT / 4) void i8_tiles(Line
         });
         return;
     }
-    /* One 32 x 32 part at a time: the next one's scales are not loaded ahead, for which
-     * there are no registers. */
-    each<kMul>([&](auto m) {
-        __builtin_amdgcn_sched_barrier(0);
-        asm volatile("" ::: "memory");
-        constexpr int r = m / TT, t = m % TT;
-        const int tok = wg.tok0 + wt + t * 32 + col, n = wg.n0 + wr + r * 32 + 4 * h;
-        const float d = a.xd[min(tok, a.S - 1)];
-        each<4>([&](auto i) {
+    /* 32 tokens x 64 rows at a time change their order in LDS: they are stored in whole
+     * pieces of 256 bytes (bf16: 128). */
+    __syncthreads();
+    constexpr float unit_w = 1.0f / (float)(1 << (8 - BITS));
+    float* const mine = (float*)lds + wv * L::kOut;
+    each<TT*((RR + 1) / 2)>([&](auto q) {
+        constexpr int t = q / ((RR + 1) / 2), r0 = q % ((RR + 1) / 2) * 2, parts = r0 + 1 < RR ? 2 : 1;
+        const float d = scales[2 * L::kRows + wt + t * 32 + col];
+        each<4 * parts>([&](auto p) {
+            constexpr int r = r0 + p / 4, i = p % 4;
+            const int n = p / 4 * 32 + 8 * i + 4 * h, at = wr + r0 * 32 + n;
+            const float4 s = *(const float4*)(scales + at);
+            float4 b = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (a.bias)
+                b = *(const float4*)(scales + L::kRows + at);
             const v16i& z = acc[r][t];
-            const int e[4] = {z[4 * i], z[4 * i + 1], z[4 * i + 2], z[4 * i + 3]};
             float v[4];
-            finish4(a, 1.0f / (float)(1 << (8 - BITS)), d, n + 8 * i, e, v);
+            v[0] = __builtin_fmaf((float)z[4 * i], unit_w * s.x * d, b.x);
+            v[1] = __builtin_fmaf((float)z[4 * i + 1], unit_w * s.y * d, b.y);
+            v[2] = __builtin_fmaf((float)z[4 * i + 2], unit_w * s.z * d, b.z);
+            v[3] = __builtin_fmaf((float)z[4 * i + 3], unit_w * s.w * d, b.w);
             activate_all<4>(v, a.act);
-            store_rows<TO>(a, tok, n + 8 * i, v);
+            *(float4*)(mine + col * L::kOutRow + n) = make_float4(v[0], v[1], v[2], v[3]);
+        });
+        constexpr int kPer = 4 * parts; /* lanes of a token, eight rows each */
+        each<kPer / 2>([&](auto j) {
+            const int i = j * 64 + lane, tok = wg.tok0 + wt + t * 32 + i / kPer, n = i % kPer * 8;
+            const float* from = mine + i / kPer * L::kOutRow + n;
+            const float4 lo = *(const float4*)from, hi = *(const float4*)(from + 4);
+            const float v[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+            const int at = wg.n0 + wr + r0 * 32 + n;
+            store_rows<TO>(a, tok, at, v);
+            store_rows<TO>(a, tok, at + 4, v + 4);
         });
     });
 }
@@ -437,72 +444,85 @@ int64_t tiles_of(int32_t S, int32_t N, int rows, int toks)
     return (int64_t)((N + rows - 1) / rows) * ((S + toks - 1) / toks);
 }
 
-constexpr int kRowsTokens = 64;
-
-bool use_rows(int32_t S, int32_t K)
+/* Up to 16 tokens i8_rows needs no join and has more in flight, until there are tiles for
+ * most CUs without splits (13 tokens, 10240 x 6144 int4 13.8 us against 14.8, int8 equal;
+ * 4 tokens, 4096 x 4096 int4 4.3 against 9; but 13 tokens, 131071 x 6144 int8 178 against
+ * 138).  Rows of an int2 bank with K = 32 are shorter than one load of a tile. */
+bool use_rows(int32_t S, int32_t N, int32_t K)
 {
-    return S <= kRowsTokens || K < 128;
+    return K < 64 || (S <= 16 && N < 192 * 128);
 }
 
+/* Tiles of a launch: rows x tokens, how many run at a time, and what a stage of 128 k takes one such
+ * round, in ns (measured with K = 6144 int8; ns_few where only half of the places are taken).  A split of the
+ * stages costs a join: its launch, and the sums written and read. */
+struct Shape {
+    int rows, toks, places, ns, ns_few;
+    bool splits;
+};
+
+constexpr Shape kShapes[] = {
+    {320, 256, 256, 2500, 2500, false}, /* two rounds of 4096 x 10240: 235 us; 265 with 256 x 256, 280 with 128 x 128 */
+    {256, 256, 256, 1750, 1750, false}, /* 8192 x 8192 x 8192 467 us, 546 with 320 x 256 */
+    {128, 128, 256, 740, 740, true},    /* 1024 x 4096 x 4096 24.4 us; 26.8 with 128 x 64, 69 with 256 x 256 */
+    {128, 64, 512, 800, 580, true},     /* 64 x 10240 x 6144 18.8 us in three splits, about 28 in one */
+    {128, 32, 512, 720, 400, true},     /* up to 32 tokens: 32 x 10240 x 6144 17.3 us, 18.8 with 128 x 64 */
+};
+constexpr int kFew = 4, kMostSplits = 8, kJoinNs = 3000, kJoinBytesNs = 4000;
+
 struct I8Plan {
-    int shape, rows, toks, n_tiles, t_tiles, stages, splits;
+    int shape, n_tiles, t_tiles, stages, splits;
     size_t total;
 };
 
 I8Plan plan_of(int32_t S, int32_t N, int32_t K)
 {
-    I8Plan p;
-    p.stages = (K + kStageK - 1) / kStageK;
-    p.shape = tiles_of(S, N, 256, 256) >= 256 ? 0 : tiles_of(S, N, 128, 128) >= 256 ? 1 : 2;
-    p.rows = p.toks = p.shape == 0 ? 256 : p.shape == 1 ? 128 : 64;
-    p.n_tiles = (N + p.rows - 1) / p.rows;
-    p.t_tiles = (S + p.toks - 1) / p.toks;
-    const int total = p.n_tiles * p.t_tiles;
-    p.splits = p.shape == 2 ? std::max(1, std::min(512 / total, p.stages / 4)) : 1;
-    p.total = p.splits > 1 ? (size_t)p.splits * total * p.rows * p.toks * 4 : 256;
+    I8Plan p = {};
+    p.stages = (K + 127) / 128;
+    int64_t least = INT64_MAX;
+    for (int i = S <= 32 ? kFew : 0; i < (S <= 32 ? kFew + 1 : kFew); ++i) {
+        const Shape& sh = kShapes[i];
+        const int64_t tiles = tiles_of(S, N, sh.rows, sh.toks);
+        for (int k = 1; k <= (sh.splits ? kMostSplits : 1); ++k) {
+            const int64_t wgs = tiles * k, part = (p.stages + k - 1) / k;
+            if (k > 1 && (wgs > sh.places || part < 4))
+                break;
+            const int64_t ns = (wgs + sh.places - 1) / sh.places * part * (wgs * 2 <= sh.places ? sh.ns_few : sh.ns) +
+                               (k > 1 ? kJoinNs + wgs * sh.rows * sh.toks * 8 / kJoinBytesNs : 0);
+            if (ns < least) {
+                least = ns;
+                p.shape = i;
+                p.splits = k;
+            }
+        }
+    }
+    const Shape& sh = kShapes[p.shape];
+    p.n_tiles = (N + sh.rows - 1) / sh.rows;
+    p.t_tiles = (S + sh.toks - 1) / sh.toks;
+    p.total = p.splits > 1 ? (size_t)p.splits * p.n_tiles * p.t_tiles * sh.rows * sh.toks * 4 : 256;
     return p;
-}
-
-template <int BITS, int R, int T, int U, typename TO>
-void launch_rows_w(const LinearI8Args& a, hipStream_t s)
-{
-    const int wgs = (a.N + 16 * R - 1) / (16 * R);
-    const dim3 grid(wgs, (a.S + 16 * T - 1) / (16 * T));
-    if (wgs >= 512)
-        hipLaunchKernelGGL((i8_rows<BITS, R, T, 4, U, TO>), grid, dim3(256), 0, s, a);
-    else
-        hipLaunchKernelGGL((i8_rows<BITS, R, T, 8, U, TO>), grid, dim3(512), 0, s, a);
 }
 
 template <int BITS, typename TO>
 hipError_t launch_rows(const LinearI8Args& a, hipStream_t s)
 {
-    if (a.S <= 16) {
-        if (a.N >= 16384)
-            launch_rows_w<BITS, 2, 1, 2, TO>(a, s);
-        else
-            launch_rows_w<BITS, 1, 1, 4, TO>(a, s);
-    } else if (a.S <= 32) {
-        launch_rows_w<BITS, 2, 2, 2, TO>(a, s);
-    } else {
-        launch_rows_w<BITS, 2, 4, 1, TO>(a, s);
-    }
+    hipLaunchKernelGGL((i8_rows<BITS, TO>), dim3((a.N + 15) / 16, (a.S + 15) / 16), dim3(kRowsWaves * 64), 0, s, a);
     return hipGetLastError();
 }
 
-template <int BITS, int RR, int TT, int WR, int WT, int PER_CU, typename TO>
+template <int BITS, int RR, int TT, int WR, int WT, int KB, int ST, int PER_CU, typename TO>
 hipError_t launch_tiles(const LinearI8Args& a, const I8Plan& p, hipStream_t s)
 {
     const I8TileArgs ta = {(int4*)a.ws, p.n_tiles, p.t_tiles, p.stages, p.splits};
-    constexpr int bytes = TileShape<BITS, RR, TT, WR, WT>::kStage * kStages;
+    constexpr int bytes = TileShape<BITS, RR, TT, WR, WT, KB, ST>::kLds;
     if (bytes > 64 * 1024) {
-        const hipError_t e = hipFuncSetAttribute((const void*)i8_tiles<BITS, RR, TT, WR, WT, PER_CU, TO>,
+        const hipError_t e = hipFuncSetAttribute((const void*)i8_tiles<BITS, RR, TT, WR, WT, KB, ST, PER_CU, TO>,
                                                  hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
         if (e != hipSuccess)
             return e;
     }
     const int total = p.n_tiles * p.t_tiles;
-    hipLaunchKernelGGL((i8_tiles<BITS, RR, TT, WR, WT, PER_CU, TO>), dim3((total * p.splits + 7) / 8 * 8),
+    hipLaunchKernelGGL((i8_tiles<BITS, RR, TT, WR, WT, KB, ST, PER_CU, TO>), dim3((total * p.splits + 7) / 8 * 8),
                        dim3(WR * WT * 64), bytes, s, a, ta);
     if (p.splits > 1)
         hipLaunchKernelGGL((i8_join<RR, TT, WR, WT, TO>), dim3(total, RR * TT * 4), dim3(WR * WT * 64), 0, s, a, ta,
@@ -513,13 +533,15 @@ hipError_t launch_tiles(const LinearI8Args& a, const I8Plan& p, hipStream_t s)
 template <int BITS, typename TO>
 hipError_t launch(const LinearI8Args& a, hipStream_t s)
 {
-    if (use_rows(a.S, a.K))
+    if (use_rows(a.S, a.N, a.K))
         return launch_rows<BITS, TO>(a, s);
     const I8Plan p = plan_of(a.S, a.N, a.K);
     switch (p.shape) {
-    case 0: return launch_tiles<BITS, 2, 4, 4, 2, 1, TO>(a, p, s);
-    case 1: return launch_tiles<BITS, 2, 2, 2, 2, 2, TO>(a, p, s);
-    default: return launch_tiles<BITS, 1, 1, 2, 2, 2, TO>(a, p, s);
+    case 0: return launch_tiles<BITS, 5, 2, 2, 4, 4, 2, 1, TO>(a, p, s);
+    case 1: return launch_tiles<BITS, 4, 2, 2, 4, 4, 2, 1, TO>(a, p, s);
+    case 2: return launch_tiles<BITS, 1, 2, 4, 2, 4, 3, 1, TO>(a, p, s);
+    case 3: return launch_tiles<BITS, 1, 2, 4, 1, 4, 3, 2, TO>(a, p, s);
+    default: return launch_tiles<BITS, 1, 1, 4, 1, 4, 3, 2, TO>(a, p, s);
     }
 }
 
@@ -551,20 +573,20 @@ hipError_t launch_quantize_i8(const void* x, int32_t type, int64_t stride, int32
 
 size_t linear_i8_workspace_need(int32_t S, int32_t N, int32_t K)
 {
-    return use_rows(S, K) ? 256 : plan_of(S, N, K).total;
+    return use_rows(S, N, K) ? 256 : plan_of(S, N, K).total;
 }
 
-/* The largest need of 1 .. S tokens: fewer tokens can be more splits of smaller
- * tiles.  The plan changes with every 64 tokens, and nothing is split from 256 tiles
- * of 128 x 128 on. */
+/* The largest need of 1 .. S tokens: fewer tokens can be more splits.  The plan changes
+ * with every 64 tokens (and at 32), and what is split has at most 256 tiles of 128 x 64, or half as many of
+ * 128 x 128. */
 size_t linear_i8_workspace_bytes(int32_t S, int32_t N, int32_t K)
 {
     size_t most = linear_i8_workspace_need(S, N, K);
-    if (use_rows(S, K))
+    if (K < 64)
         return most;
-    const int ends = std::min((S + 63) / 64, 512 / (int)std::min<int64_t>(512, tiles_of(1, N, 128, 1)) + 1);
-    for (int t = 1; t <= ends; ++t)
-        most = std::max(most, linear_i8_workspace_need(std::min(S, 64 * t), N, K));
+    const int ends = std::min((S + 63) / 64, 256 / (int)std::min<int64_t>(256, tiles_of(1, N, 128, 1)) + 1);
+    for (int t = 0; t <= ends; ++t)
+        most = std::max(most, linear_i8_workspace_need(std::min(S, t ? 64 * t : 32), N, K));
     return most;
 }
 
