@@ -145,7 +145,7 @@ int colibri_linear_i8(const coli_qbank* W, const int8_t* xq, const float* xd, in
  *   1. t among the row's tokens:            v = v > 0 ? v / repetition : v * repetition
  *   2. t among them count > 0 times since the first generated one:
  *                                           v = v - (frequency * count + presence)
- *   3. t among the row's biases:            v = v + (their sum, in the list's order)
+ *   3. t among the row's biases:            v = v + bias, for each of its entries in order
  *   4. t not allowed by the row's mask:     v = -inf
  * Outputs, each of which may be null, but not all: out = v rounded to type;
  * token = the lowest t of the largest v before that rounding, -1 where every v is

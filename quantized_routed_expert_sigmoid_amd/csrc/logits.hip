@@ -3,12 +3,20 @@
  * the best token and the log of the sum (include/colibri_step.h gives the order of
  * the steps).
  *
- * A workgroup takes a chunk of one row's vocabulary.  It counts the row's tokens that
- * fall into the chunk in LDS (whole numbers: no order matters), adds up their
- * biases there, and then takes the chunk's logits through all steps in one pass,
- * which also yields the chunk's largest value and its sum of exponentials; a second
- * launch joins the chunks of a row.  Every chunk of a row reads all of the row's
- * tokens, from the last-level cache.
+ * A workgroup takes a chunk of one row's vocabulary, sixteen logits a thread, which
+ * travel while it counts the row's tokens that fall into the chunk in LDS (whole
+ * numbers: no order matters) and picks the entries of the bias list that lie there.
+ * The logits then go through all steps in registers; every thread walks through the
+ * picked entries in the list's order and adds those of its own tokens, so none is
+ * added twice or out of turn.  The same pass yields the chunk's largest value and its
+ * sum of exponentials (running, in the manner of an online softmax, but over the runs of
+ * a thread only), and a second launch joins the chunks of a row.  Every chunk of a row
+ * reads all of the row's tokens and entries, from the caches.
+ *
+ * The logits' bytes would allow 15 us for 128 rows of 151003 bf16 with everything: it
+ * takes 37.5.  Without tokens, biases and masks the pass takes 18, with tokens 29: the
+ * loads of spans, tokens and counts follow each other, and LDS (four bytes a token) leaves
+ * room for eight workgroups a CU, so that there are 2.3 rounds of them.
  */
 #include "block_device.h"
 #include "step.h"
@@ -19,12 +27,18 @@ namespace coli {
 
 namespace {
 
-constexpr int kThreads = 512;
-constexpr int kWaves = kThreads / 64;
-constexpr int kTurn = 4 * kThreads;    /* tokens of a turn over the chunk; chunks are whole turns */
-constexpr uint32_t kSeen = 0x80000000u; /* among the tokens; then whether there is a bias, */
-constexpr uint32_t kBias = 0x40000000u;
-constexpr uint32_t kCount = kBias - 1;  /* and the count of generated ones */
+constexpr int kRun = 8;   /* consecutive tokens of a thread, */
+constexpr int kRuns = 2;  /* and its runs */
+/* Tokens of a workgroup, and the entries of a bias list that it looks at at once. */
+constexpr int chunk_of(int threads)
+{
+    return threads * kRun * kRuns;
+}
+constexpr int batch_of(int threads)
+{
+    return 2 * threads;
+}
+constexpr uint32_t kSeen = 0x80000000u;          /* among the tokens; below it the count of generated ones */
 
 /* What a chunk has to say about its row: the key is the largest value in the order
  * of unsigned numbers, then the lowest token (key_of). */
@@ -65,28 +79,61 @@ __device__ __forceinline__ unsigned long long wave_max(unsigned long long v)
     return v;
 }
 
-/* Four logits from token t on, -inf past the vocabulary's end. */
-template <typename T>
-__device__ __forceinline__ float4 logits4(const T* x, int t, int V)
+__device__ __forceinline__ void store8_any(float* p, const float* v)
 {
-    if (t + 4 <= V)
-        return load4_any(x + t);
-    const float none = -__builtin_inff();
-    return make_float4(t < V ? to_f32(x[t]) : none, t + 1 < V ? to_f32(x[t + 1]) : none,
-                       t + 2 < V ? to_f32(x[t + 2]) : none, none);
+    __builtin_memcpy(p, v, 32);
 }
 
-template <typename T>
-__global__ __launch_bounds__(kThreads) void adjust_kernel(coli_logits a, int chunk, Part* part)
+__device__ __forceinline__ void store8_any(bf16* p, const float* v)
 {
-    /* [chunk] each: counts, then the biases' sums where there are any */
-    extern __shared__ __align__(16) uint32_t counts[];
-    float* const sums = (float*)(counts + chunk);
+    const uint32_t w[4] = {pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7])};
+    __builtin_memcpy(p, w, 16);
+}
+
+/* A run of logits as they lie in memory, -inf past the vocabulary's end. */
+template <typename T>
+struct Run {
+    static constexpr int kWords = kRun * (int)sizeof(T) / 4;
+    uint32_t w[kWords];
+
+    __device__ __forceinline__ void load(const T* x, int t, int V)
+    {
+        if (t + kRun <= V) {
+            __builtin_memcpy(w, x + t, sizeof(w));
+            return;
+        }
+#pragma unroll
+        for (int i = 0; i < kWords; ++i)
+            w[i] = sizeof(T) == 4 ? 0xFF800000u : 0xFF80FF80u;
+#pragma unroll
+        for (int i = 0; i < kRun; ++i)
+            if (t + i < V) {
+                if constexpr (sizeof(T) == 4)
+                    w[i] = __float_as_uint(x[t + i]);
+                else
+                    w[i / 2] = (w[i / 2] & (i & 1 ? 0xFFFFu : 0xFFFF0000u)) | (uint32_t)x[t + i].u << (16 * (i & 1));
+            }
+    }
+
+    __device__ __forceinline__ float value(int i) const
+    {
+        if constexpr (sizeof(T) == 4)
+            return __uint_as_float(w[i]);
+        else
+            return __uint_as_float(i & 1 ? w[i / 2] & 0xFFFF0000u : w[i / 2] << 16);
+    }
+};
+
+template <typename T, int THREADS>
+__global__ __launch_bounds__(THREADS) void adjust_kernel(coli_logits a, Part* part)
+{
+    constexpr int kWaves = THREADS / 64, kChunk = chunk_of(THREADS), kBatch = batch_of(THREADS);
+    extern __shared__ __align__(16) uint32_t counts[]; /* [kChunk], of the row's tokens, where there are penalties */
     __shared__ unsigned long long keys[kWaves];
     __shared__ float exps[kWaves];
-    __shared__ int ids[kThreads], found[kWaves]; /* the chunk's among kThreads entries of the list */
-    __shared__ float bias[kThreads];
-    const int r = blockIdx.y, c0 = blockIdx.x * chunk, V = a.vocab, end = min(c0 + chunk, V);
+    __shared__ int ids[kBatch], found[2][kWaves]; /* of a batch the entries that lie in the chunk */
+    __shared__ float bias[kBatch];
+    const int r = blockIdx.y, c0 = blockIdx.x * kChunk, V = a.vocab, end = min(c0 + kChunk, V);
     const T* x = (const T*)a.logits + (int64_t)r * a.logits_stride;
 
     float rep = 1.0f, freq = 0.0f, pres = 0.0f;
@@ -109,61 +156,62 @@ __global__ __launch_bounds__(kThreads) void adjust_kernel(coli_logits a, int chu
     const bool counted = h1 > h0 && !(rep == 1.0f && freq == 0.0f && pres == 0.0f);
     const bool biased = b1 > b0;
     /* the first logits and entries travel while the counts are cleared and the tokens counted */
-    float4 next = logits4(x, c0 + 4 * (int)threadIdx.x, V);
-    if (counted || biased) {
-        const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
-        int id = -1, at = 0, n = 0;
-        float b = 0.0f;
-        uint64_t here = 0;
-        auto look = [&](int i) {
-            id = i < b1 ? a.bias_ids[i] : -1;
-            b = i < b1 ? a.bias[i] : 0.0f;
-            here = __ballot(id >= c0 && id < end);
+    Run<T> run[kRuns];
+    const int t0 = c0 + kRun * (int)threadIdx.x;
+#pragma unroll
+    for (int j = 0; j < kRuns; ++j)
+        run[j].load(x, t0 + j * (THREADS * kRun), V);
+    const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
+    int id[2];
+    float b[2];
+    uint64_t here[2];
+    auto look = [&](int base) {
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const int i = base + THREADS * k + threadIdx.x;
+            id[k] = i < b1 ? a.bias_ids[i] : -1;
+            b[k] = i < b1 ? a.bias[i] : 0.0f;
+        }
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            here[k] = __ballot(id[k] >= c0 && id[k] < end);
             if (lane == 0)
-                found[wv] = __popcll(here);
-        };
-        /* the entries that lie in the chunk, in the list's order */
-        auto gather = [&]() {
-            n = 0;
-            at = __popcll(here & ((1ull << lane) - 1));
+                found[k][wv] = __popcll(here[k]);
+        }
+    };
+    /* writes them down in the list's order; their number */
+    auto gather = [&]() {
+        int n = 0;
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            int at = n + __popcll(here[k] & ((1ull << lane) - 1));
 #pragma unroll
             for (int w = 0; w < kWaves; ++w) {
-                at += w < wv ? found[w] : 0;
-                n += found[w];
+                at += w < wv ? found[k][w] : 0;
+                n += found[k][w];
             }
-            if (here >> lane & 1) {
-                ids[at] = id;
-                bias[at] = b;
+            if (here[k] >> lane & 1) {
+                ids[at] = id[k];
+                bias[at] = b[k];
             }
-        };
-        /* the first entry of each token adds up all of them */
-        auto add = [&]() {
-            if ((int)threadIdx.x >= n)
-                return;
-            const int t = ids[threadIdx.x];
-            bool first = true;
-            for (int j = 0; j < (int)threadIdx.x; ++j)
-                first &= ids[j] != t;
-            if (!first)
-                return;
-            float s = counts[t - c0] & kBias ? sums[t - c0] : 0.0f;
-            for (int j = threadIdx.x; j < n; ++j)
-                s = ids[j] == t ? s + bias[j] : s;
-            sums[t - c0] = s;
-            counts[t - c0] |= kBias;
-        };
+        }
+        return n;
+    };
+    int listed = 0;
+    if (counted || biased) {
         if (biased)
-            look(b0 + threadIdx.x);
-        for (int i = threadIdx.x; i < chunk / 4; i += kThreads)
-            ((uint4*)counts)[i] = make_uint4(0, 0, 0, 0);
+            look(b0);
+        if (counted)
+            for (int i = threadIdx.x; i < kChunk / 4; i += THREADS)
+                ((uint4*)counts)[i] = make_uint4(0, 0, 0, 0);
         __syncthreads();
         if (biased)
-            gather();
+            listed = gather();
         if (counted) {
             auto scan = [&](int from, int to, bool generated) {
                 auto count = [&](int token) {
                     const uint32_t at = (uint32_t)(token - c0);
-                    if (at < (uint32_t)chunk) {
+                    if (at < (uint32_t)kChunk) {
                         if (generated)
                             atomicAdd(counts + at, 1u);
                         else
@@ -171,13 +219,13 @@ __global__ __launch_bounds__(kThreads) void adjust_kernel(coli_logits a, int chu
                     }
                 };
                 /* four loads of four tokens at once: the tokens come from the caches, and their latency counts */
-                constexpr int N = 4;
+                constexpr int N = 4, kStep = 4 * THREADS;
                 int64_t i = from + 4 * (int64_t)threadIdx.x;
-                for (; i + (N - 1) * kTurn + 4 <= to; i += N * kTurn) {
+                for (; i + (N - 1) * kStep + 4 <= to; i += N * kStep) {
                     int4 q[N];
 #pragma unroll
                     for (int j = 0; j < N; ++j)
-                        __builtin_memcpy(&q[j], a.tokens + i + j * kTurn, 16);
+                        __builtin_memcpy(&q[j], a.tokens + i + j * kStep, 16);
 #pragma unroll
                     for (int j = 0; j < N; ++j) {
                         count(q[j].x);
@@ -186,11 +234,11 @@ __global__ __launch_bounds__(kThreads) void adjust_kernel(coli_logits a, int chu
                         count(q[j].w);
                     }
                 }
-                /* up to three whole turns and a part */
+                /* up to three whole steps and a part */
                 int4 q[N];
 #pragma unroll
                 for (int j = 0; j < N; ++j) {
-                    const int64_t k = i + j * kTurn;
+                    const int64_t k = i + j * kStep;
                     q[j] = make_int4(-1, -1, -1, -1);
                     if (k + 4 <= to) {
                         __builtin_memcpy(&q[j], a.tokens + k, 16);
@@ -212,17 +260,6 @@ __global__ __launch_bounds__(kThreads) void adjust_kernel(coli_logits a, int chu
             scan(h0, mid, false);
             scan(mid, h1, true);
         }
-        if (biased) {
-            __syncthreads();
-            add();
-            for (int base = b0 + kThreads; base < b1; base += kThreads) {
-                look(base + threadIdx.x);
-                __syncthreads();
-                gather();
-                __syncthreads();
-                add();
-            }
-        }
         __syncthreads();
     }
 
@@ -230,51 +267,103 @@ __global__ __launch_bounds__(kThreads) void adjust_kernel(coli_logits a, int chu
     /* this thread's largest value and its token, its first NaN's, and the sum of exp(v - top) */
     float top = -__builtin_inff(), sum = 0.0f;
     int best = -1, nan = -1;
-    for (int t = c0 + 4 * (int)threadIdx.x; t < end; t += kTurn) {
-        float v[4] = {next.x, next.y, next.z, next.w};
-        if (t + kTurn < end)
-            next = logits4(x, t + kTurn, V);
-        if (counted || biased) {
-            const uint4 q = *(const uint4*)(counts + t - c0);
-            const uint32_t c[4] = {q.x, q.y, q.z, q.w};
-            if (q.x | q.y | q.z | q.w) {
+    float v[kRuns][kRun];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    if (c[i] & (kSeen | kCount))
-                        v[i] = v[i] > 0.0f ? v[i] / rep : v[i] * rep;
-                    if (c[i] & kCount)
-                        v[i] -= freq * (float)(c[i] & kCount) + pres;
-                    if (c[i] & kBias)
-                        v[i] += sums[t - c0 + i];
+    for (int j = 0; j < kRuns; ++j) {
+#pragma unroll
+        for (int i = 0; i < kRun; ++i)
+            v[j][i] = run[j].value(i);
+        if (!counted)
+            continue;
+#pragma unroll
+        for (int i = 0; i < kRun; i += 4) {
+            const uint4 q = *(const uint4*)(counts + t0 - c0 + j * (THREADS * kRun) + i);
+            if (!(q.x | q.y | q.z | q.w))
+                continue;
+            const uint32_t c[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                float& y = v[j][i + k];
+                if (c[k])
+                    y = y > 0.0f ? y / rep : y * rep;
+                if (c[k] & ~kSeen)
+                    y -= freq * (float)(c[k] & ~kSeen) + pres;
+            }
+        }
+    }
+    /* every thread goes through the entries in order and adds those of its tokens */
+    for (int base = b0; base < b1; base += kBatch) {
+        if (base > b0) {
+            __syncthreads();
+            look(base);
+            __syncthreads();
+            listed = gather();
+            __syncthreads();
+        }
+        for (int k = 0; k < listed; ++k) {
+            const uint32_t at = (uint32_t)(ids[k] - t0);
+            const float e = bias[k];
+#pragma unroll
+            for (int j = 0; j < kRuns; ++j) {
+                const uint32_t in = at - j * (THREADS * kRun);
+                if (in < (uint32_t)kRun) {
+#pragma unroll
+                    for (int i = 0; i < kRun; ++i)
+                        v[j][i] = in == (uint32_t)i ? v[j][i] + e : v[j][i];
                 }
             }
         }
+    }
+#pragma unroll
+    for (int j = 0; j < kRuns; ++j) {
+        const int t = t0 + j * (THREADS * kRun);
+        if (t >= end)
+            continue;
         if (mask) {
             const uint32_t bits = mask[t / 32] >> (t % 32);
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                v[i] = bits >> i & 1 ? v[i] : -__builtin_inff();
+            for (int i = 0; i < kRun; ++i)
+                v[j][i] = bits >> i & 1 ? v[j][i] : -__builtin_inff();
         }
         if (a.out) {
             T* o = (T*)a.out + (int64_t)r * a.out_stride + t;
-            if (t + 4 <= V) {
-                store4_any(o, make_float4(v[0], v[1], v[2], v[3]));
+            if (t + kRun <= V) {
+                store8_any(o, v[j]);
             } else {
-                for (int i = 0; t + i < V; ++i)
-                    store1(o + i, v[i]);
+#pragma unroll
+                for (int i = 0; i < kRun; ++i)
+                    if (t + i < V)
+                        store1(o + i, v[j][i]);
             }
         }
         if (part) { /* what lies past the vocabulary's end is -inf here */
-            const float most = fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3]));
+            float most = v[j][0];
+            bool odd = false;
+#pragma unroll
+            for (int i = 1; i < kRun; ++i)
+                most = fmaxf(most, v[j][i]);
+#pragma unroll
+            for (int i = 0; i < kRun; i += 2)
+                odd |= __builtin_isunordered(v[j][i], v[j][i + 1]);
             if (most > top) {
                 sum *= exp_of(top - most);
                 top = most;
-                best = t + (v[0] == most ? 0 : v[1] == most ? 1 : v[2] == most ? 2 : 3);
+#pragma unroll
+                for (int i = kRun - 1; i >= 0; --i)
+                    best = v[j][i] == most ? t + i : best;
             }
-            if (nan < 0 && (__builtin_isunordered(v[0], v[1]) || __builtin_isunordered(v[2], v[3])))
-                nan = t + (v[0] != v[0] ? 0 : v[1] != v[1] ? 1 : v[2] != v[2] ? 2 : 3);
-            if (best >= 0)
-                sum += exp_of(v[0] - top) + exp_of(v[1] - top) + (exp_of(v[2] - top) + exp_of(v[3] - top));
+            if (odd && nan < 0) {
+#pragma unroll
+                for (int i = kRun - 1; i >= 0; --i)
+                    nan = v[j][i] != v[j][i] ? t + i : nan;
+            }
+            if (best >= 0) {
+                float e[kRun];
+#pragma unroll
+                for (int i = 0; i < kRun; ++i)
+                    e[i] = exp_of(v[j][i] - top);
+                sum += (e[0] + e[1]) + (e[2] + e[3]) + ((e[4] + e[5]) + (e[6] + e[7]));
+            }
         }
     }
     if (!part)
@@ -324,25 +413,34 @@ __global__ __launch_bounds__(64) void join_kernel(coli_logits a, const Part* par
     }
 }
 
-/* Tokens of a chunk.  A row's tokens are read by each of its chunks, so long histories want
- * large ones; what is in flight on a CU is bounded by its LDS, and a row alone by its
- * workgroups. */
-int chunk_of(const coli_logits& a)
+constexpr int kSmall = 256, kLarge = 512;
+
+/* Every chunk of a row reads all of its tokens, so long histories want larger chunks (48 rows
+ * of 200001 fp32, histories of up to 131072: 48 us with 512 threads, 63 with 256; 32 rows of 151003 with up to
+ * 16000: 19.2 and 20.0), and others the smaller workgroups (128 rows of 151003 bf16, 4001: 44 and 37.5). */
+bool large_chunks(const coli_logits& a)
 {
-    const int turns = (a.vocab + kTurn - 1) / kTurn;
-    const bool far = a.penalties && a.n_tokens / a.rows > 8192;
-    const int most = a.cu_bias ? 2 : far ? 8 : 2;
-    return kTurn * std::max(1, std::min(most, (int)((int64_t)a.rows * turns / 512)));
+    return a.penalties && a.n_tokens / a.rows > 8192;
+}
+
+template <typename T, int THREADS>
+void launch(const coli_logits& a, Part* part, hipStream_t s)
+{
+    constexpr int chunk = chunk_of(THREADS);
+    const int chunks = (a.vocab + chunk - 1) / chunk;
+    hipLaunchKernelGGL((adjust_kernel<T, THREADS>), dim3(chunks, a.rows), dim3(THREADS), a.penalties ? chunk * 4 : 0, s, a,
+                       part);
+    if (part)
+        hipLaunchKernelGGL(join_kernel, dim3(a.rows), dim3(64), 0, s, a, part, chunks);
 }
 
 template <typename T>
 hipError_t launch(const coli_logits& a, Part* part, hipStream_t s)
 {
-    const int chunk = chunk_of(a), chunks = (a.vocab + chunk - 1) / chunk;
-    const int lds = chunk * (a.cu_bias ? 8 : a.penalties ? 4 : 0);
-    hipLaunchKernelGGL((adjust_kernel<T>), dim3(chunks, a.rows), dim3(kThreads), lds, s, a, chunk, part);
-    if (part)
-        hipLaunchKernelGGL(join_kernel, dim3(a.rows), dim3(64), 0, s, a, part, chunks);
+    if (large_chunks(a))
+        launch<T, kLarge>(a, part, s);
+    else
+        launch<T, kSmall>(a, part, s);
     return hipGetLastError();
 }
 
@@ -350,7 +448,7 @@ hipError_t launch(const coli_logits& a, Part* part, hipStream_t s)
 
 size_t logits_workspace_bytes(int32_t rows, int32_t vocab)
 {
-    const size_t chunks = (vocab + kTurn - 1) / kTurn;
+    const size_t chunks = (vocab + chunk_of(kSmall) - 1) / chunk_of(kSmall);
     return std::max<size_t>(256, ((size_t)rows * chunks * sizeof(Part) + 255) / 256 * 256);
 }
 

@@ -327,7 +327,7 @@ def adjust_logits(logits: torch.Tensor, *, tokens: Optional[torch.Tensor] = None
     presence, both subtracted.  spans int32 [rows][3]: the row's tokens are
     tokens[spans[r][0]:spans[r][2]], those from spans[r][1] on were generated.
     bias, bias_ids [n] with cu_bias int32 [rows + 1]: row r's entries are cu_bias[r] ..
-    cu_bias[r + 1] - 1; a token's are added up.  mask int32 [n_masks][words]: bit
+    cu_bias[r + 1] - 1, added in order.  mask int32 [n_masks][words]: bit
     t % 32 of word t // 32 allows token t; mask_of int32 [rows] names each row's mask, -1
     none.  A row in which nothing is left gets token -1 and lse -inf."""
     dev = _dev(logits)

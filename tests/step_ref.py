@@ -171,13 +171,11 @@ def adjust_row(x, tokens, span, penalties, ids, bias, words, dtype):
         x = torch.where(count > 0, x - less, x)
         A = A + (count > 0) * (x.abs() + (freq * count).abs() + less.abs()).double()
     if ids is not None:
-        add = torch.zeros(V, dtype=dtype)
+        x = x.clone()
         for t, b in zip(ids.tolist(), bias):
             if 0 <= t < V:
-                add[t] = add[t] + b.to(dtype)
-                A[t] += add[t].abs().double()
-        x = x + add
-        A = A + x.abs().double()
+                x[t] = x[t] + b.to(dtype)
+                A[t] += x[t].abs().double()
     if words is not None:
         t = torch.arange(V)
         ok = (words.long()[t // 32] >> (t % 32)) & 1
