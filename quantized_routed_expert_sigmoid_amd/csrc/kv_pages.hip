@@ -137,34 +137,25 @@ __device__ __forceinline__ Want want_of(const coli_kv_pages& p, const int32_t* a
     return w;
 }
 
-/* Gives sequence s its pages, the list's entries from `at` on (at + need of them
- * are there); LANES threads, this one `lane`, share the work. */
-template <int LANES>
-__device__ __forceinline__ void give(const coli_kv_pages& p, const Want& w, int s, int64_t at, const int32_t* list,
-                                     int lane, int32_t* granted, int32_t* src, int32_t* dst)
+/* The i-th page that sequence s gets. */
+__device__ __forceinline__ void give(const coli_kv_pages& p, const Want& w, int s, int i, int page)
 {
-    int32_t* row = p.page_table + (int64_t)s * p.max_pages;
     const int shared = w.last >= 0;
-    for (int b = w.have + lane; b < w.want; b += LANES) {
-        const int page = list[at + shared + b - w.have];
-        row[b] = page;
-        p.refs[page] = 1;
-    }
-    if (lane == 0) {
-        int from = -1, to = -1;
-        if (shared) {
-            from = w.old;
-            to = list[at];
-            row[w.last] = to;
-            p.refs[to] = 1;
-            atomicAdd(p.refs + from, -1);
-        }
-        src[s] = from;
-        dst[s] = to;
-        granted[s] = max(w.add, 0);
-        if (w.add > 0)
-            p.kv_len[s] = w.len + w.add;
-    }
+    p.page_table[(int64_t)s * p.max_pages + (i < shared ? w.last : w.have + i - shared)] = page;
+    p.refs[page] = 1;
+}
+
+/* The rest of a sequence that gets what it wants; to: the page for its copy, or -1. */
+__device__ __forceinline__ void settle(const coli_kv_pages& p, const Want& w, int s, int to, int32_t* granted,
+                                       int32_t* src, int32_t* dst)
+{
+    if (w.last >= 0)
+        atomicAdd(p.refs + w.old, -1);
+    src[s] = w.old;
+    dst[s] = to;
+    granted[s] = max(w.add, 0);
+    if (w.add > 0)
+        p.kv_len[s] = w.len + w.add;
 }
 
 __device__ __forceinline__ void refuse(int s, int32_t* granted, int32_t* src, int32_t* dst)
@@ -174,7 +165,8 @@ __device__ __forceinline__ void refuse(int s, int32_t* granted, int32_t* src, in
 }
 
 /* Pools and batches of up to 2^15 pages and 2^10 sequences in one launch: a thread
- * holds 32 pages and one sequence. */
+ * holds 32 pages and one sequence.  The pages given out are shared out among the threads one by
+ * one, each of which finds its sequence among the needs before it. */
 constexpr int kOneThreads = 1024, kOnePages = 32;
 
 __global__ __launch_bounds__(kOneThreads) void extend_one(coli_kv_pages p, const int32_t* add, int32_t* granted,
@@ -197,12 +189,20 @@ __global__ __launch_bounds__(kOneThreads) void extend_one(coli_kv_pages p, const
     wants[t] = w;
     befores[t] = before;
     __syncthreads();
-    for (int s = t / 64; s < p.n_seq; s += kOneThreads / 64) {
-        const Want v = wants[s];
-        if (v.need >= 0 && (v.need == 0 || befores[s] + v.need <= n_free))
-            give<64>(p, v, s, befores[s], list, t & 63, granted, src, dst);
-        else if ((t & 63) == 0)
-            refuse(s, granted, src, dst);
+    for (int i = t; i < min(needed, n_free); i += kOneThreads) {
+        int s = 0; /* the last sequence with before <= i: before + need of it is more */
+        for (int step = kOneThreads / 2; step; step /= 2)
+            if (befores[s + step] <= i)
+                s += step;
+        const Want& v = wants[s];
+        if (befores[s] + v.need <= n_free)
+            give(p, v, s, i - befores[s], list[i]);
+    }
+    if (t < p.n_seq) {
+        if (w.need >= 0 && (w.need == 0 || before + w.need <= n_free))
+            settle(p, w, t, w.last >= 0 ? list[before] : -1, granted, src, dst);
+        else
+            refuse(t, granted, src, dst);
     }
 }
 
@@ -274,10 +274,14 @@ __global__ __launch_bounds__(kThreads) void extend_give(coli_kv_pages p, const i
     }
     __syncthreads();
     const Want w = want;
-    if (w.need >= 0 && (w.need == 0 || before + w.need <= n_free))
-        give<kThreads>(p, w, s, before, ws.list, threadIdx.x, granted, src, dst);
-    else if (threadIdx.x == 0)
+    if (w.need >= 0 && (w.need == 0 || before + w.need <= n_free)) {
+        for (int i = threadIdx.x; i < w.need; i += kThreads)
+            give(p, w, s, i, ws.list[before + i]);
+        if (threadIdx.x == 0)
+            settle(p, w, s, w.last >= 0 ? ws.list[before] : -1, granted, src, dst);
+    } else if (threadIdx.x == 0) {
         refuse(s, granted, src, dst);
+    }
 }
 
 /* ---- trim, fork ----------------------------------------------------------- */
@@ -405,6 +409,7 @@ __global__ __launch_bounds__(kThreads) void compact_apply(coli_kv_pages p, const
 
 /* ---- copy ----------------------------------------------------------------- */
 
+typedef uint32_t v4u __attribute__((ext_vector_type(4)));
 constexpr int kCopyUnits = 4; /* 16-byte pieces of a thread and turn */
 
 /* blockIdx.x: keys or values and the chunk of a page, blockIdx.y: the pair. */
@@ -418,17 +423,15 @@ __global__ __launch_bounds__(kThreads) void copy_kernel(coli_kv_cache from, coli
         const int a = src[i], b = dst[i];
         if ((uint32_t)a >= (uint32_t)from.n_pages || (uint32_t)b >= (uint32_t)to.n_pages)
             continue;
-        const uint4* x = (const uint4*)(key ? from.k : from.v) + (int64_t)a * units;
-        uint4* y = (uint4*)(key ? to.k : to.v) + (int64_t)b * units;
+        const v4u* x = (const v4u*)(key ? from.k : from.v) + (int64_t)a * units;
+        v4u* y = (v4u*)(key ? to.k : to.v) + (int64_t)b * units;
         const int u0 = chunk * (kThreads * kCopyUnits) + threadIdx.x;
-        uint4 r[kCopyUnits];
-#pragma unroll
-        for (int j = 0; j < kCopyUnits; ++j)
-            r[j] = x[min(u0 + j * kThreads, units - 1)];
-#pragma unroll
-        for (int j = 0; j < kCopyUnits; ++j)
+        v4u r[kCopyUnits];
+        each<kCopyUnits>([&](auto j) { r[j] = x[min(u0 + j * kThreads, units - 1)]; });
+        each<kCopyUnits>([&](auto j) {
             if (u0 + j * kThreads < units)
                 y[u0 + j * kThreads] = r[j];
+        });
         if (chunk == 0) {
             const float* xs = (key ? from.k_scale : from.v_scale) + (int64_t)a * H;
             float* ys = (key ? to.k_scale : to.v_scale) + (int64_t)b * H;

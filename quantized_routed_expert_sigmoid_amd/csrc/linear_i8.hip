@@ -20,26 +20,10 @@
 #include "step.h"
 
 #include <algorithm>
-#include <type_traits>
-#include <utility>
 
 namespace coli {
 
 namespace {
-
-/* f(0) .. f(N - 1) with the number as a constant: large bodies that index registers
- * are not left to the unroller. */
-template <typename F, int... I>
-__device__ __forceinline__ void each_of(F f, std::integer_sequence<int, I...>)
-{
-    (f(std::integral_constant<int, I>()), ...);
-}
-
-template <int N, typename F>
-__device__ __forceinline__ void each(F f)
-{
-    each_of(f, std::make_integer_sequence<int, N>());
-}
 
 /* ---- activations ---------------------------------------------------------- */
 

@@ -14,9 +14,10 @@
  * reads all of the row's tokens and entries, from the caches.
  *
  * The logits' bytes would allow 15 us for 128 rows of 151003 bf16 with everything: it
- * takes 37.5.  Without tokens, biases and masks the pass takes 18, with tokens 29: the
+ * takes 37.  Without tokens, biases and masks the pass takes 18, with tokens 27: the
  * loads of spans, tokens and counts follow each other, and LDS (four bytes a token) leaves
- * room for eight workgroups a CU, so that there are 2.3 rounds of them.
+ * room for eight workgroups a CU, so that there are 2.3 rounds of them.  Histories of 131072 cost
+ * their comparisons, one for each token and chunk: 48 rows of 200001 fp32 48 us, of which 18 are the logits.
  */
 #include "block_device.h"
 #include "step.h"
@@ -197,8 +198,28 @@ __global__ __launch_bounds__(THREADS) void adjust_kernel(coli_logits a, Part* pa
         }
         return n;
     };
+    /* Four loads of four tokens a thread at once, none under a branch: each would be waited for by itself.  Near the
+     * list's end a thread reads its last four tokens, and counts those that are its own. */
+    constexpr int kLoads = 4, kStep = 4 * THREADS;
+    const int64_t far = a.n_tokens - 4;
+    int4 q[kLoads];
+    auto read = [&](int64_t block) {
+        if (far >= 0) {
+#pragma unroll
+            for (int j = 0; j < kLoads; ++j)
+                __builtin_memcpy(&q[j], a.tokens + min(block + kStep * j + 4 * (int)threadIdx.x, far), 16);
+        } else { /* less than four tokens in all */
+            const int n = a.n_tokens;
+            q[0] = make_int4(-1, n > 2 ? a.tokens[n - 3] : -1, n > 1 ? a.tokens[n - 2] : -1, a.tokens[n - 1]);
+#pragma unroll
+            for (int j = 1; j < kLoads; ++j)
+                q[j] = q[0];
+        }
+    };
     int listed = 0;
     if (counted || biased) {
+        if (counted)
+            read(h0);
         if (biased)
             look(b0);
         if (counted)
@@ -208,57 +229,44 @@ __global__ __launch_bounds__(THREADS) void adjust_kernel(coli_logits a, Part* pa
         if (biased)
             listed = gather();
         if (counted) {
-            auto scan = [&](int from, int to, bool generated) {
-                auto count = [&](int token) {
-                    const uint32_t at = (uint32_t)(token - c0);
-                    if (at < (uint32_t)kChunk) {
-                        if (generated)
-                            atomicAdd(counts + at, 1u);
-                        else
-                            atomicOr(counts + at, kSeen);
-                    }
-                };
-                /* four loads of four tokens at once: the tokens come from the caches, and their latency counts */
-                constexpr int N = 4, kStep = 4 * THREADS;
-                int64_t i = from + 4 * (int64_t)threadIdx.x;
-                for (; i + (N - 1) * kStep + 4 <= to; i += N * kStep) {
-                    int4 q[N];
-#pragma unroll
-                    for (int j = 0; j < N; ++j)
-                        __builtin_memcpy(&q[j], a.tokens + i + j * kStep, 16);
-#pragma unroll
-                    for (int j = 0; j < N; ++j) {
-                        count(q[j].x);
-                        count(q[j].y);
-                        count(q[j].z);
-                        count(q[j].w);
-                    }
-                }
-                /* up to three whole steps and a part */
-                int4 q[N];
-#pragma unroll
-                for (int j = 0; j < N; ++j) {
-                    const int64_t k = i + j * kStep;
-                    q[j] = make_int4(-1, -1, -1, -1);
-                    if (k + 4 <= to) {
-                        __builtin_memcpy(&q[j], a.tokens + k, 16);
-                    } else if (k < to) {
-                        q[j].x = a.tokens[k];
-                        q[j].y = k + 1 < to ? a.tokens[k + 1] : -1;
-                        q[j].z = k + 2 < to ? a.tokens[k + 2] : -1;
-                    }
-                }
-#pragma unroll
-                for (int j = 0; j < N; ++j) {
-                    count(q[j].x);
-                    count(q[j].y);
-                    count(q[j].z);
-                    count(q[j].w);
+            auto count = [&](int token, bool generated) {
+                const uint32_t at = (uint32_t)(token - c0);
+                if (at < (uint32_t)kChunk) {
+                    if (generated)
+                        atomicAdd(counts + at, 1u);
+                    else
+                        atomicOr(counts + at, kSeen);
                 }
             };
-            const int mid = min(max(made, h0), h1);
-            scan(h0, mid, false);
-            scan(mid, h1, true);
+            auto count_all = [&](bool generated) {
+#pragma unroll
+                for (int j = 0; j < kLoads; ++j) {
+                    count(q[j].x, generated);
+                    count(q[j].y, generated);
+                    count(q[j].z, generated);
+                    count(q[j].w, generated);
+                }
+            };
+            for (int64_t block = h0; block < h1; block += kStep * kLoads) {
+                if (block > h0)
+                    read(block);
+                const int64_t next = block + kStep * kLoads;
+                if (next <= h1 && block >= made) {
+                    count_all(true);
+                } else if (next <= h1 && next <= made) {
+                    count_all(false);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < kLoads; ++j) {
+                        const int64_t mine = block + kStep * j + 4 * (int)threadIdx.x, i = min(mine, far);
+                        const int e[4] = {q[j].x, q[j].y, q[j].z, q[j].w};
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            if (i + k >= mine && i + k < h1)
+                                count(e[k], i + k >= made);
+                    }
+                }
+            }
         }
         __syncthreads();
     }
@@ -416,11 +424,11 @@ __global__ __launch_bounds__(64) void join_kernel(coli_logits a, const Part* par
 constexpr int kSmall = 256, kLarge = 512;
 
 /* Every chunk of a row reads all of its tokens, so long histories want larger chunks (48 rows
- * of 200001 fp32, histories of up to 131072: 48 us with 512 threads, 63 with 256; 32 rows of 151003 with up to
- * 16000: 19.2 and 20.0), and others the smaller workgroups (128 rows of 151003 bf16, 4001: 44 and 37.5). */
+ * of 200001 fp32, histories of up to 131072: 48 us with 512 threads, 61 with 256; 32 rows of 151003 with up to
+ * 16000: equal), and others the smaller workgroups (128 rows of 151003 bf16, 4001: 42 and 37). */
 bool large_chunks(const coli_logits& a)
 {
-    return a.penalties && a.n_tokens / a.rows > 8192;
+    return a.penalties && a.n_tokens / a.rows > 16384;
 }
 
 template <typename T, int THREADS>
