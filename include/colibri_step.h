@@ -165,11 +165,12 @@ int colibri_linear_i8(const coli_qbank* W, const int8_t* xq, const float* xd, in
  *
  * logits and out: type [rows][vocab], rows logits_stride and out_stride elements apart,
  * at least vocab; out may be logits (same stride), no other overlap.  rows <=
- * COLI_MAX_SEQS, 1 <= vocab <= COLI_MAX_VOCAB.  ws as sized by
+ * COLI_MAX_SEQS, 1 <= vocab <= COLI_MAX_VOCAB, n_bias <= COLI_MAX_BIASES.  ws as sized by
  * colibri_logits_workspace_bytes for these or more rows and vocab (0: invalid sizes),
  * needed for token and lse.  rows == 0 is a no-op.
  */
 #define COLI_MAX_VOCAB (1 << 20)
+#define COLI_MAX_BIASES (1 << 30)
 
 typedef struct coli_logits {
     const void* logits;

@@ -4,7 +4,9 @@
  *   out[i][c] = (code[id][c] * scale[id][c / group]) * scale
  *
  * A thread takes eight consecutive dims, which lie under one scale: 2, 4 or 8
- * bytes of codes in, 16 or 32 bytes out.  Bound by the output's bytes.
+ * bytes of codes in, 16 or 32 bytes out.  Bound by the output's bytes: 8191 x 6144 bf16
+ * from int8 with groups of 128 24.5 us (6.2 TB/s, the reads partly from the last-level cache);
+ * one row of 6144 2 us.
  */
 #include "block_device.h"
 #include "step.h"

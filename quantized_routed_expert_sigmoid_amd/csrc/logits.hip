@@ -13,7 +13,8 @@
  * a thread only), and a second launch joins the chunks of a row.  Every chunk of a row
  * reads all of the row's tokens and entries, from the caches.
  *
- * The logits' bytes would allow 15 us for 128 rows of 151003 bf16 with everything: it
+ * Greedy choice from 128 rows of 151003 fp32 takes 17 us (4.6 TB/s), 30 with the logits
+ * written.  The logits' bytes would allow 15 us for 128 rows of 151003 bf16 with everything: it
  * takes 37.  Without tokens, biases and masks the pass takes 18, with tokens 27: the
  * loads of spans, tokens and counts follow each other, and LDS (four bytes a token) leaves
  * room for eight workgroups a CU, so that there are 2.3 rounds of them.  Histories of 131072 cost
@@ -28,17 +29,7 @@ namespace coli {
 
 namespace {
 
-constexpr int kRun = 8;   /* consecutive tokens of a thread, */
-constexpr int kRuns = 2;  /* and its runs */
-/* Tokens of a workgroup, and the entries of a bias list that it looks at at once. */
-constexpr int chunk_of(int threads)
-{
-    return threads * kRun * kRuns;
-}
-constexpr int batch_of(int threads)
-{
-    return 2 * threads;
-}
+constexpr int kRun = 8; /* consecutive tokens of a thread */
 constexpr uint32_t kSeen = 0x80000000u;          /* among the tokens; below it the count of generated ones */
 
 /* What a chunk has to say about its row: the key is the largest value in the order
@@ -125,10 +116,11 @@ struct Run {
     }
 };
 
-template <typename T, int THREADS>
+/* A thread takes RUNS runs; a bias list is looked at in batches of two entries a thread. */
+template <typename T, int THREADS, int RUNS>
 __global__ __launch_bounds__(THREADS) void adjust_kernel(coli_logits a, Part* part)
 {
-    constexpr int kWaves = THREADS / 64, kChunk = chunk_of(THREADS), kBatch = batch_of(THREADS);
+    constexpr int kWaves = THREADS / 64, kChunk = THREADS * RUNS * kRun, kBatch = 2 * THREADS;
     extern __shared__ __align__(16) uint32_t counts[]; /* [kChunk], of the row's tokens, where there are penalties */
     __shared__ unsigned long long keys[kWaves];
     __shared__ float exps[kWaves];
@@ -157,10 +149,10 @@ __global__ __launch_bounds__(THREADS) void adjust_kernel(coli_logits a, Part* pa
     const bool counted = h1 > h0 && !(rep == 1.0f && freq == 0.0f && pres == 0.0f);
     const bool biased = b1 > b0;
     /* the first logits and entries travel while the counts are cleared and the tokens counted */
-    Run<T> run[kRuns];
+    Run<T> run[RUNS];
     const int t0 = c0 + kRun * (int)threadIdx.x;
 #pragma unroll
-    for (int j = 0; j < kRuns; ++j)
+    for (int j = 0; j < RUNS; ++j)
         run[j].load(x, t0 + j * (THREADS * kRun), V);
     const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
     int id[2];
@@ -275,9 +267,9 @@ __global__ __launch_bounds__(THREADS) void adjust_kernel(coli_logits a, Part* pa
     /* this thread's largest value and its token, its first NaN's, and the sum of exp(v - top) */
     float top = -__builtin_inff(), sum = 0.0f;
     int best = -1, nan = -1;
-    float v[kRuns][kRun];
+    float v[RUNS][kRun];
 #pragma unroll
-    for (int j = 0; j < kRuns; ++j) {
+    for (int j = 0; j < RUNS; ++j) {
 #pragma unroll
         for (int i = 0; i < kRun; ++i)
             v[j][i] = run[j].value(i);
@@ -312,7 +304,7 @@ __global__ __launch_bounds__(THREADS) void adjust_kernel(coli_logits a, Part* pa
             const uint32_t at = (uint32_t)(ids[k] - t0);
             const float e = bias[k];
 #pragma unroll
-            for (int j = 0; j < kRuns; ++j) {
+            for (int j = 0; j < RUNS; ++j) {
                 const uint32_t in = at - j * (THREADS * kRun);
                 if (in < (uint32_t)kRun) {
 #pragma unroll
@@ -323,7 +315,7 @@ __global__ __launch_bounds__(THREADS) void adjust_kernel(coli_logits a, Part* pa
         }
     }
 #pragma unroll
-    for (int j = 0; j < kRuns; ++j) {
+    for (int j = 0; j < RUNS; ++j) {
         const int t = t0 + j * (THREADS * kRun);
         if (t >= end)
             continue;
@@ -421,9 +413,9 @@ __global__ __launch_bounds__(64) void join_kernel(coli_logits a, const Part* par
     }
 }
 
-constexpr int kSmall = 256, kLarge = 512;
+constexpr int kLeastChunk = 256 * 2 * kRun;
 
-/* Every chunk of a row reads all of its tokens, so long histories want larger chunks (48 rows
+/* Every chunk of a row reads all of the row's tokens, so long histories want larger chunks (48 rows
  * of 200001 fp32, histories of up to 131072: 48 us with 512 threads, 61 with 256; 32 rows of 151003 with up to
  * 16000: equal), and others the smaller workgroups (128 rows of 151003 bf16, 4001: 42 and 37). */
 bool large_chunks(const coli_logits& a)
@@ -431,13 +423,13 @@ bool large_chunks(const coli_logits& a)
     return a.penalties && a.n_tokens / a.rows > 16384;
 }
 
-template <typename T, int THREADS>
+template <typename T, int THREADS, int RUNS>
 void launch(const coli_logits& a, Part* part, hipStream_t s)
 {
-    constexpr int chunk = chunk_of(THREADS);
+    constexpr int chunk = THREADS * RUNS * kRun;
     const int chunks = (a.vocab + chunk - 1) / chunk;
-    hipLaunchKernelGGL((adjust_kernel<T, THREADS>), dim3(chunks, a.rows), dim3(THREADS), a.penalties ? chunk * 4 : 0, s, a,
-                       part);
+    hipLaunchKernelGGL((adjust_kernel<T, THREADS, RUNS>), dim3(chunks, a.rows), dim3(THREADS),
+                       a.penalties ? chunk * 4 : 0, s, a, part);
     if (part)
         hipLaunchKernelGGL(join_kernel, dim3(a.rows), dim3(64), 0, s, a, part, chunks);
 }
@@ -446,9 +438,9 @@ template <typename T>
 hipError_t launch(const coli_logits& a, Part* part, hipStream_t s)
 {
     if (large_chunks(a))
-        launch<T, kLarge>(a, part, s);
+        launch<T, 512, 2>(a, part, s);
     else
-        launch<T, kSmall>(a, part, s);
+        launch<T, 256, 2>(a, part, s);
     return hipGetLastError();
 }
 
@@ -456,7 +448,7 @@ hipError_t launch(const coli_logits& a, Part* part, hipStream_t s)
 
 size_t logits_workspace_bytes(int32_t rows, int32_t vocab)
 {
-    const size_t chunks = (vocab + chunk_of(kSmall) - 1) / chunk_of(kSmall);
+    const size_t chunks = (vocab + kLeastChunk - 1) / kLeastChunk;
     return std::max<size_t>(256, ((size_t)rows * chunks * sizeof(Part) + 255) / 256 * 256);
 }
 

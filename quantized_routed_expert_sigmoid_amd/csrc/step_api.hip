@@ -228,7 +228,8 @@ int colibri_linear_i8(const coli_qbank* W, const int8_t* xq, const float* xd, in
         return COLI_E_UNSUPPORTED;
     if (ws_bytes < linear_i8_workspace_need(S, W->rows, W->K))
         return COLI_E_WORKSPACE;
-    const LinearI8Args a = {W->data, W->row_scale, xq, xd, bias, residual, out, ws, S, W->rows, W->K, W->qtype, act, out_type};
+    const LinearI8Args a = {W->data, W->row_scale, xq,      xd,   bias,      residual, out,
+                            ws,      S,            W->rows, W->K, W->qtype, act,      out_type};
     return hip_status(launch_linear_i8(a, (hipStream_t)stream));
 }
 
@@ -247,6 +248,8 @@ int colibri_adjust_logits(const coli_logits* a, void* ws, size_t ws_bytes, coli_
         return COLI_E_UNSUPPORTED;
     if (a->n_tokens < 0 || a->n_bias < 0 || a->n_masks < 0)
         return COLI_E_INVAL;
+    if (a->n_bias > COLI_MAX_BIASES)
+        return COLI_E_UNSUPPORTED;
     if (a->rows == 0)
         return COLI_OK;
     if (!a->logits || (!a->out && !a->token && !a->lse))

@@ -27,7 +27,8 @@ def qre():
 # ---- quantisation ---------------------------------------------------------
 
 
-@pytest.mark.parametrize("rows,K", [(1, 32), (3, 96), (5, 1024), (2, 1056), (70, 2080), (3, 6144), (2, 8192), (3, 8224), (1, 32768)])
+@pytest.mark.parametrize("rows,K", [(1, 32), (3, 96), (5, 1024), (2, 1056), (70, 2080), (3, 6144), (2, 8192), (3, 8224),
+                                    (1, 32768)])
 @pytest.mark.parametrize("dtype", [F32, BF16])
 def test_quantize(qre, rows, K, dtype):
     g = gen("quantize", rows, K)
@@ -67,7 +68,8 @@ def make(qre, S, N, K, bits, *labels):
 # few tokens in every form of it; K below, at and past the steps of both forms; odd last depths
 SHAPES = [(1, 1, 32), (1, 100, 6144), (2, 16, 64), (5, 15, 96), (16, 257, 160), (17, 33, 2080), (32, 100, 128), (33, 40, 224),
           (64, 70, 320), (13, 16401, 96), (200, 50, 96), (65, 20, 128), (70, 130, 160), (100, 1, 2080), (130, 257, 192),
-          (120, 2600, 3232), (20, 30000, 96), (7, 25000, 224), (333, 4101, 224), (256, 64, 32768), (1, 9, 32768), (2000, 2101, 160), (4101, 4357, 160), (4096, 4096, 128)]
+          (120, 2600, 3232), (20, 30000, 96), (7, 25000, 224), (333, 4101, 224), (256, 64, 32768),
+          (1, 9, 32768), (2000, 2101, 160), (4101, 4357, 160), (4096, 4096, 128)]
 
 
 @pytest.mark.parametrize("S,N,K", SHAPES)

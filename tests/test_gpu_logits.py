@@ -94,7 +94,8 @@ def check(i, got, dtype):
 
 
 CASES = [(1, 1, None, None, 0, F32), (1, 5, 3, 2, 1, BF16), (4, 31, 40, None, 2, F32), (5, 4096, 300, 7, 3, F32),
-         (3, 4097, None, 600, 2, BF16), (2, 8190, 9000, 40, 0, BF16), (9, 20011, 70, 30, 4, F32), (2, 151003, 5000, 300, 2, BF16),
+         (3, 4097, None, 600, 2, BF16), (2, 8190, 9000, 40, 0, BF16), (9, 20011, 70, 30, 4, F32),
+         (2, 151003, 5000, 300, 2, BF16),
          (6, 1000, 1, 1, 0, F32), (7, 12289, 2500, None, 0, BF16), (2, 1048576, 100, 20, 1, F32)]
 
 

@@ -147,16 +147,18 @@ def logits(**kw):
 
 
 @pytest.mark.parametrize("kw,st", [
-    (dict(rows=-1), INVAL), (dict(vocab=0), INVAL), (dict(rows=65536), UNSUP), (dict(vocab=(1 << 20) + 1, logits_stride=1 << 21,
-                                                                                     out_stride=1 << 21), UNSUP),
+    (dict(rows=-1), INVAL), (dict(vocab=0), INVAL), (dict(rows=65536), UNSUP),
+    (dict(vocab=(1 << 20) + 1, logits_stride=1 << 21, out_stride=1 << 21), UNSUP),
     (dict(type=8), UNSUP), (dict(n_tokens=-1), INVAL), (dict(n_bias=-1), INVAL), (dict(n_masks=-1), INVAL),
+    (dict(n_bias=(1 << 30) + 1), UNSUP),
     (dict(logits=None), INVAL), (dict(out=None, token=None, lse=None), INVAL), (dict(spans=None), INVAL),
     (dict(tokens=None), INVAL), (dict(bias=None), INVAL), (dict(bias_ids=None), INVAL), (dict(mask_of=None), INVAL),
     (dict(mask_stride=3), INVAL), (dict(logits_stride=99), INVAL), (dict(out_stride=99, out=P + 4096), INVAL),
     (dict(out_stride=101), INVAL), (dict(logits_stride=1 << 41, out=P + 4096), UNSUP), (dict(logits=P + 2), UNSUP),
     (dict(out=P + 2), UNSUP), (dict(token=P + 2), UNSUP), (dict(lse=P + 1), UNSUP), (dict(tokens=P + 2), UNSUP),
     (dict(spans=P + 2), UNSUP), (dict(penalties=P + 2), UNSUP), (dict(bias=P + 2), UNSUP), (dict(bias_ids=P + 2), UNSUP),
-    (dict(cu_bias=P + 2), UNSUP), (dict(mask=P + 2), UNSUP), (dict(mask_of=P + 2), UNSUP), (dict(logits=P + 1, type=16), UNSUP),
+    (dict(cu_bias=P + 2), UNSUP), (dict(mask=P + 2), UNSUP), (dict(mask_of=P + 2), UNSUP),
+    (dict(logits=P + 1, type=16), UNSUP),
     (dict(rows=0, logits=None), OK)])
 def test_logits(L, kw, st):
     assert L.colibri_adjust_logits(r(logits(**kw)), P, BIG, None) == st
@@ -223,6 +225,7 @@ def test_linear_null(L):
 def test_linear_workspace_grows_with_the_batch(L, N, K, bits):
     """A workspace for S tokens serves every smaller batch: its size never falls."""
     w = bank(rows=N, K=K, qtype=bits)
-    sizes = sorted(set(range(1, 1300, 7)) | {64, 65, 128, 129, 256, 257, 2047, 2048, 2049, 4096, 8192, 16384, 32767, 32768, 65536})
+    sizes = sorted(set(range(1, 1300, 7)) | {64, 65, 128, 129, 256, 257, 2047, 2048, 2049, 4096, 8192, 16384,
+                                            32767, 32768, 65536})
     most = [L.colibri_linear_i8_workspace_bytes(r(w), S, 32) for S in sizes]
     assert all(a <= b for a, b in zip(most, most[1:])), list(zip(sizes, most))
