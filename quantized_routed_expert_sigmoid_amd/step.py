@@ -35,36 +35,39 @@ class LogitsDesc(ctypes.Structure):
                 + [(n, _i32) for n in ("type", "rows", "vocab", "n_tokens", "n_bias", "n_masks")])
 
 
-_fns = None  # (the library,)
+_ENTRIES = [
+    ("colibri_embed_q", [_vp, _vp, _i32, _i32, _f32, _vp, _i32, _vp]),
+    ("colibri_kv_extend", [_vp, _vp, _vp, _vp, _vp, _vp, ctypes.c_size_t, _vp]),
+    ("colibri_kv_trim", [_vp, _vp, _vp]),
+    ("colibri_kv_fork", [_vp, _vp, _vp, _i32, _vp]),
+    ("colibri_kv_compact", [_vp, _vp, _vp, _vp, _vp, ctypes.c_size_t, _vp]),
+    ("colibri_kv_copy", [_vp, _vp, _vp, _vp, _i32, _vp]),
+    ("colibri_quantize_i8", [_vp, _i32, _i64, _i32, _i32, _vp, _vp, _vp]),
+    ("colibri_linear_i8", [_vp, _vp, _vp, _i32, _vp, _i32, _vp, _vp, _i32, _vp, ctypes.c_size_t, _vp]),
+    ("colibri_adjust_logits", [_vp, _vp, ctypes.c_size_t, _vp]),
+]
+_SIZES = [("colibri_kv_pages_workspace_bytes", [_vp]), ("colibri_linear_i8_workspace_bytes", [_vp, _i32, _i32]),
+          ("colibri_logits_workspace_bytes", [_i32, _i32])]
+
+_ready = None  # the library whose entry points have their argument types
 
 
 def _g():
     """The library, with the argument types of these entry points set."""
-    global _fns
+    global _ready
     L = _qre._lib or _qre.lib()
-    if _fns is None or _fns[0] is not L:
-        sz, ci = ctypes.c_size_t, ctypes.c_int
-        for name, res, args in [
-                ("colibri_embed_q", ci, [_vp, _vp, _i32, _i32, _f32, _vp, _i32, _vp]),
-                ("colibri_kv_pages_workspace_bytes", sz, [_vp]),
-                ("colibri_kv_extend", ci, [_vp, _vp, _vp, _vp, _vp, _vp, sz, _vp]),
-                ("colibri_kv_trim", ci, [_vp, _vp, _vp]),
-                ("colibri_kv_fork", ci, [_vp, _vp, _vp, _i32, _vp]),
-                ("colibri_kv_compact", ci, [_vp, _vp, _vp, _vp, _vp, sz, _vp]),
-                ("colibri_kv_copy", ci, [_vp, _vp, _vp, _vp, _i32, _vp]),
-                ("colibri_quantize_i8", ci, [_vp, _i32, _i64, _i32, _i32, _vp, _vp, _vp]),
-                ("colibri_linear_i8_workspace_bytes", sz, [_vp, _i32, _i32]),
-                ("colibri_linear_i8", ci, [_vp, _vp, _vp, _i32, _vp, _i32, _vp, _vp, _i32, _vp, sz, _vp]),
-                ("colibri_logits_workspace_bytes", sz, [_i32, _i32]),
-                ("colibri_adjust_logits", ci, [_vp, _vp, sz, _vp])]:
-            fn = getattr(L, name)
-            fn.restype, fn.argtypes = res, args
-        _fns = (L,)
+    if _ready is not L:
+        for res, entries in ((ctypes.c_int, _ENTRIES), (ctypes.c_size_t, _SIZES)):
+            for name, args in entries:
+                fn = getattr(L, name)
+                fn.restype, fn.argtypes = res, args
+        _ready = L
     return L
 
 
 def _do(dev: torch.device, name: str, *args):
-    _g()
+    if _qre._lib is None or _ready is not _qre._lib:
+        _g()
     _call(dev, name, *args)
 
 
@@ -334,46 +337,60 @@ def adjust_logits(logits: torch.Tensor, *, tokens: Optional[torch.Tensor] = None
     if logits.dim() != 2:
         raise ValueError("logits: [rows][vocab] expected")
     rows, V = logits.shape
-    t = _type(logits.dtype)
-    _on(dev, tokens, spans, penalties, bias, bias_ids, cu_bias, mask, mask_of, out, ws)
+    dtype = logits.dtype
+    t = _type(dtype)
     ls = os = _row_stride(logits, (rows, V), "logits")
-    if (penalties is None) != (spans is None) or (penalties is None) != (tokens is None):
-        raise ValueError("tokens, spans and penalties: all or none expected")
-    if (bias is None) != (bias_ids is None) or (bias is None) != (cu_bias is None):
-        raise ValueError("bias, bias_ids and cu_bias: all or none expected")
-    if (mask is None) != (mask_of is None):
-        raise ValueError("mask and mask_of: both or none expected")
-    if penalties is not None:
+    a = LogitsDesc()
+    a.logits, a.logits_stride, a.type, a.rows, a.vocab = logits.data_ptr(), ls, t, rows, V
+    if penalties is not None and spans is not None and tokens is not None:
+        _on(dev, tokens, spans, penalties)
         _flat(tokens, torch.int32, (tokens.numel(),), "tokens")
         _flat(spans, torch.int32, (rows, 3), "spans")
         _flat(penalties, torch.float32, (rows, 3), "penalties")
-    if bias is not None:
-        _flat(bias_ids, torch.int32, (bias_ids.numel(),), "bias_ids")
-        _flat(bias, torch.float32, (bias_ids.numel(),), "bias")
+        a.tokens, a.spans, a.penalties = tokens.data_ptr(), spans.data_ptr(), penalties.data_ptr()
+        a.n_tokens = tokens.numel()
+    elif not (penalties is spans is tokens):
+        raise ValueError("tokens, spans and penalties: all or none expected")
+    if bias is not None and bias_ids is not None and cu_bias is not None:
+        _on(dev, bias, bias_ids, cu_bias)
+        n = bias_ids.numel()
+        _flat(bias_ids, torch.int32, (n,), "bias_ids")
+        _flat(bias, torch.float32, (n,), "bias")
         _flat(cu_bias, torch.int32, (rows + 1,), "cu_bias")
-    ms = 0
-    if mask is not None:
+        a.bias, a.bias_ids, a.cu_bias, a.n_bias = bias.data_ptr(), bias_ids.data_ptr(), cu_bias.data_ptr(), n
+    elif not (bias is bias_ids is cu_bias):
+        raise ValueError("bias, bias_ids and cu_bias: all or none expected")
+    if mask is not None and mask_of is not None:
+        _on(dev, mask, mask_of)
         if mask.dtype != torch.int32:
             raise TypeError(f"mask: {torch.int32} expected, got {mask.dtype}")
         if mask.dim() != 2 or mask.shape[1] < (V + 31) // 32:
             raise ValueError(f"mask: [n_masks][{(V + 31) // 32}] expected, got {tuple(mask.shape)}")
-        ms = _row_stride(mask, tuple(mask.shape), "mask")
         _flat(mask_of, torch.int32, (rows,), "mask_of")
+        a.mask, a.mask_of, a.n_masks = mask.data_ptr(), mask_of.data_ptr(), mask.shape[0]
+        a.mask_stride = _row_stride(mask, mask.shape, "mask")
+    elif mask is not mask_of:
+        raise ValueError("mask and mask_of: both or none expected")
     if out is not None:
         if not write:
             raise ValueError("out: nothing is written without `write`")
-        if out.dtype != logits.dtype:
-            raise TypeError(f"out: {logits.dtype} expected, got {out.dtype}")
+        if out.dtype != dtype:
+            raise TypeError(f"out: {dtype} expected, got {out.dtype}")
+        _on(dev, out)
         os = _row_stride(out, (rows, V), "out")
     elif write:
-        out, os = torch.empty(rows, V, dtype=logits.dtype, device=dev), V
-    token = torch.empty(rows, dtype=torch.int32, device=dev) if best else None
-    lse = torch.empty(rows, dtype=torch.float32, device=dev) if best else None
-    if best and ws is None:
-        ws = logits_workspace(rows, V, dev)
-    a = LogitsDesc(logits.data_ptr(), _at(out), _at(token), _at(lse), _at(tokens), _at(spans), _at(penalties), _at(bias),
-                   _at(bias_ids), _at(cu_bias), _at(mask), _at(mask_of), ls, os, ms, t, rows, V,
-                   0 if tokens is None else tokens.numel(), 0 if bias is None else bias.numel(),
-                   0 if mask is None else mask.shape[0])
-    _do(dev, "colibri_adjust_logits", ctypes.byref(a), *(_room(ws) if ws is not None else (None, 0)))
+        out, os = torch.empty(rows, V, dtype=dtype, device=dev), V
+    a.out, a.out_stride = _at(out), os
+    token = lse = None
+    room = None, 0
+    if best:
+        token = torch.empty(rows, dtype=torch.int32, device=dev)
+        lse = torch.empty(rows, dtype=torch.float32, device=dev)
+        a.token, a.lse = token.data_ptr(), lse.data_ptr()
+        if ws is None:
+            ws = logits_workspace(rows, V, dev)
+        else:
+            _on(dev, ws)
+        room = _room(ws)
+    _do(dev, "colibri_adjust_logits", ctypes.byref(a), *room)
     return LogitsResult(out, token, lse)
