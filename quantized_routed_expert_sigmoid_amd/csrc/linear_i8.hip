@@ -9,9 +9,9 @@
  * nothing is folded on the way and neither splits of a row nor their order change a
  * bit of the result.  Two forms:
  *
- * - i8_rows, few tokens: the weights go from memory straight to the matrix cores'
- *   registers, and the activations again and again from the caches;
- * - i8_tiles, more tokens or a very large bank: tiles of both in LDS.
+ * - i8_rows, few tokens or a small bank: the weights go from memory straight to the
+ *   matrix cores' registers, and the activations again and again from the caches;
+ * - i8_tiles, the rest: tiles of both in LDS.
  *
  * Codes of fewer bits are unpacked to the top of their bytes, 2^(8 - bits) times
  * their value, which the row's scale takes out again.
@@ -436,46 +436,54 @@ int64_t tiles_of(int32_t S, int32_t N, int rows, int toks)
     return (int64_t)((N + rows - 1) / rows) * ((S + toks - 1) / toks);
 }
 
-/* Up to 16 tokens i8_rows needs no join and has more in flight, until there are tiles for
- * most CUs without splits (13 tokens, 10240 x 6144 int4 13.8 us against 14.8, int8 equal;
- * 4 tokens, 4096 x 4096 int4 4.3 against 9; but 13 tokens, 131071 x 6144 int8 178 against
- * 138).  Rows of an int2 bank with K = 32 are shorter than one load of a tile. */
-bool use_rows(int32_t S, int32_t N, int32_t K)
-{
-    return K < 64 || (S <= 16 && N < 192 * 128);
-}
-
 /* Tiles of a launch: rows x tokens, how many run at a time, and what a stage of 128 k takes one such
- * round, in ns (measured with K = 6144 int8; ns_few where only half of the places are taken).  A split of the
- * stages costs a join: its launch, and the sums written and read. */
+ * round, in ns (measured with K = 6144 int8; ns_few where only half of the places are taken). */
 struct Shape {
     int rows, toks, places, ns, ns_few;
-    bool splits;
+    int most; /* tokens; 0: any number, and no splits */
 };
 
 constexpr Shape kShapes[] = {
-    {320, 256, 256, 2500, 2500, false}, /* two rounds of 4096 x 10240: 235 us; 265 with 256 x 256, 280 with 128 x 128 */
-    {256, 256, 256, 1750, 1750, false}, /* 8192 x 8192 x 8192 467 us, 546 with 320 x 256 */
-    {128, 128, 256, 740, 740, true},    /* 1024 x 4096 x 4096 24.4 us; 26.8 with 128 x 64, 69 with 256 x 256 */
-    {128, 64, 512, 800, 580, true},     /* 64 x 10240 x 6144 18.8 us in three splits, about 28 in one */
-    {128, 32, 512, 720, 400, true},     /* up to 32 tokens: 32 x 10240 x 6144 17.3 us, 18.8 with 128 x 64 */
+    {320, 256, 256, 2500, 2500, 0}, /* two rounds of 4096 x 10240: 235 us; 265 with 256 x 256, 280 with 128 x 128 */
+    {256, 256, 256, 1750, 1750, 0}, /* 8192 x 8192 x 8192 467 us, 546 with 320 x 256 */
+    {128, 128, 256, 740, 740, COLI_MAX_TOKENS}, /* 1024 x 4096 x 4096 24.4 us; 26.8 with 128 x 64, 69 with 256 x 256 */
+    {128, 64, 512, 800, 580, COLI_MAX_TOKENS},  /* 64 x 10240 x 6144 int8 19.6 us in three splits, about 28 in one */
+    {128, 32, 512, 720, 520, 128},              /* 64 x 4096 x 4096 10.7 us in four splits; 128 x 64 11.3 */
 };
-constexpr int kFew = 4, kMostSplits = 8, kJoinNs = 3000, kJoinBytesNs = 4000;
+constexpr int kRowsShape = 5;
+
+/* A split of the stages costs a join: its launch, and the sums written and read. */
+constexpr int kMostSplits = 8, kJoinNs = 4000, kJoinBytesNs = 3500;
+
+/* i8_rows in the same measure: it needs no join, but reads the weights again for every 16 tokens
+ * (32 x 2048 x 4096 int8 6.4 us against 8.5 with tiles, 64 x 10240 x 6144 55 against 19.6); fewer than 16
+ * tokens share the lines of their activations (1 x 10240 x 6144 int8 14.0, tiles 17.2; 13: 18.1 and 17.4). */
+int64_t rows_ns(int32_t S, int32_t N, int32_t K, int32_t bits)
+{
+    const int64_t groups16 = S < 16 ? 11 + 5 * S / 16 : (S + 15) / 16 * 16;
+    return (int64_t)N * K / (bits == 8 ? 4700 : 5800) * groups16 / 16;
+}
 
 struct I8Plan {
     int shape, n_tiles, t_tiles, stages, splits;
     size_t total;
 };
 
-I8Plan plan_of(int32_t S, int32_t N, int32_t K)
+I8Plan plan_of(int32_t S, int32_t N, int32_t K, int32_t bits)
 {
     I8Plan p = {};
+    p.shape = kRowsShape;
+    p.total = 256;
+    if (K < 64) /* an int2 row of 32 codes is shorter than one load of a tile */
+        return p;
     p.stages = (K + 127) / 128;
-    int64_t least = INT64_MAX;
-    for (int i = S <= 32 ? kFew : 0; i < (S <= 32 ? kFew + 1 : kFew); ++i) {
+    int64_t least = rows_ns(S, N, K, bits);
+    for (int i = 0; i < kRowsShape; ++i) {
         const Shape& sh = kShapes[i];
+        if (sh.most && S > sh.most)
+            continue;
         const int64_t tiles = tiles_of(S, N, sh.rows, sh.toks);
-        for (int k = 1; k <= (sh.splits ? kMostSplits : 1); ++k) {
+        for (int k = 1; k <= (sh.most ? kMostSplits : 1); ++k) {
             const int64_t wgs = tiles * k, part = (p.stages + k - 1) / k;
             if (k > 1 && (wgs > sh.places || part < 4))
                 break;
@@ -488,10 +496,13 @@ I8Plan plan_of(int32_t S, int32_t N, int32_t K)
             }
         }
     }
+    if (p.shape == kRowsShape)
+        return p;
     const Shape& sh = kShapes[p.shape];
     p.n_tiles = (N + sh.rows - 1) / sh.rows;
     p.t_tiles = (S + sh.toks - 1) / sh.toks;
-    p.total = p.splits > 1 ? (size_t)p.splits * p.n_tiles * p.t_tiles * sh.rows * sh.toks * 4 : 256;
+    if (p.splits > 1)
+        p.total = (size_t)p.splits * p.n_tiles * p.t_tiles * sh.rows * sh.toks * 4;
     return p;
 }
 
@@ -525,15 +536,14 @@ hipError_t launch_tiles(const LinearI8Args& a, const I8Plan& p, hipStream_t s)
 template <int BITS, typename TO>
 hipError_t launch(const LinearI8Args& a, hipStream_t s)
 {
-    if (use_rows(a.S, a.N, a.K))
-        return launch_rows<BITS, TO>(a, s);
-    const I8Plan p = plan_of(a.S, a.N, a.K);
+    const I8Plan p = plan_of(a.S, a.N, a.K, BITS);
     switch (p.shape) {
     case 0: return launch_tiles<BITS, 5, 2, 2, 4, 4, 2, 1, TO>(a, p, s);
     case 1: return launch_tiles<BITS, 4, 2, 2, 4, 4, 2, 1, TO>(a, p, s);
     case 2: return launch_tiles<BITS, 1, 2, 4, 2, 4, 3, 1, TO>(a, p, s);
     case 3: return launch_tiles<BITS, 1, 2, 4, 1, 4, 3, 2, TO>(a, p, s);
-    default: return launch_tiles<BITS, 1, 1, 4, 1, 4, 3, 2, TO>(a, p, s);
+    case 4: return launch_tiles<BITS, 1, 1, 4, 1, 4, 3, 2, TO>(a, p, s);
+    default: return launch_rows<BITS, TO>(a, s);
     }
 }
 
@@ -563,22 +573,20 @@ hipError_t launch_quantize_i8(const void* x, int32_t type, int64_t stride, int32
                             : launch_quantize((const bf16*)x, stride, rows, K, q, d, s);
 }
 
-size_t linear_i8_workspace_need(int32_t S, int32_t N, int32_t K)
+size_t linear_i8_workspace_need(int32_t S, int32_t N, int32_t K, int32_t bits)
 {
-    return use_rows(S, N, K) ? 256 : plan_of(S, N, K).total;
+    return plan_of(S, N, K, bits).total;
 }
 
-/* The largest need of 1 .. S tokens: fewer tokens can be more splits.  The plan changes
- * with every 64 tokens (and at 32), and what is split has at most 256 tiles of 128 x 64, or half as many of
- * 128 x 128. */
-size_t linear_i8_workspace_bytes(int32_t S, int32_t N, int32_t K)
+/* The largest need of 1 .. S tokens: fewer tokens can be more splits.  Tiles change
+ * with every 32 tokens, and what is split has at most 256 of 128 x 64 (half as many of
+ * 128 x 128; those of 128 x 32 end at 128 tokens). */
+size_t linear_i8_workspace_bytes(int32_t S, int32_t N, int32_t K, int32_t bits)
 {
-    size_t most = linear_i8_workspace_need(S, N, K);
-    if (K < 64)
-        return most;
-    const int ends = std::min((S + 63) / 64, 256 / (int)std::min<int64_t>(256, tiles_of(1, N, 128, 1)) + 1);
-    for (int t = 0; t <= ends; ++t)
-        most = std::max(most, linear_i8_workspace_need(std::min(S, t ? 64 * t : 32), N, K));
+    size_t most = linear_i8_workspace_need(S, N, K, bits);
+    const int few = std::max(4, 2 * (256 / (int)std::min<int64_t>(256, tiles_of(1, N, 128, 1)) + 1));
+    for (int t = 1; t <= std::min((S + 31) / 32, few); ++t)
+        most = std::max(most, linear_i8_workspace_need(std::min(S, 32 * t), N, K, bits));
     return most;
 }
 

@@ -46,8 +46,8 @@ struct LinearI8Args {
 };
 
 /* What one call of S tokens needs; the most that one of 1 .. S tokens does. */
-size_t linear_i8_workspace_need(int32_t S, int32_t N, int32_t K);
-size_t linear_i8_workspace_bytes(int32_t S, int32_t N, int32_t K);
+size_t linear_i8_workspace_need(int32_t S, int32_t N, int32_t K, int32_t bits);
+size_t linear_i8_workspace_bytes(int32_t S, int32_t N, int32_t K, int32_t bits);
 hipError_t launch_linear_i8(const LinearI8Args& a, hipStream_t s);
 
 size_t logits_workspace_bytes(int32_t rows, int32_t vocab);

@@ -207,7 +207,7 @@ int colibri_quantize_i8(const void* x, int32_t type, int64_t x_stride, int32_t r
 
 size_t colibri_linear_i8_workspace_bytes(const coli_qbank* W, int32_t S, int32_t out_type)
 {
-    return check_linear_i8(W, S, out_type) ? 0 : linear_i8_workspace_bytes(S, W->rows, W->K);
+    return check_linear_i8(W, S, out_type) ? 0 : linear_i8_workspace_bytes(S, W->rows, W->K, W->qtype);
 }
 
 int colibri_linear_i8(const coli_qbank* W, const int8_t* xq, const float* xd, int32_t S, const float* bias,
@@ -226,7 +226,7 @@ int colibri_linear_i8(const coli_qbank* W, const int8_t* xq, const float* xd, in
     if (!aligned(xq, 16) || !aligned(xd, 4) || !aligned(bias, 4) || !aligned(residual, 4) || !aligned(out, 4) ||
         !aligned(ws, kAlign))
         return COLI_E_UNSUPPORTED;
-    if (ws_bytes < linear_i8_workspace_need(S, W->rows, W->K))
+    if (ws_bytes < linear_i8_workspace_need(S, W->rows, W->K, W->qtype))
         return COLI_E_WORKSPACE;
     const LinearI8Args a = {W->data, W->row_scale, xq,      xd,   bias,      residual, out,
                             ws,      S,            W->rows, W->K, W->qtype, act,      out_type};

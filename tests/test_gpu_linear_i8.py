@@ -65,11 +65,12 @@ def make(qre, S, N, K, bits, *labels):
     return g, data, scale, xq, xd, qre.QBank(data.unsqueeze(0).cuda(), scale.unsqueeze(0).cuda(), bits)
 
 
-# few tokens in every form of it; K below, at and past the steps of both forms; odd last depths
+# every form and tile, with and without splits; K below, at and past the steps of both forms; odd last depths
 SHAPES = [(1, 1, 32), (1, 100, 6144), (2, 16, 64), (5, 15, 96), (16, 257, 160), (17, 33, 2080), (32, 100, 128), (33, 40, 224),
           (64, 70, 320), (13, 16401, 96), (200, 50, 96), (65, 20, 128), (70, 130, 160), (100, 1, 2080), (130, 257, 192),
           (120, 2600, 3232), (20, 30000, 96), (7, 25000, 224), (333, 4101, 224), (256, 64, 32768),
-          (1, 9, 32768), (2000, 2101, 160), (4101, 4357, 160), (4096, 4096, 128)]
+          (90, 4099, 2080), (33, 9001, 1184), (300, 1100, 6176), (64, 6001, 4128), (20, 9001, 3104), (129, 5003, 1120),
+          (128, 10111, 6176), (1, 9, 32768), (2000, 2101, 160), (4101, 4357, 160), (4096, 4096, 128)]
 
 
 @pytest.mark.parametrize("S,N,K", SHAPES)
