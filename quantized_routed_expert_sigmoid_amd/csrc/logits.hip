@@ -29,8 +29,8 @@ namespace coli {
 
 namespace {
 
-constexpr int kRun = 8; /* consecutive tokens of a thread */
-constexpr uint32_t kSeen = 0x80000000u;          /* among the tokens; below it the count of generated ones */
+constexpr int kRun = 8;                 /* consecutive tokens of a thread */
+constexpr uint32_t kSeen = 0x80000000u; /* among the tokens; below it the count of generated ones */
 
 /* What a chunk has to say about its row: the key is the largest value in the order
  * of unsigned numbers, then the lowest token (key_of). */

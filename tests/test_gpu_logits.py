@@ -113,8 +113,16 @@ def test_adjust(qre, rows, V, hist, n_bias, masks, dtype):
 
 @pytest.mark.parametrize("hist", [60000, 200000])
 def test_long_histories(qre, hist):
-    i = make(3, 9001, hist, 5, 0, F32, "long")
+    i = make(3, 9001, hist, 2500, 0, F32, "long")
     i["spans"][0] = ints([0, 0, hist])
+    check(i, call(qre, i), F32)
+
+
+@pytest.mark.parametrize("n", range(6))
+def test_few_tokens_in_all(qre, n):
+    i = make(3, 40, 4, None, 0, F32, "few")
+    i["tokens"] = ints([7, 7, 3, 39, 0][:n])
+    i["spans"] = ints([[0, 1, n], [0, 0, n], [1, n, n]])
     check(i, call(qre, i), F32)
 
 
