@@ -125,6 +125,12 @@ int colibri_quantize_i8(const void* x, int32_t type, int64_t x_stride, int32_t r
                         coli_stream_t stream);
 
 /*
+ * colibri_add_rms_norm with q and d by the rule of colibri_quantize_i8, on the unrounded
+ * y: q int8 [rows][K], d fp32 [rows].  All else as there.
+ */
+int colibri_add_rms_norm_i8(const coli_norm* n, coli_stream_t stream);
+
+/*
  * colibri_linear_q for activations with one scale per token, for W a bank of one
  * matrix [rows][K] with one scale per row (group 0), int8, int4 or int2:
  *   out[t][r] = act(scale(r) * xd[t] * sum_k code(r, k) * xq[t][k] + bias[r]) + residual[t][r]

@@ -152,6 +152,11 @@ def add_rms_norm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6, *,
     (which may be residual or x itself, to update the stream in place).  y is
     returned in y_dtype if that is given (the layer takes fp32), the Q8_0 codes
     and scales (what linear_q takes) unless q8 is False."""
+    return _norm(x, weight, eps, residual, sum_out, y_dtype, q8, False, "colibri_add_rms_norm")
+
+
+def _norm(x, weight, eps, residual, sum_out, y_dtype, codes: bool, per_row: bool, entry: str) -> NormResult:
+    """`entry`, whose codes, if asked for, have one scale per row or one per 32."""
     dev = _dev(x)
     if not (x.dim() == 2):
         raise ValueError("x: [rows][K] expected")
@@ -178,12 +183,12 @@ def add_rms_norm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6, *,
         _flat(sum_out, residual.dtype if residual is not None else sum_out.dtype, (rows, K), "sum_out")
     y = None if y_dtype is None else torch.empty(rows, K, dtype=y_dtype, device=dev)
     q = d = None
-    if q8:
+    if codes:
         q = torch.empty(rows, K, dtype=torch.int8, device=dev)
-        d = torch.empty(rows, K // 32, dtype=torch.float32, device=dev)
+        d = torch.empty((rows,) if per_row else (rows, K // 32), dtype=torch.float32, device=dev)
     n = NormDesc(x.data_ptr(), _at(residual), weight.data_ptr(), _at(sum_out), _at(y), _at(q), _at(d),
                  x.stride(0) if rows > 1 else K, rs, rows, K, xt, rt, xt if y is None else _type(y_dtype), eps)
-    _call(dev, "colibri_add_rms_norm", ctypes.byref(n))
+    _call(dev, entry, ctypes.byref(n))
     return NormResult(sum_out, y, q, d)
 
 

@@ -16,7 +16,9 @@
 
 namespace coli {
 
-hipError_t launch_add_rms_norm(const coli_norm& n, hipStream_t s);
+/* COLI_OK where the norm can be launched, or its rows are none.  per_row: q and d with one scale per row. */
+int check_add_rms_norm(const coli_norm* n);
+hipError_t launch_add_rms_norm(const coli_norm& n, bool per_row, hipStream_t s);
 
 struct LinearArgs {
     const void* w;

@@ -86,9 +86,9 @@ int check_attn_sizes(const coli_kv_cache* c, const coli_kv_batch* b, const coli_
 
 } // namespace
 
-extern "C" {
+namespace coli {
 
-int colibri_add_rms_norm(const coli_norm* n, coli_stream_t stream)
+int check_add_rms_norm(const coli_norm* n)
 {
     if (!n || n->rows < 0 || n->K < 32 || n->K % 32 || !(n->eps >= 0.0f) || !isfinite(n->eps))
         return COLI_E_INVAL;
@@ -104,7 +104,17 @@ int colibri_add_rms_norm(const coli_norm* n, coli_stream_t stream)
         return COLI_E_UNSUPPORTED;
     if (!good_stride(n->x_stride, n->K, 4) || (n->residual && !good_stride(n->residual_stride, n->K, 4)))
         return COLI_E_INVAL;
-    return hip_status(launch_add_rms_norm(*n, (hipStream_t)stream));
+    return COLI_OK;
+}
+
+} // namespace coli
+
+extern "C" {
+
+int colibri_add_rms_norm(const coli_norm* n, coli_stream_t stream)
+{
+    const int st = check_add_rms_norm(n);
+    return st || n->rows == 0 ? st : hip_status(launch_add_rms_norm(*n, false, (hipStream_t)stream));
 }
 
 size_t colibri_linear_workspace_bytes(const coli_qbank* W, int32_t S, int32_t out_type)

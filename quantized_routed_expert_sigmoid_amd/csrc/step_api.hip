@@ -3,6 +3,7 @@
  * include/colibri_step.h): argument validation on the host, then one launcher.
  * Nothing here synchronises or allocates.
  */
+#include "block.h"
 #include "layer.h"
 #include "step.h"
 
@@ -187,6 +188,12 @@ int colibri_kv_copy(const coli_kv_cache* from, const coli_kv_cache* to, const in
     if (!aligned(src, 4) || !aligned(dst, 4))
         return COLI_E_UNSUPPORTED;
     return hip_status(launch_kv_copy(*from, *to, src, dst, n, (hipStream_t)stream));
+}
+
+int colibri_add_rms_norm_i8(const coli_norm* n, coli_stream_t stream)
+{
+    const int st = check_add_rms_norm(n);
+    return st || n->rows == 0 ? st : hip_status(launch_add_rms_norm(*n, true, (hipStream_t)stream));
 }
 
 int colibri_quantize_i8(const void* x, int32_t type, int64_t x_stride, int32_t rows, int32_t K, int8_t* q, float* d,

@@ -16,7 +16,8 @@ import torch
 
 import quantized_routed_expert_sigmoid_amd as _qre
 
-from .block import _ACTS, KVCache, _at, _call, _dev, _f32, _flat, _i32, _i64, _length, _on, _room, _type, _vp
+from .block import (_ACTS, KVCache, NormResult, _at, _call, _dev, _f32, _flat, _i32, _i64, _length, _norm, _on,
+                    _room, _type, _vp)
 
 _IDS = {torch.int32: 4, torch.int64: 8}
 
@@ -42,6 +43,7 @@ _ENTRIES = [
     ("colibri_kv_fork", [_vp, _vp, _vp, _i32, _vp]),
     ("colibri_kv_compact", [_vp, _vp, _vp, _vp, _vp, ctypes.c_size_t, _vp]),
     ("colibri_kv_copy", [_vp, _vp, _vp, _vp, _i32, _vp]),
+    ("colibri_add_rms_norm_i8", [_vp, _vp]),
     ("colibri_quantize_i8", [_vp, _i32, _i64, _i32, _i32, _vp, _vp, _vp]),
     ("colibri_linear_i8", [_vp, _vp, _vp, _i32, _vp, _i32, _vp, _vp, _i32, _vp, ctypes.c_size_t, _vp]),
     ("colibri_adjust_logits", [_vp, _vp, ctypes.c_size_t, _vp]),
@@ -242,6 +244,16 @@ def quantize_i8(x: torch.Tensor):
     d = torch.empty(rows, dtype=torch.float32, device=dev)
     _do(dev, "colibri_quantize_i8", x.data_ptr(), t, stride, rows, K, q.data_ptr(), d.data_ptr())
     return q, d
+
+
+def add_rms_norm_i8(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6, *,
+                    residual: Optional[torch.Tensor] = None, sum_out: Optional[torch.Tensor] = None,
+                    y_dtype: Optional[torch.dtype] = None) -> NormResult:
+    """add_rms_norm whose codes have one scale per row, q int8 [rows][K] and d fp32 [rows]: what linear_i8 takes,
+    equal to quantize_i8 of the unrounded y."""
+    if _qre._lib is None or _ready is not _qre._lib:
+        _g()
+    return _norm(x, weight, eps, residual, sum_out, y_dtype, True, True, "colibri_add_rms_norm_i8")
 
 
 def linear_i8_workspace(bank, S: int, dtype: torch.dtype = torch.float32) -> torch.Tensor:

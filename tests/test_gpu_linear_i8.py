@@ -6,7 +6,7 @@ import torch
 
 from tests import step_ref as ref
 from tests.gpu_common import say
-from tests.test_gpu_block import gen, within
+from tests.test_gpu_block import NORM, gen, within
 from tests.test_gpu_step import codes
 
 pytestmark = pytest.mark.gpu
@@ -52,6 +52,29 @@ def test_quantize_of_halves(qre):
     x[:, 0], x[0, 1:5], x[1, 1:5] = 127.0, torch.tensor([0.5, -0.5, 2.5, -2.5]), torch.tensor([0.49, -0.49, 126.5, -126.5])
     q, d = qre.quantize_i8(x.cuda())
     assert d.tolist() == [1.0, 1.0] and q[:, :5].tolist() == [[127, 1, -1, 3, -3], [127, 0, 0, 127, -127]]
+
+
+@pytest.mark.parametrize("rows,K,xt,rt,yt", NORM)
+def test_norm_with_one_scale_per_row(qre, rows, K, xt, rt, yt):
+    """The sum and y of add_rms_norm, and the codes that quantize_i8 gives the unrounded y."""
+    g = gen("norm i8", rows, K)
+    x = torch.randn(rows, K, generator=g).mul(3).to(xt).cuda()
+    r = None if rt is None else torch.randn(rows, K, generator=g).to(rt).cuda()
+    w = (1 + 0.3 * torch.randn(K, generator=g)).cuda()
+    if rows > 2:
+        x[1] = 0  # a row of zeros, where there is no residual
+        x[2, 0] = 1e4  # one value far above the rest
+    want = qre.add_rms_norm(x, w, 1e-5, residual=r, y_dtype=F32, q8=False)
+    q, d = qre.quantize_i8(want.y)
+    got = qre.add_rms_norm_i8(x, w, 1e-5, residual=r, y_dtype=yt)
+    assert torch.equal(got.q, q) and torch.equal(got.d, d) and got.d.shape == (rows,)
+    assert torch.equal(got.y, want.y.to(yt)) and (r is None or torch.equal(got.sum, want.sum))
+    only = qre.add_rms_norm_i8(x, w, 1e-5, residual=r)
+    assert only.y is None and torch.equal(only.q, q) and torch.equal(only.d, d)
+    if r is not None:
+        stream = r.clone()
+        assert qre.add_rms_norm_i8(x, w, 1e-5, residual=stream, sum_out=stream).sum is stream
+        assert torch.equal(stream, want.sum)
 
 
 # ---- product --------------------------------------------------------------

@@ -59,6 +59,15 @@ def test_linear(qre):
         qre.quantize_i8(torch.ones(2, 65, device="cuda")[:, 1:])
 
 
+def test_norm(qre):
+    x, w = torch.ones(3, 64, device="cuda"), torch.ones(64, device="cuda")
+    for a, kw, error in [((x.t(), w), {}, ValueError), ((x, w[:32]), {}, ValueError), ((x, w.cpu()), {}, ValueError),
+                         ((x.half(), w), {}, TypeError), ((x, w), dict(residual=x[:2]), ValueError),
+                         ((x, w), dict(eps=float("inf")), qre.ColibriError), ((x, w), dict(y_dtype=torch.float16), TypeError)]:
+        with pytest.raises(error):
+            qre.add_rms_norm_i8(*a, **kw)
+
+
 def test_logits(qre):
     x = torch.zeros(2, 40, device="cuda")
     good = dict(tokens=ints([1]), spans=ints([[0, 0, 1]] * 2), penalties=torch.ones(2, 3, device="cuda"),

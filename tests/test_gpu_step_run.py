@@ -48,14 +48,14 @@ class Model:
         """Hidden states, logits and the best tokens of the rows' last places; the cache has room for them."""
         q, p = self.qre, self.pages
         h = q.embed_q(self.bank["embed"], ids, math.sqrt(K))
-        n = q.add_rms_norm(h, self.norm.cuda(), 1e-5, y_dtype=F32, q8=False)
-        qkv = self.linear("qkv", n.y).view(ids.numel(), -1, D)
+        n = q.add_rms_norm_i8(h, self.norm.cuda(), 1e-5)
+        qkv = q.linear_i8(self.bank["qkv"], n.q, n.d).view(ids.numel(), -1, D)
         a, k, v = qkv.split([HQ, H, H], 1)
         q.kv_append(self.cache, p.page_table, cu, p.kv_len, k, v)
         a = q.kv_attention(self.cache, p.page_table, cu, p.kv_len, a)
         s = self.linear("o", a.view(ids.numel(), -1), residual=h)
-        n = q.add_rms_norm(s, self.norm.cuda(), 1e-5, y_dtype=F32, q8=False)
-        logits = self.linear("head", n.y)
+        n = q.add_rms_norm_i8(s, self.norm.cuda(), 1e-5)
+        logits = q.linear_i8(self.bank["head"], n.q, n.d)
         return h, qkv, a, s, logits, q.adjust_logits(logits, tokens=tokens, spans=spans, penalties=penalties, mask=mask,
                                                      mask_of=mask_of)
 

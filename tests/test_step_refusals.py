@@ -191,6 +191,18 @@ def test_quantize(L, a, st):
     assert L.colibri_quantize_i8(*a, None) == st
 
 
+@pytest.mark.parametrize("kw,st", [
+    (dict(rows=-1), INVAL), (dict(K=48), INVAL), (dict(K=8224, x_stride=8224), UNSUP), (dict(x=None), INVAL),
+    (dict(q=None), INVAL), (dict(d=None), INVAL), (dict(sum=None, y=None, q=None, d=None), INVAL), (dict(x_type=8), UNSUP),
+    (dict(eps=float("nan")), INVAL), (dict(x=P + 8), UNSUP), (dict(q=P + 2), UNSUP), (dict(x_stride=60), INVAL),
+    (dict(residual_stride=63), INVAL), (dict(rows=0, x=None), OK)])
+def test_norm(L, kw, st):
+    d = dict(x=P, residual=P, weight=P, sum=P, y=P, q=P, d=P, x_stride=64, residual_stride=64, rows=2, K=64, x_type=32,
+             residual_type=32, y_type=32, eps=1e-6)
+    assert L.colibri_add_rms_norm_i8(r(block.NormDesc(**d | kw)), None) == st
+    assert L.colibri_add_rms_norm_i8(None, None) == INVAL
+
+
 @pytest.mark.parametrize("kw,st", BANK_BAD + [(dict(group=32), UNSUP), (dict(group=48), INVAL)])
 def test_linear_bank(L, kw, st):
     w = bank(**kw)
